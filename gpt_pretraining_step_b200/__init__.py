@@ -32,7 +32,11 @@ ABI_FUNCTIONS = [
     "gpt_op_newton_schulz_noalloc", "gpt_get_adam_step", "gpt_set_adam_step", "gpt_set_wait_limit",
     "gpt_op_check", "gpt_op_set_wait_limit", "gpt_op_embedding_bwd_scratch", "gpt_op_embedding_bwd",
     "adamw_step_shard", "gpt_tensor_region", "gpt_grad_bucket", "gpt_set_grad_events",
+    "gpt_op_attention_plan_bytes", "gpt_op_attention_plan", "gpt_op_attention_packed_scratch",
+    "gpt_op_attention_packed_fwd", "gpt_op_attention_packed_bwd", "gpt_op_policy_loss_scratch",
+    "gpt_op_policy_loss", "gpt_op_preference_loss_scratch", "gpt_op_preference_loss",
 ]
+DTYPE_BF16, DTYPE_FP32 = 0, 1
 GRAD_BUCKETS = 6
 
 
@@ -57,6 +61,11 @@ class HParams(ctypes.Structure):
                 ("adam_eps", ctypes.c_float), ("adam_wd", ctypes.c_float)]
 
 
+class Heads(ctypes.Structure):
+    """gpt_heads: a [tokens, heads, 128] bf16 tensor by pointer and strides."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
 _LIB = None
 
 
@@ -68,6 +77,7 @@ def lib():
             raise RuntimeError(f"{LIB_PATH} is missing: run `python -m gpt_pretraining_step_b200.build`")
         L = ctypes.CDLL(LIB_PATH)
         vp, i32, f32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+        hp, i64 = ctypes.POINTER(Heads), ctypes.c_longlong
         sig = {
             "gpt_workspace_size": (i32, [ctypes.POINTER(Config), ctypes.POINTER(sz), ctypes.POINTER(sz),
                                          ctypes.POINTER(sz)]),
@@ -115,6 +125,18 @@ def lib():
             "gpt_op_newton_schulz_scratch": (sz, [i32, i32, i32]),
             "gpt_op_newton_schulz": (i32, [vp, vp, i32, i32, i32, i32, vp, vp]),
             "gpt_op_newton_schulz_noalloc": (i32, [vp, vp, i32, i32, i32, i32, vp]),
+            "gpt_op_attention_plan_bytes": (sz, [i32]),
+            "gpt_op_attention_plan": (i32, [vp, i32, i32, i32, vp, vp]),
+            "gpt_op_attention_packed_scratch": (sz, [i32, i32, i32]),
+            "gpt_op_attention_packed_fwd": (i32, [hp, hp, hp, hp, vp, i32, i32, i32, f32, vp, vp, vp]),
+            "gpt_op_attention_packed_bwd": (i32, [hp, hp, hp, hp, vp, hp, hp, hp, hp, i32, i32, i32, f32, vp, vp,
+                                                  vp]),
+            "gpt_op_policy_loss_scratch": (sz, [i32]),
+            "gpt_op_policy_loss": (i32, [vp, i32, i64, vp, vp, vp, vp, vp, i32, i32, f32, f32, f32, vp, vp, vp, i64,
+                                         vp, vp]),
+            "gpt_op_preference_loss_scratch": (sz, [i32, i32]),
+            "gpt_op_preference_loss": (i32, [vp, i32, i64, vp, vp, i32, vp, i32, i32, f32, f32, vp, vp, vp, vp, vp,
+                                             i64, vp, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -442,6 +464,195 @@ def attention_bwd(q, k, v, o, lse, dout, window=-1, stream=None):
     _check(lib().gpt_op_attention_bwd_ex(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(D),
                                          _ptr(dq), _ptr(dk), _ptr(dv), B, H, Hkv, T, int(window), _stream(stream)))
     return dq, dk, dv
+
+
+# ------------------------------------------------ fine-tuning on packed sequences
+
+def _given(name, t, dtype, shape, device, contiguous=True):
+    """A tensor argument's check; a wrong one would be read out of range."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or (contiguous
+                                                                                    and not t.is_contiguous()):
+        raise GptError(GPT_EINVAL, f"{name} must be a {'contiguous ' if contiguous else ''}{dtype} tensor "
+                                   f"{tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _current_device(t, name):
+    """The device of t, which has to be the current one (its streams run the call)."""
+    import torch
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise GptError(GPT_EINVAL, f"{name} is on {t.device}, not on the current CUDA device")
+    return t.device
+
+
+def _on_stream(tensors, stream):
+    """Tensors made here are used on `stream`: their memory must not be given
+    out again on the current stream before that work has run."""
+    import torch
+    if stream is not None and stream.cuda_stream != torch.cuda.current_stream().cuda_stream:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _heads(name, t, n, device, heads=None):
+    import torch
+    if t.dim() != 3 or t.shape[2] != 128 or t.stride(2) != 1 or (heads and t.shape[1] != heads):
+        raise GptError(GPT_EINVAL, f"{name} must be [{n}, {heads or 'heads'}, 128] with contiguous dims, "
+                                   f"got {tuple(t.shape)}")
+    _given(name, t, torch.bfloat16, (n, t.shape[1], 128), device, contiguous=False)
+    return ctypes.byref(Heads(t.data_ptr(), t.stride(0), t.stride(1)))
+
+
+class AttentionPlan:
+    """Masks and work order of one batch of packed sequences (gpt_op_attention_plan)."""
+
+    def __init__(self, cu_seqlens, n_tokens, window=-1, stream=None):
+        import torch
+        dev = _current_device(cu_seqlens, "cu_seqlens")
+        self.n_tokens, self.window = int(n_tokens), int(window)
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+            raise GptError(GPT_EINVAL, "cu_seqlens must be [sequences + 1]")
+        _given("cu_seqlens", cu_seqlens, torch.int32, cu_seqlens.shape, dev)
+        self.buf = torch.empty(max(lib().gpt_op_attention_plan_bytes(self.n_tokens), 256), dtype=torch.uint8,
+                               device=dev)
+        _on_stream([self.buf], stream)
+        self.update(cu_seqlens, stream)
+
+    def update(self, cu_seqlens, stream=None):
+        """Plan another batch of the same n_tokens and window into the same buffer."""
+        import torch
+        _given("cu_seqlens", cu_seqlens, torch.int32, (cu_seqlens.numel(),), self.buf.device)
+        _check(lib().gpt_op_attention_plan(_ptr(cu_seqlens), cu_seqlens.numel() - 1, self.n_tokens, self.window,
+                                           _ptr(self.buf), _stream(stream)))
+
+
+def attention_plan(cu_seqlens, n_tokens, window=-1, stream=None):
+    """Plan of the sequences cu_seqlens (int32 [n + 1], on the device) packed
+    into n_tokens positions, for attention_packed_fwd and _bwd."""
+    return AttentionPlan(cu_seqlens, n_tokens, window, stream)
+
+
+def attention_packed_fwd(q, k, v, plan, scale=0.0, o=None, lse=None, stream=None):
+    """Causal attention of each sequence of the plan.  q [n_tokens, H, 128], k
+    and v [n_tokens, Hkv, 128] bf16 with any token and head strides (multiples
+    of 8); scale 0 is 1 / sqrt(128).  Returns o [n_tokens, H, 128] and lse
+    [H, n_tokens], new unless given; rows past the last sequence keep what
+    they held (new tensors: anything)."""
+    import torch
+    n, dev = plan.n_tokens, _current_device(q, "q")
+    H, Hkv = q.shape[1], k.shape[1]
+    if o is None:
+        o = torch.empty((n, H, 128), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((H, n), dtype=torch.float32, device=dev)
+    scratch = torch.empty(max(lib().gpt_op_attention_packed_scratch(n, H, 0), 256), dtype=torch.uint8, device=dev)
+    _on_stream([o, lse, scratch], stream)
+    _check(lib().gpt_op_attention_packed_fwd(
+        _heads("q", q, n, dev), _heads("k", k, n, dev), _heads("v", v, n, dev, Hkv), _heads("o", o, n, dev, H),
+        _ptr(_given("lse", lse, torch.float32, (H, n), dev)), n, H, Hkv, scale, _ptr(plan.buf), _ptr(scratch),
+        _stream(stream)))
+    return o, lse
+
+
+def attention_packed_bwd(q, k, v, o, lse, dout, plan, scale=0.0, dq=None, dk=None, dv=None, stream=None):
+    """Gradients (bf16, shaped as q, k and v; new unless given) of
+    attention_packed_fwd, from its o and lse and the gradient dout of o."""
+    import torch
+    n, dev = plan.n_tokens, _current_device(q, "q")
+    H, Hkv = q.shape[1], k.shape[1]
+    dq, dk, dv = (torch.empty((n, h, 128), dtype=torch.bfloat16, device=dev) if t is None else t
+                  for t, h in ((dq, H), (dk, Hkv), (dv, Hkv)))
+    scratch = torch.empty(max(lib().gpt_op_attention_packed_scratch(n, H, 1), 256), dtype=torch.uint8, device=dev)
+    _on_stream([dq, dk, dv, scratch], stream)
+    _check(lib().gpt_op_attention_packed_bwd(
+        _heads("q", q, n, dev), _heads("k", k, n, dev), _heads("v", v, n, dev, Hkv), _heads("o", o, n, dev, H),
+        _ptr(_given("lse", lse, torch.float32, (H, n), dev)), _heads("dout", dout, n, dev, H),
+        _heads("dq", dq, n, dev, H), _heads("dk", dk, n, dev, Hkv), _heads("dv", dv, n, dev, Hkv), n, H, Hkv, scale,
+        _ptr(plan.buf), _ptr(scratch), _stream(stream)))
+    return dq, dk, dv
+
+
+def _optional_ptr(t):
+    return None if t is None else _ptr(t)
+
+
+def _loss_args(logits, targets, grad, dlogits):
+    """Checked (M, V, dtype code, row stride, gradient or None) of both losses."""
+    import torch
+    dev = _current_device(logits, "logits")
+    if logits.dim() != 2 or logits.dtype not in (torch.bfloat16, torch.float32) or (logits.shape[1] > 1
+                                                                                    and logits.stride(1) != 1):
+        raise GptError(GPT_EINVAL, "logits must be a [M, V] bf16 or fp32 tensor with contiguous rows")
+    M, V = logits.shape
+    ld = logits.stride(0) if M > 1 else max(logits.stride(0), V)
+    _given("targets", targets, torch.int32, (M,), dev)
+    ld_d = ld
+    if not grad:
+        dlogits = None
+    elif dlogits is None:
+        # the rows' alignment follows the logits'
+        dlogits = torch.empty_strided((M, V), (ld, 1), dtype=logits.dtype, device=dev)
+    else:
+        _given("dlogits", dlogits, logits.dtype, (M, V), dev, contiguous=False)
+        if V > 1 and dlogits.stride(1) != 1:
+            raise GptError(GPT_EINVAL, "dlogits must have contiguous rows")
+        ld_d = dlogits.stride(0) if M > 1 else max(dlogits.stride(0), V)
+    return M, V, DTYPE_FP32 if logits.dtype == torch.float32 else DTYPE_BF16, ld, dlogits, ld_d, dev
+
+
+def policy_loss(logits, targets, old_logp, advantage, weight, ref_logp=None, kl_coef=0.0, clip_low=0.2,
+                clip_high=0.2, grad=True, dlogits=None, stream=None):
+    """Clipped policy loss with a KL term and its gradient (gpt_op_policy_loss).
+
+    logits [M, V] bf16 or fp32, targets int32 [M] (-1: not counted); old_logp
+    (None: the present ones), advantage, weight and ref_logp (None: no KL
+    term) fp32 [M].  Returns (stats [4], logp [M], dlogits): stats are the
+    loss and the weighted sums of the clipped surrogate, of the KL estimate
+    and of the clipped positions; dlogits (None with grad=False) is new unless
+    given, and may be logits itself."""
+    import torch
+    M, V, code, ld, dlogits, ld_d, dev = _loss_args(logits, targets, grad, dlogits)
+    for name, t in (("old_logp", old_logp), ("advantage", advantage), ("weight", weight), ("ref_logp", ref_logp)):
+        if t is not None:
+            _given(name, t, torch.float32, (M,), dev)
+    stats = torch.empty(4, dtype=torch.float32, device=dev)
+    logp = torch.empty(M, dtype=torch.float32, device=dev)
+    scratch = torch.empty(max(lib().gpt_op_policy_loss_scratch(M), 256), dtype=torch.uint8, device=dev)
+    _on_stream([stats, logp, scratch] + ([dlogits] if grad else []), stream)
+    _check(lib().gpt_op_policy_loss(
+        _ptr(logits), code, ld, _ptr(targets), _optional_ptr(old_logp), _optional_ptr(ref_logp), _ptr(advantage),
+        _ptr(weight), M, V, clip_low, clip_high, kl_coef, _ptr(stats), _ptr(logp), _optional_ptr(dlogits), ld_d,
+        _ptr(scratch), _stream(stream)))
+    return stats, logp, dlogits
+
+
+def preference_loss(logits, targets, cu_seqlens, ref_logp=None, beta=0.1, label_smoothing=0.0, grad=True,
+                    dlogits=None, stream=None):
+    """Preference loss over pairs of packed answers and its gradient
+    (gpt_op_preference_loss): sequences 2 i (chosen) and 2 i + 1 (rejected) of
+    cu_seqlens int32 [2 pairs + 1].  logits, targets, grad and dlogits as for
+    policy_loss; ref_logp fp32 [2 pairs], the reference model's seq_logp.
+    Returns (loss [], margin [pairs], seq_logp [2 pairs], logp [M], dlogits);
+    rows past the last sequence keep what they held (new tensors: anything)."""
+    import torch
+    M, V, code, ld, dlogits, ld_d, dev = _loss_args(logits, targets, grad, dlogits)
+    n = cu_seqlens.numel() - 1
+    if n < 2 or n % 2:
+        raise GptError(GPT_EINVAL, "cu_seqlens must be [2 * pairs + 1]")
+    _given("cu_seqlens", cu_seqlens, torch.int32, (n + 1,), dev)
+    if ref_logp is not None:
+        _given("ref_logp", ref_logp, torch.float32, (n,), dev)
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    margin = torch.empty(n // 2, dtype=torch.float32, device=dev)
+    seq_logp = torch.empty(n, dtype=torch.float32, device=dev)
+    logp = torch.empty(M, dtype=torch.float32, device=dev)
+    scratch = torch.empty(max(lib().gpt_op_preference_loss_scratch(M, n // 2), 256), dtype=torch.uint8, device=dev)
+    _on_stream([loss, margin, seq_logp, logp, scratch] + ([dlogits] if grad else []), stream)
+    _check(lib().gpt_op_preference_loss(
+        _ptr(logits), code, ld, _ptr(targets), _ptr(cu_seqlens), n // 2, _optional_ptr(ref_logp), M, V, beta,
+        label_smoothing, _ptr(loss), _ptr(margin), _ptr(seq_logp), _ptr(logp), _optional_ptr(dlogits), ld_d,
+        _ptr(scratch), _stream(stream)))
+    return loss, margin, seq_logp, logp, dlogits
 
 
 def rmsnorm_fwd(x, stream=None):

@@ -15,6 +15,7 @@
 #include "common.cuh"
 #include "gemm.h"
 #include "kernels.cuh"
+#include "losses.cuh"
 #include "polar_express_table.h"
 
 using namespace gpt;
@@ -1636,6 +1637,7 @@ int gpt_op_check(void* stream) {
   if (flag) GPT_CK(cudaMemset(word, 0, sizeof(int)));
   if (flag & ERRF_TIMEOUT) return fail(GPT_ETIMEOUT, "a bounded device wait of an op-level call expired");
   if (flag & ERRF_TOKEN_RANGE) return fail(GPT_ERANGE, "token or target id outside [0, vocab)");
+  if (flag & ERRF_SEQUENCE) return fail(GPT_ERANGE, "sequence offsets out of order or past the buffers");
   if (flag) return fail(GPT_ECUDA, "op-level device error flag set");
   return GPT_OK;
 }
@@ -1750,6 +1752,156 @@ int gpt_op_attention_bwd(const void* q, const void* k, const void* v, const void
                          const float* lse, float* Dscratch, float* dq, void* dk, void* dv, int B, int H, int T,
                          void* stream) {
   return gpt_op_attention_bwd_ex(q, k, v, o, dout, lse, Dscratch, dq, dk, dv, B, H, H, T, -1, stream);
+}
+
+// ------------------------------------------------ fine-tuning on packed sequences
+
+static bool aligned_scratch(const void* p) { return (reinterpret_cast<uintptr_t>(p) & (kAlign - 1)) == 0; }
+
+// The kernels' view of a [tokens, heads, 128] tensor; GPT_EINVAL if its base
+// or strides do not suit 16-byte accesses, or an output's rows overlap.
+static int heads_arg(const gpt_heads* t, const char* name, long long tokens, long long heads, bool output,
+                     PackedTensor* out) {
+  if (!t || !t->data) return fail(GPT_EINVAL, std::string("null pointer: ") + name);
+  const long long tok = tokens > 1 ? t->token_stride : 128, head = heads > 1 ? t->head_stride : 128;
+  if (reinterpret_cast<uintptr_t>(t->data) & 15) return fail(GPT_EINVAL, std::string(name) + " must be 16-byte aligned");
+  if (tok < 8 || head < 8 || tok % 8 || head % 8 || tok >= (1ll << 38) || head >= (1ll << 38))
+    return fail(GPT_EINVAL, std::string(name) + ": strides must be positive multiples of 8 elements");
+  const bool token_major = tokens < 2 || tok >= (heads - 1) * head + 128;
+  const bool head_major = heads < 2 || head >= (tokens - 1) * tok + 128;
+  const bool apart = (tokens < 2 || tok >= 128) && (heads < 2 || head >= 128);
+  if (output && !(apart && (token_major || head_major)))
+    return fail(GPT_EINVAL, std::string(name) + ": an output's rows overlap");
+  *out = PackedTensor{t->data, tok, head};
+  return GPT_OK;
+}
+
+static int packed_shape(int n_tokens, int H, int Hkv, float scale, const void* plan, const void* scratch) {
+  if (n_tokens < 0 || H < 1) return fail(GPT_EINVAL, "bad attention shape");
+  if (Hkv < 1 || H % Hkv) return fail(GPT_EINVAL, "kv heads must divide the query heads");
+  if (static_cast<long long>(n_tokens) * H > (1ll << 31) - 1) return fail(GPT_EINVAL, "attention too large");
+  if (!(scale >= 0.f) || std::isinf(scale)) return fail(GPT_EINVAL, "scale must be positive (0: 1 / sqrt(128))");
+  if (!plan || !scratch) return fail(GPT_EINVAL, "null pointer");
+  if (!aligned_scratch(plan) || !aligned_scratch(scratch))
+    return fail(GPT_EINVAL, "plan and scratch must be 256-byte aligned");
+  return GPT_OK;
+}
+
+size_t gpt_op_attention_plan_bytes(int n_tokens) { return n_tokens < 0 ? 0 : attention_plan_bytes(1, n_tokens); }
+
+int gpt_op_attention_plan(const int32_t* cu_seqlens, int n_seq, int n_tokens, int window, void* plan, void* stream) {
+  if (!cu_seqlens || !plan) return fail(GPT_EINVAL, "null pointer");
+  if (n_seq < 0 || n_tokens < 0 || n_tokens > (1 << 30)) return fail(GPT_EINVAL, "bad plan shape");
+  if (!aligned_scratch(plan)) return fail(GPT_EINVAL, "plan must be 256-byte aligned");
+  int* err = nullptr;
+  int rc = op_err(&err);
+  if (rc) return rc;
+  launch_attention_plan(cu_seqlens, n_seq, 1, n_tokens, window, false, plan, err, static_cast<cudaStream_t>(stream));
+  GPT_CK(cudaGetLastError());
+  return GPT_OK;
+}
+
+size_t gpt_op_attention_packed_scratch(int n_tokens, int H, int backward) {
+  return n_tokens < 0 || H < 1 ? 0 : attention_packed_scratch(n_tokens, H, backward != 0);
+}
+
+int gpt_op_attention_packed_fwd(const gpt_heads* q, const gpt_heads* k, const gpt_heads* v, const gpt_heads* o,
+                                float* lse, int n_tokens, int H, int Hkv, float scale, const void* plan,
+                                void* scratch, void* stream) {
+  int rc = packed_shape(n_tokens, H, Hkv, scale, plan, scratch);
+  if (rc || n_tokens == 0) return rc;
+  if (!lse) return fail(GPT_EINVAL, "null pointer: lse");
+  PackedTensor tq, tk, tv, to;
+  if ((rc = heads_arg(q, "q", n_tokens, H, false, &tq)) || (rc = heads_arg(k, "k", n_tokens, Hkv, false, &tk)) ||
+      (rc = heads_arg(v, "v", n_tokens, Hkv, false, &tv)) || (rc = heads_arg(o, "o", n_tokens, H, true, &to)))
+    return rc;
+  int* err = nullptr;
+  if ((rc = op_err(&err))) return rc;
+  GPT_CK(launch_attn_packed_fwd(tq, tk, tv, to, lse, H, Hkv, n_tokens, scale > 0.f ? scale : 1.f / sqrtf(128.f), plan,
+                                scratch, static_cast<cudaStream_t>(stream), err, g_op_wait_cycles.load()));
+  return GPT_OK;
+}
+
+int gpt_op_attention_packed_bwd(const gpt_heads* q, const gpt_heads* k, const gpt_heads* v, const gpt_heads* o,
+                                const float* lse, const gpt_heads* dout, const gpt_heads* dq, const gpt_heads* dk,
+                                const gpt_heads* dv, int n_tokens, int H, int Hkv, float scale, const void* plan,
+                                void* scratch, void* stream) {
+  int rc = packed_shape(n_tokens, H, Hkv, scale, plan, scratch);
+  if (rc || n_tokens == 0) return rc;
+  if (!lse) return fail(GPT_EINVAL, "null pointer: lse");
+  PackedTensor tq, tk, tv, to, tdo, tdq, tdk, tdv;
+  if ((rc = heads_arg(q, "q", n_tokens, H, false, &tq)) || (rc = heads_arg(k, "k", n_tokens, Hkv, false, &tk)) ||
+      (rc = heads_arg(v, "v", n_tokens, Hkv, false, &tv)) || (rc = heads_arg(o, "o", n_tokens, H, false, &to)) ||
+      (rc = heads_arg(dout, "dout", n_tokens, H, false, &tdo)) ||
+      (rc = heads_arg(dq, "dq", n_tokens, H, true, &tdq)) || (rc = heads_arg(dk, "dk", n_tokens, Hkv, true, &tdk)) ||
+      (rc = heads_arg(dv, "dv", n_tokens, Hkv, true, &tdv)))
+    return rc;
+  int* err = nullptr;
+  if ((rc = op_err(&err))) return rc;
+  GPT_CK(launch_attn_packed_bwd(tq, tk, tv, to, tdo, lse, tdq, tdk, tdv, H, Hkv, n_tokens,
+                                scale > 0.f ? scale : 1.f / sqrtf(128.f), plan, scratch,
+                                static_cast<cudaStream_t>(stream), err, g_op_wait_cycles.load()));
+  return GPT_OK;
+}
+
+// Rows of logits and gradient common to both losses.
+static int loss_rows(const void* logits, int dtype, long long ld, const int32_t* targets, int M, int V, void* dlogits,
+                     long long ld_d, const void* scratch, LossRows* r) {
+  if (M < 0 || V < 1 || V > (1 << 24)) return fail(GPT_EINVAL, "bad logits shape (M >= 0, V in [1, 2^24])");
+  if (dtype != GPT_DTYPE_BF16 && dtype != GPT_DTYPE_FP32)
+    return fail(GPT_EINVAL, "logits must be GPT_DTYPE_BF16 or GPT_DTYPE_FP32");
+  if (!scratch || (M > 0 && (!logits || !targets))) return fail(GPT_EINVAL, "null pointer");
+  if (ld < V || (dlogits && ld_d < V)) return fail(GPT_EINVAL, "row strides must be at least V");
+  const uintptr_t es = dtype == GPT_DTYPE_FP32 ? 4 : 2;
+  if ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(dlogits)) & (es - 1))
+    return fail(GPT_EINVAL, "logits and dlogits must be aligned to their type");
+  if (dlogits == logits && dlogits && ld_d != ld) return fail(GPT_EINVAL, "in place, ld_d must be ld");
+  if (!aligned_scratch(scratch)) return fail(GPT_EINVAL, "scratch must be 256-byte aligned");
+  *r = LossRows{logits, dlogits, ld, ld_d, targets, M, V, dtype == GPT_DTYPE_FP32};
+  return GPT_OK;
+}
+
+size_t gpt_op_policy_loss_scratch(int M) { return M < 0 ? 0 : policy_loss_scratch(M); }
+
+int gpt_op_policy_loss(const void* logits, int dtype, long long ld, const int32_t* targets, const float* old_logp,
+                       const float* ref_logp, const float* advantage, const float* weight, int M, int V,
+                       float clip_low, float clip_high, float kl_coef, float* stats, float* logp, void* dlogits,
+                       long long ld_d, void* scratch, void* stream) {
+  LossRows r;
+  int rc = loss_rows(logits, dtype, ld, targets, M, V, dlogits, ld_d, scratch, &r);
+  if (rc) return rc;
+  if (!stats || (M > 0 && (!advantage || !weight || !logp))) return fail(GPT_EINVAL, "null pointer");
+  if (!(clip_low >= 0.f && clip_low <= 1.f) || !(clip_high >= 0.f) || std::isinf(clip_high))
+    return fail(GPT_EINVAL, "clip_low must be in [0, 1] and clip_high finite and not negative");
+  if (!std::isfinite(kl_coef) || (!ref_logp && kl_coef != 0.f))
+    return fail(GPT_EINVAL, "kl_coef must be finite, and 0 without ref_logp");
+  PolicyArgs a{old_logp, ref_logp, advantage, weight, clip_low, clip_high, kl_coef, stats, logp};
+  int* err = nullptr;
+  if ((rc = op_err(&err))) return rc;
+  GPT_CK(launch_policy_loss(r, a, scratch, err, static_cast<cudaStream_t>(stream)));
+  return GPT_OK;
+}
+
+size_t gpt_op_preference_loss_scratch(int M, int n_pairs) {
+  return M < 0 || n_pairs < 1 ? 0 : preference_loss_scratch(M, n_pairs);
+}
+
+int gpt_op_preference_loss(const void* logits, int dtype, long long ld, const int32_t* targets,
+                           const int32_t* cu_seqlens, int n_pairs, const float* ref_logp, int M, int V, float beta,
+                           float label_smoothing, float* loss, float* margin, float* seq_logp, float* logp,
+                           void* dlogits, long long ld_d, void* scratch, void* stream) {
+  LossRows r;
+  int rc = loss_rows(logits, dtype, ld, targets, M, V, dlogits, ld_d, scratch, &r);
+  if (rc) return rc;
+  if (n_pairs < 1 || n_pairs > (1 << 29)) return fail(GPT_EINVAL, "n_pairs must be positive");
+  if (!cu_seqlens || !loss || !margin || !seq_logp || (M > 0 && !logp)) return fail(GPT_EINVAL, "null pointer");
+  if (!std::isfinite(beta) || !(label_smoothing >= 0.f && label_smoothing <= 1.f))
+    return fail(GPT_EINVAL, "beta must be finite and label_smoothing in [0, 1]");
+  PreferenceArgs a{cu_seqlens, n_pairs, ref_logp, beta, label_smoothing, loss, margin, seq_logp, logp};
+  int* err = nullptr;
+  if ((rc = op_err(&err))) return rc;
+  GPT_CK(launch_preference_loss(r, a, scratch, err, static_cast<cudaStream_t>(stream)));
+  return GPT_OK;
 }
 
 int gpt_op_rmsnorm_fwd(const float* x, void* y, float* rstd, int M, int d, void* stream) {

@@ -26,6 +26,40 @@ namespace {
 
 constexpr int HD = 128;
 
+// ------------------------------------------------------- packed sequences
+//
+// The second build of both kernels (kPacked): every row of T positions holds
+// sequences of different lengths end to end, and query t sees the keys
+// lo[t] .. t, lo[t] = max(start of t's sequence, t - window).  lo does not
+// decrease with t, so a tile of 128 queries sees the key blocks from that of
+// lo[first query] to its own: tiles and key blocks stay on the 128-position
+// grid whatever the sequence boundaries (a tile may hold many short
+// sequences, or parts of two long ones), blocks outside are never visited,
+// and the softmax masks by lo per row.  The other way round the queries that
+// see key t are t .. hi[t], hi[t] = min(end of the sequence - 1, t + window).
+// The plan (attention_plan_kernel, once per batch) holds lo, hi and the work
+// items sorted by their number of blocks, longest first, which a counter
+// hands out.  Positions past the last sequence are neither read nor written:
+// attention_setup_kernel copies the tensor maps to device memory with their
+// token extent cut to the sequences' end, so TMA fills those rows with zeros
+// (their memory may hold NaN, which a zero probability would not remove).
+struct PackedArgs {
+  const int* lo;            // [B * T], row-local
+  const int* hi;            // [B * T], row-local; -1 past the last sequence
+  const int* order;         // work entries: forward b * npairs + pair, backward b * nblocks + key block
+  const int* ctl;           // kCtl* words
+  const CUtensorMap* maps;  // q, k, v (and dO) with the extent patched in
+  long long o_tok, o_head;    // forward: strides of o in elements; backward: of dk
+  long long dv_tok, dv_head;  // backward: strides of dv
+};
+enum { kCtlSched = 0, kCtlEntries = 1, kCtlValid = 2, kCtlWords = 8 };
+
+// makes a tensor map that a kernel wrote to device memory usable by this
+// thread's TMA instructions
+__device__ __forceinline__ void tensormap_acquire(const CUtensorMap* m) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(m) : "memory");
+}
+
 // ------------------------------------------------- forward on tcgen05 / TMEM
 //
 // Persistent: one CTA per SM takes work items, a pair of 128-query tiles
@@ -102,6 +136,7 @@ __device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)
 // (causal end), per tile counts nkvA, nkvB (0: tile B past the sequence).
 struct FwdItem {
   int bh, bkv, qtA, j0, nkvA, nkvB, nkv;
+  int oB;   // tile B's first key block, counted from j0 (0 unless packed)
   bool hasB;
 };
 
@@ -120,6 +155,24 @@ __device__ __forceinline__ FwdItem fwd_item(int n, int nq, int H, int Hkv, int k
   it.nkvA = it.qtA + 1 - it.j0;
   it.nkvB = it.hasB ? it.qtA + 2 - it.j0 : 0;
   it.nkv = it.hasB ? it.nkvB : it.nkvA;
+  it.oB = 0;
+  return it;
+}
+
+// A packed item as the TMA thread published it: batch row, head, first query
+// tile, first key block of tile A and of tile B (-1: no tile B).
+__device__ __forceinline__ FwdItem fwd_item_packed(const volatile int* f, int H, int Hkv, int kvs) {
+  FwdItem it;
+  const int b = f[0], h = f[1];
+  it.bh = b * H + h;
+  it.bkv = b * kvs + h / (H / Hkv);
+  it.qtA = f[2];
+  it.j0 = f[3];
+  it.hasB = f[4] >= 0;
+  it.oB = it.hasB ? f[4] - it.j0 : 0;
+  it.nkvA = it.qtA + 1 - it.j0;
+  it.nkvB = it.hasB ? it.qtA + 2 - it.j0 : 0;
+  it.nkv = it.hasB ? it.nkvB : it.nkvA;
   return it;
 }
 
@@ -135,12 +188,12 @@ __device__ __forceinline__ void causal_mask_row(uint32_t (&sr)[128], int lane) {
   for (int k = 32 * (Q + 1); k < 128; ++k) sr[k] = __float_as_uint(-INFINITY);
 }
 
-template <bool kFine>
+template <bool kFine, bool kPacked>
 __global__ void __launch_bounds__(384, 1)
     attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, bf16* __restrict__ o, float* __restrict__ lse,
                        int H, int Hkv, int kvs, int T, int wl, float scale_log2, int n_items, int* sched,
-                       int* err, long long wait_cycles) {
+                       int* err, long long wait_cycles, const PackedArgs pk) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // the 128-byte-swizzled tiles need a 1024-byte-aligned base, which the
   // dynamic shared memory window provides; refuse to run otherwise
@@ -166,10 +219,16 @@ __global__ void __launch_bounds__(384, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 17);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* item_ring = reinterpret_cast<volatile int*>(tmem_holder + 2);   // [4]
+  volatile int* item_info = item_ring + 4;   // [4][6], packed items: fwd_item_packed's fields
 
   const int warp = warp_id(), lane = lane_id();
   const int nq = (T + 127) / 128;
   const long long wlim = wait_limit_or_default(wait_cycles);
+  const int Tv = kPacked ? pk.ctl[kCtlValid] : T;   // positions of a row that hold sequences
+  auto item_of = [&](int n, int idx) -> FwdItem {
+    if constexpr (kPacked) return fwd_item_packed(item_info + 6 * (n & 3), H, Hkv, kvs);
+    else return fwd_item(idx, nq, H, Hkv, kvs, wl);
+  };
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -182,9 +241,11 @@ __global__ void __launch_bounds__(384, 1)
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
-    tma_prefetch_desc(&tq);
-    tma_prefetch_desc(&tk);
-    tma_prefetch_desc(&tv);
+    if constexpr (!kPacked) {
+      tma_prefetch_desc(&tq);
+      tma_prefetch_desc(&tk);
+      tma_prefetch_desc(&tv);
+    }
   }
   if (warp == 1) {
     tmem_alloc(tmem_holder, 512);
@@ -199,35 +260,70 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 0) {
     if (lane == 0) {
       // -------------------------------------------------------------- TMA
+      const CUtensorMap* mq = kPacked ? pk.maps : &tq;
+      const CUtensorMap* mk = kPacked ? pk.maps + 1 : &tk;
+      const CUtensorMap* mv = kPacked ? pk.maps + 2 : &tv;
+      int entries = 0;
+      if constexpr (kPacked) {
+        tensormap_acquire(mq);
+        tensormap_acquire(mk);
+        tensormap_acquire(mv);
+        entries = pk.ctl[kCtlEntries];
+        n_items = entries * H;
+      }
+      // Packed: item number and fields are fetched one item ahead, so that the
+      // counter's and the plan's latency hides behind the previous item's loads.
+      int nx_idx = -1, nx_qt = 0, nx_b = 0, nx_h = 0, nx_a = 0, nx_c = -1;
+      auto take = [&] {
+        nx_idx = atomicAdd(sched, 1);
+        if (nx_idx >= n_items) { nx_idx = -1; return; }
+        const int npairs = (nq + 1) / 2;
+        nx_h = nx_idx / entries;
+        const int e = pk.order[nx_idx - nx_h * entries];
+        nx_b = e / npairs;
+        nx_qt = 2 * (e - nx_b * npairs);
+        const int* lor = pk.lo + static_cast<long long>(nx_b) * T + nx_qt * 128;
+        nx_a = lor[0] >> 7;
+        nx_c = (nx_qt + 1) * 128 < Tv ? lor[128] >> 7 : -1;
+      };
+      if constexpr (kPacked) take();
       bool ok = true;
       int g = 0, last_q = -1;   // ring position of the next K/V block; last item whose Q was loaded
       for (int n = 0;; ++n) {
         // the previous item's Q is no longer read and every warp has its number
         if (n > 0 && !mbar_wait_t<kFine>(q_empty, (n - 1) & 1, abort_flag, err, wlim)) { ok = false; break; }
-        int idx = sched ? atomicAdd(sched, 1) : n * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-        if (idx >= n_items) idx = -1;
+        int idx;
+        if constexpr (kPacked) {
+          idx = nx_idx;
+          volatile int* f = item_info + 6 * (n & 3);
+          f[0] = nx_b; f[1] = nx_h; f[2] = nx_qt; f[3] = nx_a; f[4] = nx_c;
+        } else {
+          idx = sched ? atomicAdd(sched, 1) : n * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+          if (idx >= n_items) idx = -1;
+        }
         item_ring[n & 3] = idx;
         if (idx < 0) {
           mbar_arrive(q_full);   // end marker: releases the ring entry
           break;
         }
-        const FwdItem it = fwd_item(idx, nq, H, Hkv, kvs, wl);
+        const FwdItem it = item_of(n, idx);
         mbar_arrive_expect_tx(q_full, it.hasB ? 2 * TF_BUF : TF_BUF);
-        tma_load_3d(sQ, &tq, q_full, 0, it.qtA * 128, it.bh);
-        tma_load_3d(sQ + TF_TILE, &tq, q_full, 64, it.qtA * 128, it.bh);
+        tma_load_3d(sQ, mq, q_full, 0, it.qtA * 128, it.bh);
+        tma_load_3d(sQ + TF_TILE, mq, q_full, 64, it.qtA * 128, it.bh);
         if (it.hasB) {
-          tma_load_3d(sQ + TF_BUF, &tq, q_full, 0, it.qtA * 128 + 128, it.bh);
-          tma_load_3d(sQ + TF_BUF + TF_TILE, &tq, q_full, 64, it.qtA * 128 + 128, it.bh);
+          tma_load_3d(sQ + TF_BUF, mq, q_full, 0, it.qtA * 128 + 128, it.bh);
+          tma_load_3d(sQ + TF_BUF + TF_TILE, mq, q_full, 64, it.qtA * 128 + 128, it.bh);
         }
         last_q = n;
+        if constexpr (kPacked) take();
         for (int j = 0; j < it.nkv; ++j) {
           const int s = g & 1;
           const uint32_t par = (g >> 1) & 1;
           const int kc = (it.j0 + j) * 128;
           if (!mbar_wait_t<kFine>(&k_empty[s], par ^ 1u, abort_flag, err, wlim)) { ok = false; break; }
           mbar_arrive_expect_tx(&k_full[s], TF_BUF);
-          tma_load_3d(sK + s * TF_BUF, &tk, &k_full[s], 0, kc, it.bkv);
-          tma_load_3d(sK + s * TF_BUF + TF_TILE, &tk, &k_full[s], 64, kc, it.bkv);
+          tma_load_3d(sK + s * TF_BUF, mk, &k_full[s], 0, kc, it.bkv);
+          tma_load_3d(sK + s * TF_BUF + TF_TILE, mk, &k_full[s], 64, kc, it.bkv);
           if (!mbar_wait_t<kFine>(&v_empty[s], par ^ 1u, abort_flag, err, wlim)) {
             // K of this block is in flight: count it, V is not
             for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(&k_full[s], par); ++i) {}
@@ -235,8 +331,8 @@ __global__ void __launch_bounds__(384, 1)
             break;
           }
           mbar_arrive_expect_tx(&v_full[s], TF_BUF);
-          tma_load_3d(sV + s * TF_BUF, &tv, &v_full[s], 0, kc, it.bkv);
-          tma_load_3d(sV + s * TF_BUF + TF_TILE, &tv, &v_full[s], 64, kc, it.bkv);
+          tma_load_3d(sV + s * TF_BUF, mv, &v_full[s], 0, kc, it.bkv);
+          tma_load_3d(sV + s * TF_BUF + TF_TILE, mv, &v_full[s], 64, kc, it.bkv);
           ++g;
         }
         if (!ok) break;
@@ -288,12 +384,12 @@ __global__ void __launch_bounds__(384, 1)
         if (!mbar_wait_t<kFine>(q_full, n & 1, abort_flag, err, wlim)) { ok = false; break; }
         const int idx = item_ring[n & 3];
         if (idx < 0) break;
-        const FwdItem it = fwd_item(idx, nq, H, Hkv, kvs, wl);
+        const FwdItem it = item_of(n, idx);
         // S of the first block on both tiles, each once its previous P V (which
         // reads P from the same columns) has completed
         if (!mbar_wait_t<kFine>(&k_full[g0 & 1], (g0 >> 1) & 1, abort_flag, err, wlim)) { ok = false; break; }
         for (int t = 0; t < 2 && ok; ++t) {
-          if (t == 1 && !it.hasB) break;
+          if (t == 1 && (!it.hasB || (kPacked && it.oB > 0))) break;
           if (npv[t] > 0 && !mbar_wait_t<kFine>(&pv_done[t], (npv[t] - 1) & 1, abort_flag, err, wlim)) { ok = false; break; }
           tc_fence_after();
           issue_s(t, g0 & 1);
@@ -312,12 +408,15 @@ __global__ void __launch_bounds__(384, 1)
           for (int t = 0; t < 2; ++t) {
             const int nkv_t = t ? it.nkvB : it.nkvA;
             if (j >= nkv_t) continue;
-            if (!mbar_wait_t<kFine>(&p_full[t], npv[t] & 1, abort_flag, err, wlim)) { ok = false; break; }
-            tc_fence_after();
-            issue_pv(t, s, j > 0);
-            ++npv[t];
-            if (j + 1 < nkv_t) {
-              if (!mbar_wait_t<kFine>(&pv_done[t], (npv[t] - 1) & 1, abort_flag, err, wlim)) { ok = false; break; }
+            const int o_t = kPacked && t ? it.oB : 0;   // the tile's first block
+            if (!kPacked || j >= o_t) {
+              if (!mbar_wait_t<kFine>(&p_full[t], npv[t] & 1, abort_flag, err, wlim)) { ok = false; break; }
+              tc_fence_after();
+              issue_pv(t, s, j > o_t);
+              ++npv[t];
+            }
+            if (j + 1 < nkv_t && (!kPacked || j + 1 >= o_t)) {
+              if ((!kPacked || npv[t] > 0) && !mbar_wait_t<kFine>(&pv_done[t], (npv[t] - 1) & 1, abort_flag, err, wlim)) { ok = false; break; }
               tc_fence_after();
               issue_s(t, s1);
               if (j + 1 == it.nkv - 1) umma_commit(q_empty);   // the item's last S
@@ -355,14 +454,20 @@ __global__ void __launch_bounds__(384, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(q_empty);   // this warp has the item number
       if (idx < 0) break;
-      const FwdItem it = fwd_item(idx, nq, H, Hkv, kvs, wl);
+      const FwdItem it = item_of(n, idx);
       if (tile == 1 && !it.hasB) continue;
       const int qt = it.qtA + tile;
       const int q0 = qt * 128;
       const int q = q0 + r;
       const int nkv_t = tile ? it.nkvB : it.nkvA;
+      const int j_first = kPacked && tile ? it.oB : 0;
+      int lo = 0, lo_max = 0;   // packed: first key of this row, and the largest of the warp's rows
+      if constexpr (kPacked) {
+        if (q < Tv) lo = __ldg(pk.lo + static_cast<long long>(it.bh / H) * T + q);
+        lo_max = __reduce_max_sync(0xffffffffu, lo);
+      }
       float m_ref = -INFINITY, l = 0.f;   // reference max (log2 units) and row sum relative to it
-      for (int j = 0; j < nkv_t && ok; ++j) {
+      for (int j = j_first; j < nkv_t && ok; ++j) {
         if (!wait_all(&s_full[tile], nblk & 1)) { ok = false; break; }
         ++nblk;
         tc_fence_after();
@@ -380,7 +485,9 @@ __global__ void __launch_bounds__(384, 1)
           tmem_wait_ld();
         }
         const int kbase = (it.j0 + j) * 128;
-        const bool diag = it.j0 + j == qt, edge = (kbase + 128 > T) || (kbase < q0 + 127 - wl);
+        const bool diag = it.j0 + j == qt;
+        // packed: keys past the last sequence lie above every stored row of the diagonal block
+        const bool edge = kPacked ? kbase < lo_max : (kbase + 128 > T) || (kbase < q0 + 127 - wl);
         if (diag && !edge) {
           // causal diagonal block: only the keys above the row are masked, so
           // per element in one 32-key chunk, whole chunks beyond it
@@ -395,7 +502,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int k = 0; k < 128; ++k) {
             const int key = kbase + k;
-            if (key > q || key >= T || key < q - wl) sr[k] = __float_as_uint(-INFINITY);
+            if (key > q || (kPacked ? key < lo : key >= T || key < q - wl)) sr[k] = __float_as_uint(-INFINITY);
           }
         }
         // block max of the raw scores (the scale is positive), eight independent
@@ -419,7 +526,7 @@ __global__ void __launch_bounds__(384, 1)
         const float factor = none ? 1.f : ex2_approx(m_ref - m_new);
         // O holds the products of blocks < j (S of this block was issued after
         // the last of them completed), so it may be rescaled now
-        if (j >= 1 && __any_sync(0xffffffffu, move)) {
+        if (j > j_first && __any_sync(0xffffffffu, move)) {
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t ra[32];
@@ -476,13 +583,14 @@ __global__ void __launch_bounds__(384, 1)
         tc_fence_after();
         const int b = it.bh / H, h = it.bh - (it.bh / H) * H;
         const float inv = 1.f / l;
-        bf16* orow = o + (static_cast<long long>(b) * T + q) * (static_cast<long long>(H) * 128) + h * 128;
+        bf16* orow = kPacked ? o + (static_cast<long long>(b) * T + q) * pk.o_tok + h * pk.o_head
+                             : o + (static_cast<long long>(b) * T + q) * (static_cast<long long>(H) * 128) + h * 128;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t ra[32];
           tmem_load32_async(t_o + c * 32, ra);
           tmem_wait_ld();
-          if (q < T) {
+          if (q < Tv) {
 #pragma unroll
             for (int k = 0; k < 32; k += 8) {
               uint4 w;
@@ -494,7 +602,7 @@ __global__ void __launch_bounds__(384, 1)
             }
           }
         }
-        if (q < T) lse[static_cast<long long>(it.bh) * T + q] = (m_ref + log2f(l)) * 0.69314718055994531f;
+        if (q < Tv) lse[static_cast<long long>(it.bh) * T + q] = (m_ref + log2f(l)) * 0.69314718055994531f;
         // O of this tile has been read: the next item's first P V may overwrite it
         tc_fence_before();
       }
@@ -598,7 +706,23 @@ __device__ __forceinline__ BwdBlock bwd_block(int idx, int H, int Hkv, int kvs, 
   return k;
 }
 
-template <bool kFine>
+// A packed item as the TMA thread published it: batch row, kv head, key
+// block, number of query blocks that see it.
+__device__ __forceinline__ BwdBlock bwd_block_packed(const volatile int* f, int H, int Hkv, int kvs) {
+  BwdBlock k;
+  k.b = f[0];
+  k.hk = f[1];
+  k.j = f[2];
+  k.nb = f[3];
+  k.k0 = k.j * 128;
+  k.bkv = k.b * Hkv + k.hk;
+  k.kvrow = k.b * kvs + k.hk;
+  k.G = H / Hkv;
+  k.n_it = k.G * k.nb;
+  return k;
+}
+
+template <bool kFine, bool kPacked>
 __global__ void __launch_bounds__(512, 1)
     attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
@@ -606,7 +730,7 @@ __global__ void __launch_bounds__(512, 1)
                        const float* __restrict__ Dv, bf16* __restrict__ dk, bf16* __restrict__ dv, int H, int Hkv,
                        int kvs, int T, int wl, float scale, int n_units, int* sched, int* err,
                        long long wait_cycles, const float* __restrict__ rk, const float2* __restrict__ rope,
-                       bf16* __restrict__ dqkv) {
+                       bf16* __restrict__ dqkv, const PackedArgs pa) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // the 128-byte-swizzled tiles need a 1024-byte-aligned base, which the
   // dynamic shared memory window provides; refuse to run otherwise
@@ -641,10 +765,16 @@ __global__ void __launch_bounds__(512, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 16);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* item_ring = reinterpret_cast<volatile int*>(tmem_holder + 2);   // [4]
+  volatile int* item_info = item_ring + 4;   // [4][4], packed items: bwd_block_packed's fields
 
   const int warp = warp_id(), lane = lane_id();
   const int nq = (T + 127) / 128;
   const long long wlim = wait_limit_or_default(wait_cycles);
+  const int Tv = kPacked ? pa.ctl[kCtlValid] : T;   // positions of a row that hold sequences
+  auto block_of = [&](int n, int idx) -> BwdBlock {
+    if constexpr (kPacked) return bwd_block_packed(item_info + 4 * (n & 3), H, Hkv, kvs);
+    else return bwd_block(idx, H, Hkv, kvs, nq, wl);
+  };
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
@@ -662,10 +792,12 @@ __global__ void __launch_bounds__(512, 1)
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
-    tma_prefetch_desc(&tq);
-    tma_prefetch_desc(&tk);
-    tma_prefetch_desc(&tv);
-    tma_prefetch_desc(&tdo);
+    if constexpr (!kPacked) {
+      tma_prefetch_desc(&tq);
+      tma_prefetch_desc(&tk);
+      tma_prefetch_desc(&tv);
+      tma_prefetch_desc(&tdo);
+    }
     tma_prefetch_desc(&tdq);
   }
   if (warp == 1) {
@@ -684,6 +816,32 @@ __global__ void __launch_bounds__(512, 1)
   if (warp == 0) {
     if (lane == 0) {
       // -------------------------------------------------------------- TMA
+      const CUtensorMap* mq = kPacked ? pa.maps : &tq;
+      const CUtensorMap* mk = kPacked ? pa.maps + 1 : &tk;
+      const CUtensorMap* mv = kPacked ? pa.maps + 2 : &tv;
+      const CUtensorMap* mdo = kPacked ? pa.maps + 3 : &tdo;
+      int entries = 0;
+      if constexpr (kPacked) {
+        tensormap_acquire(mq);
+        tensormap_acquire(mk);
+        tensormap_acquire(mv);
+        tensormap_acquire(mdo);
+        entries = pa.ctl[kCtlEntries];
+        n_units = entries * Hkv;
+      }
+      // packed: fetched one item ahead, as in the forward
+      int nx_idx = -1, nx_b = 0, nx_hk = 0, nx_j = 0, nx_nb = 0;
+      auto take = [&] {
+        nx_idx = atomicAdd(sched, 1);
+        if (nx_idx >= n_units) { nx_idx = -1; return; }
+        nx_hk = nx_idx / entries;
+        const int e = pa.order[nx_idx - nx_hk * entries];
+        nx_b = e / nq;
+        nx_j = e - nx_b * nq;
+        // hi grows with the key: the block's last key is seen furthest
+        nx_nb = (pa.hi[static_cast<long long>(nx_b) * T + min(nx_j * 128 + 127, Tv - 1)] >> 7) - nx_j + 1;
+      };
+      if constexpr (kPacked) take();
       bool ok = true;
       int g = 0, nblk = 0;          // query blocks and items loaded so far
       int issued_q = 0, issued_do = 0;
@@ -692,13 +850,13 @@ __global__ void __launch_bounds__(512, 1)
         const int s = g & 1;
         if (!mbar_wait_t<kFine>(&q_empty[s], ((g >> 1) & 1) ^ 1u, abort_flag, err, wlim)) return false;
         mbar_arrive_expect_tx(&q_full[s], TF_BUF);
-        tma_load_3d(sQ + s * TF_BUF, &tq, &q_full[s], 0, i * 128, bh);
-        tma_load_3d(sQ + s * TF_BUF + TF_TILE, &tq, &q_full[s], 64, i * 128, bh);
+        tma_load_3d(sQ + s * TF_BUF, mq, &q_full[s], 0, i * 128, bh);
+        tma_load_3d(sQ + s * TF_BUF + TF_TILE, mq, &q_full[s], 64, i * 128, bh);
         ++issued_q;
         if (!mbar_wait_t<kFine>(do_empty, (g & 1) ^ 1u, abort_flag, err, wlim)) return false;
         mbar_arrive_expect_tx(do_full, TF_BUF);
-        tma_load_4d(sdO, &tdo, do_full, 0, h, i * 128, kb.b);
-        tma_load_4d(sdO + TF_TILE, &tdo, do_full, 64, h, i * 128, kb.b);
+        tma_load_4d(sdO, mdo, do_full, 0, h, i * 128, kb.b);
+        tma_load_4d(sdO + TF_TILE, mdo, do_full, 64, h, i * 128, kb.b);
         ++issued_do;
         ++g;
         return true;
@@ -711,7 +869,11 @@ __global__ void __launch_bounds__(512, 1)
       for (int n = 0; ok; ++n) {
         int idx = pending;
         pending = -1;
-        if (idx < 0) {
+        if constexpr (kPacked) {
+          idx = nx_idx;
+          volatile int* f = item_info + 4 * (n & 3);
+          f[0] = nx_b; f[1] = nx_hk; f[2] = nx_j; f[3] = nx_nb;
+        } else if (idx < 0) {
           const int unit = sched ? atomicAdd(sched, 1) : taken * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
           ++taken;
           if (unit < n_units) {
@@ -727,18 +889,19 @@ __global__ void __launch_bounds__(512, 1)
           mbar_arrive(kv_full);
           break;
         }
-        const BwdBlock kb = bwd_block(idx, H, Hkv, kvs, nq, wl);
+        const BwdBlock kb = block_of(n, idx);
         // the first query block's Q and dO may load while the previous item
         // finishes; K and V (which publish the item number) once its last
         // products are done
         if (!load_q_do(kb, 0)) { ok = false; break; }
         if (n > 0 && !mbar_wait_t<kFine>(kv_empty, (n - 1) & 1, abort_flag, err, wlim)) { ok = false; break; }
         mbar_arrive_expect_tx(kv_full, 2 * TF_BUF);
-        tma_load_3d(sK, &tk, kv_full, 0, kb.k0, kb.kvrow);
-        tma_load_3d(sK + TF_TILE, &tk, kv_full, 64, kb.k0, kb.kvrow);
-        tma_load_3d(sV, &tv, kv_full, 0, kb.k0, kb.kvrow);
-        tma_load_3d(sV + TF_TILE, &tv, kv_full, 64, kb.k0, kb.kvrow);
+        tma_load_3d(sK, mk, kv_full, 0, kb.k0, kb.kvrow);
+        tma_load_3d(sK + TF_TILE, mk, kv_full, 64, kb.k0, kb.kvrow);
+        tma_load_3d(sV, mv, kv_full, 0, kb.k0, kb.kvrow);
+        tma_load_3d(sV + TF_TILE, mv, kv_full, 64, kb.k0, kb.kvrow);
         ++nblk;
+        if constexpr (kPacked) take();
         for (int it = 1; it < kb.n_it; ++it)
           if (!load_q_do(kb, it)) { ok = false; break; }
       }
@@ -778,7 +941,7 @@ __global__ void __launch_bounds__(512, 1)
         const int idx = item_ring[n & 3];
         if (idx < 0) break;
         {
-          const BwdBlock kb = bwd_block(idx, H, Hkv, kvs, nq, wl);
+          const BwdBlock kb = block_of(n, idx);
           const int n_it = kb.n_it;
           // S^T of the first query block goes where the previous key block's
           // last dQ was (wait until the dQ warps have read it), dP^T where
@@ -900,7 +1063,7 @@ __global__ void __launch_bounds__(512, 1)
       if (lane == 0) mbar_arrive(kv_empty);   // this warp has the item number
       if (idx < 0) break;
       {
-        const BwdBlock kb = bwd_block(idx, H, Hkv, kvs, nq, wl);
+        const BwdBlock kb = block_of(n, idx);
         for (int it = 0; it < kb.n_it && ok; ++it, ++g) {
           const int q0 = kb.q_block(it) * 128 + quarter * 32, bh = kb.b * H + kb.q_head(it);
           const bool got = mbar_wait_t<kFine>(mm_done, g & 1, abort_flag, err, wlim);
@@ -981,10 +1144,16 @@ __global__ void __launch_bounds__(512, 1)
       if (lane == 0 && (idx < 0 || !dqkv)) mbar_arrive(kv_empty);
       if (idx < 0) break;
       {
-        const BwdBlock kb = bwd_block(idx, H, Hkv, kvs, nq, wl);
+        const BwdBlock kb = block_of(n, idx);
         const int n_it = kb.n_it, k0 = kb.k0, bkv = kb.kvrow;
         const int key = k0 + r;
-        const bool key_ok = key < T;
+        const bool key_ok = key < Tv;
+        int hi = 0, hi_min = 0, hi_max = 0;   // packed: last query that sees this key, and over the warp's keys
+        if constexpr (kPacked) {
+          hi = key_ok ? __ldg(pa.hi + static_cast<long long>(kb.b) * T + key) : -1;
+          hi_min = __reduce_min_sync(0xffffffffu, hi);
+          hi_max = __reduce_max_sync(0xffffffffu, hi);
+        }
         if (dqkv && key_ok) {
           // the epilogue's rotation table row and inverse RMS, on their way to L2
           asm volatile("prefetch.global.L2 [%0];" ::"l"(rope + static_cast<long long>(key) * 64 + 32 * half));
@@ -998,10 +1167,10 @@ __global__ void __launch_bounds__(512, 1)
           const long long bh = static_cast<long long>(kb.b) * H + kb.q_head(it2);
           if (t256 < 128) {
             const int qq = q0f + t256;
-            return qq < T ? __ldg(lse + bh * T + qq) * -1.4426950408889634f : -INFINITY;
+            return qq < Tv ? __ldg(lse + bh * T + qq) * -1.4426950408889634f : -INFINITY;
           }
           const int qq = q0f + t256 - 128;
-          return qq < T ? -__ldg(Dv + bh * T + qq) : 0.f;
+          return qq < Tv ? -__ldg(Dv + bh * T + qq) : 0.f;
         };
         // block it2's values go to buffer (g0 + it2) & 1; a barrier publishes them
         auto publish = [&](int it2, float v) {
@@ -1066,7 +1235,11 @@ __global__ void __launch_bounds__(512, 1)
                 } else if constexpr (mode == 2) {
 #pragma unroll
                   for (int e = 0; e < 8; ++e)
-                    if (!key_ok || (diag && key > q0 + c * 32 + kq + e) || key < q0 + c * 32 + kq + e - wl) p[e] = 0.f;
+                    if constexpr (kPacked) {
+                      if ((diag && key > q0 + c * 32 + kq + e) || hi < q0 + c * 32 + kq + e) p[e] = 0.f;
+                    } else {
+                      if (!key_ok || (diag && key > q0 + c * 32 + kq + e) || key < q0 + c * 32 + kq + e - wl) p[e] = 0.f;
+                    }
                 }
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) pk[16 * cc + ((kq + e) >> 1)] = pack_bf16x2(p[e], p[e + 1]);
@@ -1079,7 +1252,18 @@ __global__ void __launch_bounds__(512, 1)
           using M3 = std::integral_constant<int, 3>;
           auto do_chunk = [&](auto kCC) {
             const int c = 2 * half + decltype(kCC)::value;
-            if (diag && !edge) {
+            if constexpr (kPacked) {
+              // the same forms by the warp's keys' last queries
+              const int qc = q0 + c * 32;
+              if (qc > hi_max || (diag && c < quarter))
+                run_chunk(kCC, M3{});
+              else if (qc + 31 > hi_min)
+                run_chunk(kCC, M2{});
+              else if (diag && c == quarter)
+                run_chunk(kCC, M1{});
+              else
+                run_chunk(kCC, M0{});
+            } else if (diag && !edge) {
               if (c < quarter)
                 run_chunk(kCC, M3{});
               else if (c == quarter)
@@ -1264,8 +1448,10 @@ __global__ void __launch_bounds__(512, 1)
           tc_fence_before();
         } else if (ok) {
           tc_fence_after();
-          bf16* dkrow = dk + (static_cast<long long>(bkv) * T + key) * 128;
-          bf16* dvrow = dv + (static_cast<long long>(bkv) * T + key) * 128;
+          bf16* dkrow = kPacked ? dk + (static_cast<long long>(kb.b) * T + key) * pa.o_tok + kb.hk * pa.o_head
+                                : dk + (static_cast<long long>(bkv) * T + key) * 128;
+          bf16* dvrow = kPacked ? dv + (static_cast<long long>(kb.b) * T + key) * pa.dv_tok + kb.hk * pa.dv_head
+                                : dv + (static_cast<long long>(bkv) * T + key) * 128;
 #pragma unroll 1
           for (int c = 2 * half; c < 2 * half + 2; ++c) {
             uint32_t vr[32], kr[32];
@@ -1325,6 +1511,253 @@ __global__ void attn_bwd_dot_kernel(const bf16* __restrict__ o, const bf16* __re
   if (lane_id() == 0) Dv[w] = s;
 }
 
+// --------------------------------------------------- packed: plan and setup
+
+// The plan's layout in int32 words: kPlanMeta words (total positions held by
+// sequences, forward and backward entry counts, B, T, positions past the
+// sequences covered), lo and hi [B * T], forward order [B * npairs], backward
+// order [B * nblocks].
+enum { kMetaTotal = 0, kMetaFwd = 1, kMetaBwd = 2, kMetaB = 3, kMetaT = 4, kMetaMagic = 5, kPlanMeta = 64 };
+constexpr int kPlanMagic = 0x5e91a7e;
+struct PlanView {
+  int* meta;
+  int* lo;
+  int* hi;
+  int* fwd;
+  int* bwd;
+  size_t words;
+};
+__host__ __device__ inline PlanView plan_view(void* base, int B, int T) {
+  const size_t n = static_cast<size_t>(B) * T, nq = (T + 127) / 128;
+  int* p = static_cast<int*>(base);
+  PlanView v;
+  v.meta = p;
+  v.lo = p + kPlanMeta;
+  v.hi = v.lo + n;
+  v.fwd = v.hi + n;
+  v.bwd = v.fwd + B * ((nq + 1) / 2);
+  v.words = kPlanMeta + 2 * n + B * ((nq + 1) / 2) + B * nq;
+  return v;
+}
+
+// Sequence of position p, row-local: [start, end) within p's row of T
+// positions (a sequence that crosses a row's end is split there).  Offsets
+// that are not in order give some range that still holds p.
+struct SeqRange { int start, end; };
+__device__ __forceinline__ SeqRange seq_range(const int* __restrict__ cu, int n_seq, int total, int B, int T, int p) {
+  int a = total, b = B * T;   // past the last sequence: one more
+  if (p < total && n_seq > 0) {
+    int l = 0, r = n_seq - 1;   // the last s with cu[s] <= p
+    while (l < r) {
+      const int m = (l + r + 1) >> 1;
+      if (__ldg(cu + m) <= p) l = m;
+      else r = m - 1;
+    }
+    a = __ldg(cu + l);
+    b = __ldg(cu + l + 1);
+  }
+  const int row = p / T * T;
+  SeqRange s;
+  s.start = max(0, min(a, p) - row);
+  s.end = min(T, max(b, p + 1) - row);
+  return s;
+}
+
+// Blocks past the first fill lo and hi; the first checks the offsets (in
+// order, from 0, at most B * T; otherwise nothing is covered and the error is
+// latched), and sorts the work entries of both directions by their number of
+// 128 x 128 blocks with a counting sort (longest first; entries of one length
+// in no fixed order, which no output of the forward depends on).
+__global__ void __launch_bounds__(1024)
+    attention_plan_kernel(const int* __restrict__ cu, int n_seq, int B, int T, int window, int cover, void* plan,
+                          int* err) {
+  const PlanView P = plan_view(plan, B, T);
+  const int n = B * T;
+  const int last = n_seq > 0 ? __ldg(cu + n_seq) : 0;
+  const int total = max(0, min(last, n));
+  const int wl = window < 0 ? n : window;
+  if (blockIdx.x > 0) {
+    const int p = (blockIdx.x - 1) * blockDim.x + threadIdx.x;
+    if (p >= n) return;
+    const int t = p % T;
+    int lo = 0, hi = -1;
+    if (p < total || cover) {
+      const SeqRange s = seq_range(cu, n_seq, total, B, T, p);
+      lo = max(s.start, t - min(wl, t));
+      hi = min(s.end - 1, t + min(wl, T - 1 - t));
+    }
+    P.lo[p] = lo;
+    P.hi[p] = hi;
+    return;
+  }
+  constexpr int kBuckets = 1024;
+  __shared__ int hist[kBuckets];
+  __shared__ int warp_total[32];
+  int bad = (n_seq > 0 && __ldg(cu) != 0) || last > n;
+  for (int i = threadIdx.x; i < n_seq; i += blockDim.x) bad |= __ldg(cu + i + 1) < __ldg(cu + i);
+  bad = __syncthreads_or(bad);
+  const int valid = bad ? 0 : cover ? n : total;
+  if (threadIdx.x == 0) {
+    if (bad && err) atomicOr(err, ERRF_SEQUENCE);
+    P.meta[kMetaTotal] = valid;
+    P.meta[kMetaB] = B;
+    P.meta[kMetaT] = T;
+    P.meta[kMetaMagic] = kPlanMagic;
+  }
+  const int nq = (T + 127) / 128, npairs = (nq + 1) / 2;
+  for (int dir = 0; dir < 2; ++dir) {
+    const int per_row = dir ? nq : npairs, count = B * per_row;
+    // blocks of entry e: 0 if it holds no position of a sequence
+    auto cost = [&](int e) -> int {
+      const int b = e / per_row, i = e - b * per_row, r0 = b * T;
+      const int tv = max(0, min(T, valid - r0));
+      if (dir) {
+        const int k0 = i * 128;
+        if (k0 >= tv) return 0;
+        const int k = min(k0 + 127, tv - 1);
+        const SeqRange s = seq_range(cu, n_seq, total, B, T, r0 + k);
+        return (min(s.end - 1, k + min(wl, T - 1 - k)) >> 7) - i + 1;
+      }
+      int c = 0;
+      for (int qt = 2 * i; qt < 2 * i + 2; ++qt) {
+        const int q = qt * 128;
+        if (q >= tv) break;
+        const SeqRange s = seq_range(cu, n_seq, total, B, T, r0 + q);
+        c += qt + 1 - (max(s.start, q - min(wl, q)) >> 7);
+      }
+      return c;
+    };
+    for (int i = threadIdx.x; i < kBuckets; i += blockDim.x) hist[i] = 0;
+    __syncthreads();
+    for (int e = threadIdx.x; e < count; e += blockDim.x) {
+      const int c = cost(e);
+      if (c > 0) atomicAdd(&hist[kBuckets - min(c, kBuckets)], 1);
+    }
+    __syncthreads();
+    // exclusive sums of the 1024 buckets, one per thread
+    const int mine = hist[threadIdx.x];
+    int x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane_id() >= o) x += y;
+    }
+    if (lane_id() == 31) warp_total[warp_id()] = x;
+    __syncthreads();
+    if (warp_id() == 0) {
+      int w = warp_total[lane_id()];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane_id() >= o) w += y;
+      }
+      warp_total[lane_id()] = w;
+    }
+    __syncthreads();
+    const int before = x - mine + (warp_id() ? warp_total[warp_id() - 1] : 0);
+    if (threadIdx.x == 0) P.meta[dir ? kMetaBwd : kMetaFwd] = warp_total[31];
+    hist[threadIdx.x] = before;
+    __syncthreads();
+    int* order = dir ? P.bwd : P.fwd;
+    for (int e = threadIdx.x; e < count; e += blockDim.x) {
+      const int c = cost(e);
+      if (c > 0) order[atomicAdd(&hist[kBuckets - min(c, kBuckets)], 1)] = e;
+    }
+    __syncthreads();
+  }
+}
+
+// Control words and tensor maps of one packed launch, by one warp.  A plan
+// made for another shape is refused: no entries, the error latched.
+struct SetupMaps {
+  CUtensorMap m[4];
+};
+__device__ __forceinline__ void packed_setup(const SetupMaps& in, int n_maps, CUtensorMap* out, int* ctl,
+                                             const int* meta, int B, int T, int dir, int* err,
+                                             CUtensorMap* stage) {
+  const int lane = lane_id();
+  const bool fits = meta[kMetaMagic] == kPlanMagic && meta[kMetaB] == B && meta[kMetaT] == T;
+  const int valid = fits ? (B == 1 ? meta[kMetaTotal] : T) : 0;
+  if (lane == 0) {
+    if (!fits && err) atomicOr(err, ERRF_SHAPE);
+    ctl[kCtlSched] = 0;
+    ctl[kCtlEntries] = fits ? meta[dir ? kMetaBwd : kMetaFwd] : 0;
+    ctl[kCtlValid] = valid;
+  }
+  for (int i = 0; i < n_maps; ++i)
+    reinterpret_cast<uint32_t*>(&stage[i])[lane] = reinterpret_cast<const uint32_t*>(&in.m[i])[lane];
+  __syncwarp();
+  if (lane == 0 && B == 1 && valid > 0 && valid < T) {
+    // the token extent (dimension 1 of q, k, v; 2 of dO) ends with the sequences
+    for (int i = 0; i < n_maps; ++i) {
+      if (i < 3)
+        asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(
+                         smem_u32(&stage[i])), "r"(valid) : "memory");
+      else
+        asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 2, %1;" ::"r"(
+                         smem_u32(&stage[i])), "r"(valid) : "memory");
+    }
+  }
+  __syncwarp();
+  for (int i = 0; i < n_maps; ++i)
+    asm volatile(
+        "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::"l"(
+            out + i),
+        "r"(smem_u32(&stage[i]))
+        : "memory");
+}
+
+__global__ void __launch_bounds__(32)
+    attention_setup_kernel(const __grid_constant__ SetupMaps in, CUtensorMap* out, int* ctl, const int* meta, int B,
+                           int T, int* err) {
+  __shared__ __align__(128) CUtensorMap stage[4];
+  packed_setup(in, 3, out, ctl, meta, B, T, 0, err, stage);
+}
+
+// Backward: D[b, h, t] = sum_i dO * O of the rows that hold sequences and
+// zeros in the fp32 dq accumulator, one warp per (t, h) row; the first block
+// also does the setup.
+__global__ void __launch_bounds__(256)
+    attention_packed_pre_kernel(const __grid_constant__ SetupMaps in, CUtensorMap* out, int* ctl, const int* meta,
+                                const bf16* __restrict__ o, long long o_tok, long long o_head,
+                                const bf16* __restrict__ dout, long long do_tok, long long do_head,
+                                float* __restrict__ Dv, float* __restrict__ dq, int B, int H, int T, int* err) {
+  __shared__ __align__(128) CUtensorMap stage[4];
+  if (blockIdx.x == 0) {
+    if (warp_id() == 0) packed_setup(in, 4, out, ctl, meta, B, T, 1, err, stage);
+    return;
+  }
+  const long long w = static_cast<long long>(blockIdx.x - 1) * 8 + warp_id();
+  const int h = static_cast<int>(w % H);
+  const long long p = w / H;
+  if (p >= static_cast<long long>(B) * T) return;
+  const int b = static_cast<int>(p / T), t = static_cast<int>(p - static_cast<long long>(b) * T);
+  if (meta[kMetaMagic] != kPlanMagic || meta[kMetaB] != B || meta[kMetaT] != T || p >= meta[kMetaTotal]) return;
+  const long long row = (static_cast<long long>(b) * H + h) * T + t;
+  const uint2 x = *reinterpret_cast<const uint2*>(o + p * o_tok + h * o_head + lane_id() * 4);
+  const uint2 y = *reinterpret_cast<const uint2*>(dout + p * do_tok + h * do_head + lane_id() * 4);
+  reinterpret_cast<float4*>(dq + row * HD)[lane_id()] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float s = bf16_lo(x.x) * bf16_lo(y.x) + bf16_hi(x.x) * bf16_hi(y.x) + bf16_lo(x.y) * bf16_lo(y.y) +
+            bf16_hi(x.y) * bf16_hi(y.y);
+  s = warp_sum(s);
+  if (lane_id() == 0) Dv[row] = s;
+}
+
+// dq in bf16 from the fp32 sums, rows that hold sequences; one warp per (t, h).
+__global__ void __launch_bounds__(256)
+    attention_packed_dq_kernel(const float* __restrict__ acc, bf16* __restrict__ dq, long long dq_tok,
+                               long long dq_head, const int* ctl, int H, int T) {
+  const long long w = static_cast<long long>(blockIdx.x) * 8 + warp_id();
+  const int h = static_cast<int>(w % H);
+  const long long t = w / H;
+  if (t >= ctl[kCtlValid]) return;
+  const float4 v = reinterpret_cast<const float4*>(acc + (static_cast<long long>(h) * T + t) * HD)[lane_id()];
+  uint2 u;
+  u.x = pack_bf16x2(v.x, v.y);
+  u.y = pack_bf16x2(v.z, v.w);
+  *reinterpret_cast<uint2*>(dq + t * dq_tok + h * dq_head + lane_id() * 4) = u;
+}
+
 }  // namespace
 
 // Window in tokens as the kernels take it: keys t - wl .. t; "no window" is a
@@ -1353,7 +1786,7 @@ void launch_attn_fwd(const bf16* q, const bf16* k, const bf16* v, bf16* o, float
                      long long wait_cycles) {
   // a limit shorter than one blocking probe needs the finely polling build
   const bool fine = wait_limit_or_default(wait_cycles) < kShortWaitCycles;
-  auto kern = fine ? attn_fwd_tc_kernel<true> : attn_fwd_tc_kernel<false>;
+  auto kern = fine ? attn_fwd_tc_kernel<true, false> : attn_fwd_tc_kernel<false, false>;
   static std::atomic<unsigned long long> configured[2] = {};
   if (set_smem_limit_once(kern, TF_SMEM, configured[fine ? 1 : 0]) != cudaSuccess) {
     if (err) cudaMemsetAsync(err, 0xff, sizeof(int), s);   // latched as a device error
@@ -1375,7 +1808,7 @@ void launch_attn_fwd(const bf16* q, const bf16* k, const bf16* v, bf16* o, float
   const float scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(HD));
   kern<<<grid, 384, TF_SMEM, s>>>(mq, mk, mv, o, lse, H, Hkv, kv_stride, T, window_bound(window, T),
                                                 scale_log2,
-                                                static_cast<int>(n_items), sched_word(sched, s), err, wait_cycles);
+                                                static_cast<int>(n_items), sched_word(sched, s), err, wait_cycles, PackedArgs{});
 }
 
 void launch_attn_bwd(const bf16* q, const bf16* k, const bf16* v, const bf16* o, const bf16* dout,
@@ -1383,7 +1816,7 @@ void launch_attn_bwd(const bf16* q, const bf16* k, const bf16* v, const bf16* o,
                      cudaStream_t s, int* err, int Hkv, int window, int* sched, int kv_stride,
                      long long wait_cycles, const float* rk, const float2* rope, bf16* dqkv, bool d_ready) {
   const bool fine = wait_limit_or_default(wait_cycles) < kShortWaitCycles;
-  auto kern = fine ? attn_bwd_tc_kernel<true> : attn_bwd_tc_kernel<false>;
+  auto kern = fine ? attn_bwd_tc_kernel<true, false> : attn_bwd_tc_kernel<false, false>;
   static std::atomic<unsigned long long> configured[2] = {};
   if (set_smem_limit_once(kern, TB_SMEM, configured[fine ? 1 : 0]) != cudaSuccess) {
     if (err) cudaMemsetAsync(err, 0xff, sizeof(int), s);   // latched as a device error
@@ -1417,7 +1850,118 @@ void launch_attn_bwd(const bf16* q, const bf16* k, const bf16* v, const bf16* o,
   int* word = wl >= T ? nullptr : sched_word(sched, s);
   kern<<<grid, 512, TB_SMEM, s>>>(mq, mk, mv, mdo, mdq, lse, Dv, dk, dv, H, Hkv, kv_stride, T, wl,
                                                 1.f / sqrtf(static_cast<float>(HD)), static_cast<int>(n_units),
-                                                word, err, wait_cycles, rk, rope, dqkv);
+                                                word, err, wait_cycles, rk, rope, dqkv, PackedArgs{});
+}
+
+// ---------------------------------------------------------- packed launchers
+
+namespace {
+
+constexpr size_t al256(size_t x) { return (x + 255) / 256 * 256; }
+
+// control words, then the four tensor maps, then (backward) D and the fp32 dq
+constexpr size_t kPackedHead = 256 + 4 * sizeof(CUtensorMap);
+
+// Strides of an extent-1 dimension are never used: any legal value stands in.
+long long stride_or(long long extent, long long stride) { return extent > 1 ? stride : HD; }
+
+bool map_heads(CUtensorMap* m, const PackedTensor& t, long long tokens, long long heads) {
+  return make_map(m, t.ptr, 2, HD, tokens, heads, stride_or(tokens, t.tok), stride_or(heads, t.head), 64, 128);
+}
+
+}  // namespace
+
+size_t attention_plan_bytes(int B, int T) { return al256(plan_view(nullptr, B, T).words * sizeof(int)); }
+
+size_t attention_packed_scratch(int T, int H, bool backward) {
+  const size_t rows = static_cast<size_t>(T) * H;
+  return al256(kPackedHead) + (backward ? al256(rows * sizeof(float)) + al256(rows * HD * sizeof(float)) : 0);
+}
+
+void launch_attention_plan(const int* cu, int n_seq, int B, int T, int window, bool cover, void* plan, int* err,
+                           cudaStream_t s) {
+  const int blocks = 1 + static_cast<int>((static_cast<long long>(B) * T + 1023) / 1024);
+  attention_plan_kernel<<<blocks, 1024, 0, s>>>(cu, n_seq, B, T, window, cover ? 1 : 0, plan, err);
+}
+
+cudaError_t launch_attn_packed_fwd(const PackedTensor& q, const PackedTensor& k, const PackedTensor& v,
+                                   const PackedTensor& o, float* lse, int H, int Hkv, int T, float scale,
+                                   const void* plan, void* scratch, cudaStream_t s, int* err, long long wait_cycles) {
+  const bool fine = wait_limit_or_default(wait_cycles) < kShortWaitCycles;
+  auto kern = fine ? attn_fwd_tc_kernel<true, true> : attn_fwd_tc_kernel<false, true>;
+  static std::atomic<unsigned long long> configured[2] = {};
+  cudaError_t e = set_smem_limit_once(kern, TF_SMEM, configured[fine ? 1 : 0]);
+  if (e != cudaSuccess) return e;
+  SetupMaps maps = {};
+  if (!map_heads(&maps.m[0], q, T, H) || !map_heads(&maps.m[1], k, T, Hkv) || !map_heads(&maps.m[2], v, T, Hkv))
+    return cudaErrorInvalidValue;
+  const PlanView P = plan_view(const_cast<void*>(plan), 1, T);
+  int* ctl = static_cast<int*>(scratch);
+  CUtensorMap* dmaps = reinterpret_cast<CUtensorMap*>(static_cast<uint8_t*>(scratch) + 256);
+  attention_setup_kernel<<<1, 32, 0, s>>>(maps, dmaps, ctl, P.meta, 1, T, err);
+  PackedArgs pa = {};
+  pa.lo = P.lo;
+  pa.hi = P.hi;
+  pa.order = P.fwd;
+  pa.ctl = ctl;
+  pa.maps = dmaps;
+  pa.o_tok = o.tok;
+  pa.o_head = o.head;
+  const long long items = 1ll * ((T + 127) / 128 + 1) / 2 * H;
+  const int grid = static_cast<int>(std::min<long long>(items, device_sm_count()));
+  kern<<<grid, 384, TF_SMEM, s>>>(maps.m[0], maps.m[1], maps.m[2], static_cast<bf16*>(const_cast<void*>(o.ptr)), lse, H, Hkv, Hkv, T, 1 << 30,
+                                  scale * 1.4426950408889634f, 0, ctl + kCtlSched, err, wait_cycles, pa);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_attn_packed_bwd(const PackedTensor& q, const PackedTensor& k, const PackedTensor& v,
+                                   const PackedTensor& o, const PackedTensor& dout, const float* lse,
+                                   const PackedTensor& dq, const PackedTensor& dk, const PackedTensor& dv, int H,
+                                   int Hkv, int T, float scale, const void* plan, void* scratch, cudaStream_t s,
+                                   int* err, long long wait_cycles) {
+  const bool fine = wait_limit_or_default(wait_cycles) < kShortWaitCycles;
+  auto kern = fine ? attn_bwd_tc_kernel<true, true> : attn_bwd_tc_kernel<false, true>;
+  static std::atomic<unsigned long long> configured[2] = {};
+  cudaError_t e = set_smem_limit_once(kern, TB_SMEM, configured[fine ? 1 : 0]);
+  if (e != cudaSuccess) return e;
+  const size_t rows = static_cast<size_t>(T) * H;
+  uint8_t* base = static_cast<uint8_t*>(scratch);
+  int* ctl = reinterpret_cast<int*>(base);
+  CUtensorMap* dmaps = reinterpret_cast<CUtensorMap*>(base + 256);
+  float* Dv = reinterpret_cast<float*>(base + al256(kPackedHead));
+  float* acc = reinterpret_cast<float*>(base + al256(kPackedHead) + al256(rows * sizeof(float)));
+  SetupMaps maps = {};
+  CUtensorMap mdq;
+  const long long dims[4] = {HD, H, T, 1};
+  const long long strides[3] = {stride_or(H, dout.head) * 2, stride_or(T, dout.tok) * 2, 16};
+  const int box[4] = {64, 1, 128, 1};
+  if (!map_heads(&maps.m[0], q, T, H) || !map_heads(&maps.m[1], k, T, Hkv) || !map_heads(&maps.m[2], v, T, Hkv) ||
+      !make_map_4d(&maps.m[3], dout.ptr, dims, strides, box) ||
+      !make_map(&mdq, acc, 4, HD, T, H, HD, 1ll * T * HD, 32, 32))
+    return cudaErrorInvalidValue;
+  const PlanView P = plan_view(const_cast<void*>(plan), 1, T);
+  const int row_blocks = static_cast<int>((rows + 7) / 8);
+  attention_packed_pre_kernel<<<1 + row_blocks, 256, 0, s>>>(
+      maps, dmaps, ctl, P.meta, static_cast<const bf16*>(o.ptr), o.tok, o.head, static_cast<const bf16*>(dout.ptr),
+      dout.tok, dout.head, Dv, acc, 1, H, T, err);
+  PackedArgs pa = {};
+  pa.lo = P.lo;
+  pa.hi = P.hi;
+  pa.order = P.bwd;
+  pa.ctl = ctl;
+  pa.maps = dmaps;
+  pa.o_tok = dk.tok;
+  pa.o_head = dk.head;
+  pa.dv_tok = dv.tok;
+  pa.dv_head = dv.head;
+  const long long units = 1ll * ((T + 127) / 128) * Hkv;
+  const int grid = static_cast<int>(std::min<long long>(units, device_sm_count()));
+  kern<<<grid, 512, TB_SMEM, s>>>(maps.m[0], maps.m[1], maps.m[2], maps.m[3], mdq, lse, Dv,
+                                  static_cast<bf16*>(const_cast<void*>(dk.ptr)),
+                                  static_cast<bf16*>(const_cast<void*>(dv.ptr)), H, Hkv, Hkv, T, 1 << 30, scale, 0,
+                                  ctl + kCtlSched, err, wait_cycles, nullptr, nullptr, nullptr, pa);
+  attention_packed_dq_kernel<<<row_blocks, 256, 0, s>>>(acc, static_cast<bf16*>(const_cast<void*>(dq.ptr)), dq.tok, dq.head, ctl, H, T);
+  return cudaGetLastError();
 }
 
 }  // namespace gpt

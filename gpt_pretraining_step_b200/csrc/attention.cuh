@@ -38,4 +38,34 @@ void launch_attn_bwd(const bf16* q, const bf16* k, const bf16* v, const bf16* o,
                      int kv_stride = 0, long long wait_cycles = 0, const float* rk = nullptr,
                      const float2* rope = nullptr, bf16* dqkv = nullptr, bool d_ready = false);
 
+// ------------------------------------------------------- packed sequences
+
+// A [tokens, heads, 128] bf16 tensor with any token and head strides (in
+// elements, multiples of 8; the 128 dims contiguous, 16-byte aligned).
+struct PackedTensor {
+  const void* ptr;
+  long long tok, head;
+};
+
+// The plan of a batch of sequences (cu [n_seq + 1], int32, device) that lie
+// end to end in B rows of T positions: masks and work order for the packed
+// kernels.  cover: positions past cu[n_seq] form one more sequence; otherwise
+// they are left alone.  Offsets that do not start at 0, decrease, or pass
+// B * T latch ERRF_SEQUENCE and plan no work.
+size_t attention_plan_bytes(int B, int T);
+void launch_attention_plan(const int* cu, int n_seq, int B, int T, int window, bool cover, void* plan, int* err,
+                           cudaStream_t s);
+
+// Packed attention over one row of T positions with a plan of B = 1.
+// cudaErrorInvalidValue: a tensor whose base or strides TMA cannot take.
+size_t attention_packed_scratch(int T, int H, bool backward);
+cudaError_t launch_attn_packed_fwd(const PackedTensor& q, const PackedTensor& k, const PackedTensor& v,
+                                   const PackedTensor& o, float* lse, int H, int Hkv, int T, float scale,
+                                   const void* plan, void* scratch, cudaStream_t s, int* err, long long wait_cycles);
+cudaError_t launch_attn_packed_bwd(const PackedTensor& q, const PackedTensor& k, const PackedTensor& v,
+                                   const PackedTensor& o, const PackedTensor& dout, const float* lse,
+                                   const PackedTensor& dq, const PackedTensor& dk, const PackedTensor& dv, int H,
+                                   int Hkv, int T, float scale, const void* plan, void* scratch, cudaStream_t s,
+                                   int* err, long long wait_cycles);
+
 }  // namespace gpt

@@ -17,6 +17,7 @@ enum : int {
   ERRF_TOKEN_RANGE = 1,   // a token or target id outside [0, vocab)
   ERRF_TIMEOUT = 2,       // a bounded wait on an mbarrier expired
   ERRF_SHAPE = 4,         // a launch saw a shape it cannot handle
+  ERRF_SEQUENCE = 8,      // sequence offsets out of order or past the buffers
 };
 
 // By default a wait gives up after this many SM clock cycles (about 2 s at

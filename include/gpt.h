@@ -370,7 +370,8 @@ const char* gpt_last_error(void);
 /* Synchronises the stream, then reports and clears the op-level error word
  * of the current device: GPT_ETIMEOUT if a bounded device wait of an
  * op-level call expired since the last check (that call's outputs are
- * invalid), GPT_OK otherwise.  The word is shared by every op-level call on
+ * invalid), GPT_ERANGE if target ids or sequence offsets were out of range,
+ * GPT_OK otherwise.  The word is shared by every op-level call on
  * the device, whatever its stream or thread. */
 int gpt_op_check(void* stream);
 
@@ -433,6 +434,119 @@ int gpt_op_attention_fwd_ex(const void* q, const void* k, const void* v, void* o
 int gpt_op_attention_bwd_ex(const void* q, const void* k, const void* v, const void* o, const void* dout,
                             const float* lse, float* Dscratch, float* dq, void* dk, void* dv, int B, int H, int Hkv,
                             int T, int window, void* stream);
+
+/* --------------------------------------------------------------------
+ * Fine-tuning on examples of different lengths (the pages' chat and
+ * preference stages name no kernels; these are this library's own calls):
+ * attention over sequences packed end to end, and two losses on logits.
+ * ------------------------------------------------------------------ */
+
+/* A [tokens, heads, 128] bf16 tensor on the device: any strides (in
+ * elements, multiples of 8) between tokens and between heads, the 128 dims
+ * contiguous, the base 16-byte aligned.  It may be head-major, token-major or
+ * a column slice of a fused projection's rows. */
+typedef struct gpt_heads {
+  void* data;
+  int64_t token_stride, head_stride;
+} gpt_heads;
+
+/* Plan of a batch of sequences for the packed attention calls.  Sequence s
+ * holds positions cu_seqlens[s] .. cu_seqlens[s + 1] - 1 of n_tokens
+ * (lengths of 0 are allowed); the positions past cu_seqlens[n_seq] belong to
+ * no sequence.  Query t sees the keys of its own sequence up to itself, and
+ * with window >= 0 only the last window + 1 of them.  One plan serves every
+ * layer, head count and direction of the batch, on any number of streams at
+ * once after this call has run; a new batch of the same n_tokens may be
+ * planned into the same buffer, also by replaying a captured graph.
+ *   cu_seqlens  device int32 [n_seq + 1]; it has to start at 0, not decrease
+ *               and end within n_tokens: otherwise the plan holds no
+ *               sequence, so the calls that use it write nothing, and
+ *               gpt_op_check reports GPT_ERANGE
+ *   plan        device buffer of gpt_op_attention_plan_bytes(n_tokens) bytes,
+ *               256-byte aligned */
+size_t gpt_op_attention_plan_bytes(int n_tokens);
+int gpt_op_attention_plan(const int32_t* cu_seqlens, int n_seq, int n_tokens, int window, void* plan, void* stream);
+
+/* Attention over the packed sequences of plan, forward: per query head h
+ * (kv head h / (H / Hkv)) o_t = sum_j softmax_j(scale q_t . k_j) v_j over the
+ * keys that t sees, and lse fp32 [H, n_tokens], the natural log of the
+ * softmax denominator.  Rows past the last sequence are neither read nor
+ * written.  Within a 128-position tile a NaN or infinity in k or v of one
+ * sequence may reach the others of the tile.
+ *   scale    > 0, or 0 for 1 / sqrt(128)
+ *   plan     made for the same n_tokens (another plan: nothing is written and
+ *            gpt_op_check reports it)
+ *   scratch  device buffer of gpt_op_attention_packed_scratch(n_tokens, H, 0)
+ *            bytes, 256-byte aligned, of this call alone while it runs */
+size_t gpt_op_attention_packed_scratch(int n_tokens, int H, int backward);
+int gpt_op_attention_packed_fwd(const gpt_heads* q, const gpt_heads* k, const gpt_heads* v, const gpt_heads* o,
+                                float* lse, int n_tokens, int H, int Hkv, float scale, const void* plan,
+                                void* scratch, void* stream);
+
+/* Its backward: gradients of q, k and v (bf16; dk and dv summed over the
+ * query heads of a kv head) from dout, with o and lse of the forward.  Sums
+ * are held in fp32; those of dq add up in no fixed order, so two runs may
+ * differ in its last bit.  scratch: gpt_op_attention_packed_scratch(n_tokens,
+ * H, 1) bytes.  Outputs must not overlap each other or the inputs. */
+int gpt_op_attention_packed_bwd(const gpt_heads* q, const gpt_heads* k, const gpt_heads* v, const gpt_heads* o,
+                                const float* lse, const gpt_heads* dout, const gpt_heads* dq, const gpt_heads* dk,
+                                const gpt_heads* dv, int n_tokens, int H, int Hkv, float scale, const void* plan,
+                                void* scratch, void* stream);
+
+/* Element types of logits. */
+enum { GPT_DTYPE_BF16 = 0, GPT_DTYPE_FP32 = 1 };
+
+/* Clipped policy loss with a KL term, and its gradient.  With lp[m] the
+ * log-probability of targets[m] under row m of the logits, r = exp(lp -
+ * old_logp), A = advantage and d = ref_logp - lp, a position's loss is
+ *   -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_coef (exp(d) - d - 1)
+ * and the loss is its sum over the counted positions times weight[m].
+ *   logits     [M, V] in dtype, row stride ld >= V elements; -inf allowed
+ *   targets    device int32 [M]; -1: the position is not counted.  Other ids
+ *              outside [0, V) are not counted either and latched as GPT_ERANGE
+ *   old_logp   fp32 [M], or NULL: the present ones (r = 1, with -A as the
+ *              derivative by lp)
+ *   ref_logp   fp32 [M], or NULL: no KL term (kl_coef must be 0)
+ *   advantage  fp32 [M];  weight  fp32 [M], 0: not counted
+ *   stats      fp32 [4]: the loss, and the weighted sums of the clipped
+ *              surrogate, of the KL estimate exp(d) - d - 1, and of 1 where
+ *              the clip holds
+ *   logp       fp32 [M]: lp, 0 where not counted
+ *   dlogits    [M, V] in dtype with row stride ld_d: the gradient of the loss
+ *              (rows not counted are zero, whatever their logits hold); may
+ *              be logits itself (ld_d = ld); NULL: no gradient
+ *   scratch    device buffer of gpt_op_policy_loss_scratch(M) bytes, 256-byte
+ *              aligned, of this call alone while it runs
+ * Log-probabilities, sums and scalars are held in 32 bits or more; results
+ * do not depend on the order in which rows are processed. */
+size_t gpt_op_policy_loss_scratch(int M);
+int gpt_op_policy_loss(const void* logits, int dtype, long long ld, const int32_t* targets, const float* old_logp,
+                       const float* ref_logp, const float* advantage, const float* weight, int M, int V,
+                       float clip_low, float clip_high, float kl_coef, float* stats, float* logp, void* dlogits,
+                       long long ld_d, void* scratch, void* stream);
+
+/* Preference loss over pairs of answers, and its gradient.  The rows hold
+ * 2 n_pairs sequences end to end (cu_seqlens as for gpt_op_attention_plan,
+ * ending within M), the chosen answer of pair i at 2 i, the rejected one at
+ * 2 i + 1.  With L_s the sum of the targets' log-probabilities over the
+ * counted positions of s and z_i = beta ((L_2i - ref_2i) - (L_2i+1 -
+ * ref_2i+1)), the loss is the mean over the pairs of
+ *   -(1 - label_smoothing) log sigmoid(z) - label_smoothing log sigmoid(-z).
+ *   logits, dtype, ld, targets, dlogits, ld_d   as for gpt_op_policy_loss
+ *   ref_logp   fp32 [2 n_pairs]: the reference model's sums (seq_logp of a
+ *              call on its logits with dlogits NULL), or NULL: zero
+ *   loss       fp32 [1];  margin  fp32 [n_pairs]: z
+ *   seq_logp   fp32 [2 n_pairs]: L;  logp  fp32 [M]: per position, 0 where
+ *              not counted
+ *   scratch    device buffer of gpt_op_preference_loss_scratch(M, n_pairs)
+ *              bytes, 256-byte aligned, of this call alone while it runs
+ * Rows past the last sequence are neither read nor written.  Bad offsets:
+ * nothing is written and gpt_op_check reports GPT_ERANGE. */
+size_t gpt_op_preference_loss_scratch(int M, int n_pairs);
+int gpt_op_preference_loss(const void* logits, int dtype, long long ld, const int32_t* targets,
+                           const int32_t* cu_seqlens, int n_pairs, const float* ref_logp, int M, int V, float beta,
+                           float label_smoothing, float* loss, float* margin, float* seq_logp, float* logp,
+                           void* dlogits, long long ld_d, void* scratch, void* stream);
 
 /* Embedding gradient ("¿Cómo Entrenar Tu Propio ChatGPT por $50?", section
  * "1. Modelo GPT": the token embedding x0 = wte[tok]; its gradient scatters
