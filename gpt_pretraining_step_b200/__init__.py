@@ -8,6 +8,7 @@ memory and the stream.  If the compiled library is missing the import of
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -467,40 +468,57 @@ def attention_bwd(q, k, v, o, lse, dout, window=-1, stream=None):
 
 
 # ------------------------------------------------ fine-tuning on packed sequences
+#
+# A tensor of another type, shape or device than the call takes would be read
+# out of range, so these calls check theirs.  They are made once per layer, on
+# batches that may be small: the checks compare plain integers and the stream
+# comes as a raw handle, which keeps a call to some ten microseconds of host time.
 
-def _given(name, t, dtype, shape, device, contiguous=True):
-    """A tensor argument's check; a wrong one would be read out of range."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or (contiguous
-                                                                                    and not t.is_contiguous()):
-        raise GptError(GPT_EINVAL, f"{name} must be a {'contiguous ' if contiguous else ''}{dtype} tensor "
-                                   f"{tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t
+def _refuse(name, t, want):
+    raise GptError(GPT_EINVAL, f"{name} must be {want}; got {t.dtype} {tuple(t.shape)} with strides {t.stride()} "
+                               f"on {t.device}")
 
 
-def _current_device(t, name):
-    """The device of t, which has to be the current one (its streams run the call)."""
+def _current(name, t):
+    """Index of t's device, which has to be the current one (its streams run the call)."""
     import torch
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
         raise GptError(GPT_EINVAL, f"{name} is on {t.device}, not on the current CUDA device")
-    return t.device
+    return dev
 
 
-def _on_stream(tensors, stream):
-    """Tensors made here are used on `stream`: their memory must not be given
-    out again on the current stream before that work has run."""
+def _flat(name, t, dtype, shape, dev):
+    """Address of a contiguous tensor argument."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(name, t, f"a contiguous {dtype} tensor {shape} on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _heads(name, t, n, heads, dev, bf16):
+    """gpt_heads of a [n, heads, 128] tensor argument."""
+    if t.dtype != bf16 or t.shape != (n, heads, 128) or t.get_device() != dev or t.stride(2) != 1:
+        _refuse(name, t, f"a bf16 tensor {(n, heads, 128)} with contiguous rows of 128 on cuda:{dev}")
+    return Heads(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _raw_stream(stream, dev, made=()):
+    """Handle of `stream` or of the current one.  Memory of the tensors made
+    for the call must not be given out again on the current stream before
+    another stream's work on it has run."""
     import torch
-    if stream is not None and stream.cuda_stream != torch.cuda.current_stream().cuda_stream:
-        for t in tensors:
-            t.record_stream(stream)
+    current = torch._C._cuda_getCurrentRawStream(dev)
+    if stream is None or stream.cuda_stream == current:
+        return current
+    for t in made:
+        t.record_stream(stream)
+    return stream.cuda_stream
 
 
-def _heads(name, t, n, device, heads=None):
-    import torch
-    if t.dim() != 3 or t.shape[2] != 128 or t.stride(2) != 1 or (heads and t.shape[1] != heads):
-        raise GptError(GPT_EINVAL, f"{name} must be [{n}, {heads or 'heads'}, 128] with contiguous dims, "
-                                   f"got {tuple(t.shape)}")
-    _given(name, t, torch.bfloat16, (n, t.shape[1], 128), device, contiguous=False)
-    return ctypes.byref(Heads(t.data_ptr(), t.stride(0), t.stride(1)))
+@functools.lru_cache(maxsize=256)
+def _bytes(query, *sizes):
+    """Size of a plan or scratch buffer (a pure function of its arguments)."""
+    return max(getattr(lib(), query)(*sizes), 256)
 
 
 class AttentionPlan:
@@ -508,22 +526,20 @@ class AttentionPlan:
 
     def __init__(self, cu_seqlens, n_tokens, window=-1, stream=None):
         import torch
-        dev = _current_device(cu_seqlens, "cu_seqlens")
-        self.n_tokens, self.window = int(n_tokens), int(window)
-        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
-            raise GptError(GPT_EINVAL, "cu_seqlens must be [sequences + 1]")
-        _given("cu_seqlens", cu_seqlens, torch.int32, cu_seqlens.shape, dev)
-        self.buf = torch.empty(max(lib().gpt_op_attention_plan_bytes(self.n_tokens), 256), dtype=torch.uint8,
-                               device=dev)
-        _on_stream([self.buf], stream)
+        self.n_tokens, self.window, self.device = int(n_tokens), int(window), _current("cu_seqlens", cu_seqlens)
+        self.buf = torch.empty(_bytes("gpt_op_attention_plan_bytes", self.n_tokens), dtype=torch.uint8,
+                               device=cu_seqlens.device)
         self.update(cu_seqlens, stream)
 
     def update(self, cu_seqlens, stream=None):
         """Plan another batch of the same n_tokens and window into the same buffer."""
         import torch
-        _given("cu_seqlens", cu_seqlens, torch.int32, (cu_seqlens.numel(),), self.buf.device)
-        _check(lib().gpt_op_attention_plan(_ptr(cu_seqlens), cu_seqlens.numel() - 1, self.n_tokens, self.window,
-                                           _ptr(self.buf), _stream(stream)))
+        n = cu_seqlens.numel()
+        if n < 1:
+            _refuse("cu_seqlens", cu_seqlens, "[sequences + 1]")
+        cu = _flat("cu_seqlens", cu_seqlens, torch.int32, (n,), self.device)
+        _check(lib().gpt_op_attention_plan(cu, n - 1, self.n_tokens, self.window, self.buf.data_ptr(),
+                                           _raw_stream(stream, self.device, (self.buf,))))
 
 
 def attention_plan(cu_seqlens, n_tokens, window=-1, stream=None):
@@ -539,18 +555,17 @@ def attention_packed_fwd(q, k, v, plan, scale=0.0, o=None, lse=None, stream=None
     [H, n_tokens], new unless given; rows past the last sequence keep what
     they held (new tensors: anything)."""
     import torch
-    n, dev = plan.n_tokens, _current_device(q, "q")
+    n, dev, bf16 = plan.n_tokens, _current("q", q), torch.bfloat16
     H, Hkv = q.shape[1], k.shape[1]
     if o is None:
-        o = torch.empty((n, H, 128), dtype=torch.bfloat16, device=dev)
+        o = torch.empty((n, H, 128), dtype=bf16, device=q.device)
     if lse is None:
-        lse = torch.empty((H, n), dtype=torch.float32, device=dev)
-    scratch = torch.empty(max(lib().gpt_op_attention_packed_scratch(n, H, 0), 256), dtype=torch.uint8, device=dev)
-    _on_stream([o, lse, scratch], stream)
+        lse = torch.empty((H, n), dtype=torch.float32, device=q.device)
+    scratch = torch.empty(_bytes("gpt_op_attention_packed_scratch", n, H, 0), dtype=torch.uint8, device=q.device)
     _check(lib().gpt_op_attention_packed_fwd(
-        _heads("q", q, n, dev), _heads("k", k, n, dev), _heads("v", v, n, dev, Hkv), _heads("o", o, n, dev, H),
-        _ptr(_given("lse", lse, torch.float32, (H, n), dev)), n, H, Hkv, scale, _ptr(plan.buf), _ptr(scratch),
-        _stream(stream)))
+        _heads("q", q, n, H, dev, bf16), _heads("k", k, n, Hkv, dev, bf16), _heads("v", v, n, Hkv, dev, bf16),
+        _heads("o", o, n, H, dev, bf16), _flat("lse", lse, torch.float32, (H, n), dev), n, H, Hkv, scale,
+        plan.buf.data_ptr(), scratch.data_ptr(), _raw_stream(stream, dev, (o, lse, scratch))))
     return o, lse
 
 
@@ -558,46 +573,52 @@ def attention_packed_bwd(q, k, v, o, lse, dout, plan, scale=0.0, dq=None, dk=Non
     """Gradients (bf16, shaped as q, k and v; new unless given) of
     attention_packed_fwd, from its o and lse and the gradient dout of o."""
     import torch
-    n, dev = plan.n_tokens, _current_device(q, "q")
+    n, dev, bf16 = plan.n_tokens, _current("q", q), torch.bfloat16
     H, Hkv = q.shape[1], k.shape[1]
-    dq, dk, dv = (torch.empty((n, h, 128), dtype=torch.bfloat16, device=dev) if t is None else t
-                  for t, h in ((dq, H), (dk, Hkv), (dv, Hkv)))
-    scratch = torch.empty(max(lib().gpt_op_attention_packed_scratch(n, H, 1), 256), dtype=torch.uint8, device=dev)
-    _on_stream([dq, dk, dv, scratch], stream)
+    if dq is None:
+        dq = torch.empty((n, H, 128), dtype=bf16, device=q.device)
+    if dk is None:
+        dk = torch.empty((n, Hkv, 128), dtype=bf16, device=q.device)
+    if dv is None:
+        dv = torch.empty((n, Hkv, 128), dtype=bf16, device=q.device)
+    scratch = torch.empty(_bytes("gpt_op_attention_packed_scratch", n, H, 1), dtype=torch.uint8, device=q.device)
     _check(lib().gpt_op_attention_packed_bwd(
-        _heads("q", q, n, dev), _heads("k", k, n, dev), _heads("v", v, n, dev, Hkv), _heads("o", o, n, dev, H),
-        _ptr(_given("lse", lse, torch.float32, (H, n), dev)), _heads("dout", dout, n, dev, H),
-        _heads("dq", dq, n, dev, H), _heads("dk", dk, n, dev, Hkv), _heads("dv", dv, n, dev, Hkv), n, H, Hkv, scale,
-        _ptr(plan.buf), _ptr(scratch), _stream(stream)))
+        _heads("q", q, n, H, dev, bf16), _heads("k", k, n, Hkv, dev, bf16), _heads("v", v, n, Hkv, dev, bf16),
+        _heads("o", o, n, H, dev, bf16), _flat("lse", lse, torch.float32, (H, n), dev),
+        _heads("dout", dout, n, H, dev, bf16), _heads("dq", dq, n, H, dev, bf16), _heads("dk", dk, n, Hkv, dev, bf16),
+        _heads("dv", dv, n, Hkv, dev, bf16), n, H, Hkv, scale, plan.buf.data_ptr(), scratch.data_ptr(),
+        _raw_stream(stream, dev, (dq, dk, dv, scratch))))
     return dq, dk, dv
 
 
-def _optional_ptr(t):
-    return None if t is None else _ptr(t)
+def _rows(name, t, dev):
+    """Row stride of a [M, V] tensor argument with contiguous rows."""
+    if t.dim() != 2 or t.get_device() != dev or (t.stride(1) != 1 and t.shape[1] > 1):
+        _refuse(name, t, f"[M, V] with contiguous rows on cuda:{dev}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
-def _loss_args(logits, targets, grad, dlogits):
-    """Checked (M, V, dtype code, row stride, gradient or None) of both losses."""
+def _loss_rows(logits, grad, dlogits):
+    """(M, V, dtype code, row stride, gradient or None, its address and row
+    stride, device) of both losses."""
     import torch
-    dev = _current_device(logits, "logits")
-    if logits.dim() != 2 or logits.dtype not in (torch.bfloat16, torch.float32) or (logits.shape[1] > 1
-                                                                                    and logits.stride(1) != 1):
-        raise GptError(GPT_EINVAL, "logits must be a [M, V] bf16 or fp32 tensor with contiguous rows")
+    dev = _current("logits", logits)
+    ld = _rows("logits", logits, dev)
     M, V = logits.shape
-    ld = logits.stride(0) if M > 1 else max(logits.stride(0), V)
-    _given("targets", targets, torch.int32, (M,), dev)
-    ld_d = ld
+    code = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}.get(logits.dtype)
+    if code is None:
+        _refuse("logits", logits, "bf16 or fp32")
     if not grad:
-        dlogits = None
-    elif dlogits is None:
+        return M, V, code, ld, None, None, ld, dev
+    ld_d = ld
+    if dlogits is None:
         # the rows' alignment follows the logits'
-        dlogits = torch.empty_strided((M, V), (ld, 1), dtype=logits.dtype, device=dev)
+        dlogits = torch.empty_strided((M, V), (ld, 1), dtype=logits.dtype, device=logits.device)
     else:
-        _given("dlogits", dlogits, logits.dtype, (M, V), dev, contiguous=False)
-        if V > 1 and dlogits.stride(1) != 1:
-            raise GptError(GPT_EINVAL, "dlogits must have contiguous rows")
-        ld_d = dlogits.stride(0) if M > 1 else max(dlogits.stride(0), V)
-    return M, V, DTYPE_FP32 if logits.dtype == torch.float32 else DTYPE_BF16, ld, dlogits, ld_d, dev
+        ld_d = _rows("dlogits", dlogits, dev)
+        if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype:
+            _refuse("dlogits", dlogits, f"{logits.dtype} {(M, V)}")
+    return M, V, code, ld, dlogits, dlogits.data_ptr(), ld_d, dev
 
 
 def policy_loss(logits, targets, old_logp, advantage, weight, ref_logp=None, kl_coef=0.0, clip_low=0.2,
@@ -611,18 +632,18 @@ def policy_loss(logits, targets, old_logp, advantage, weight, ref_logp=None, kl_
     and of the clipped positions; dlogits (None with grad=False) is new unless
     given, and may be logits itself."""
     import torch
-    M, V, code, ld, dlogits, ld_d, dev = _loss_args(logits, targets, grad, dlogits)
-    for name, t in (("old_logp", old_logp), ("advantage", advantage), ("weight", weight), ("ref_logp", ref_logp)):
-        if t is not None:
-            _given(name, t, torch.float32, (M,), dev)
-    stats = torch.empty(4, dtype=torch.float32, device=dev)
-    logp = torch.empty(M, dtype=torch.float32, device=dev)
-    scratch = torch.empty(max(lib().gpt_op_policy_loss_scratch(M), 256), dtype=torch.uint8, device=dev)
-    _on_stream([stats, logp, scratch] + ([dlogits] if grad else []), stream)
+    M, V, code, ld, dlogits, d, ld_d, dev = _loss_rows(logits, grad, dlogits)
+    f32 = torch.float32
+    stats = torch.empty(4, dtype=f32, device=logits.device)
+    logp = torch.empty(M, dtype=f32, device=logits.device)
+    scratch = torch.empty(_bytes("gpt_op_policy_loss_scratch", M), dtype=torch.uint8, device=logits.device)
     _check(lib().gpt_op_policy_loss(
-        _ptr(logits), code, ld, _ptr(targets), _optional_ptr(old_logp), _optional_ptr(ref_logp), _ptr(advantage),
-        _ptr(weight), M, V, clip_low, clip_high, kl_coef, _ptr(stats), _ptr(logp), _optional_ptr(dlogits), ld_d,
-        _ptr(scratch), _stream(stream)))
+        logits.data_ptr(), code, ld, _flat("targets", targets, torch.int32, (M,), dev),
+        None if old_logp is None else _flat("old_logp", old_logp, f32, (M,), dev),
+        None if ref_logp is None else _flat("ref_logp", ref_logp, f32, (M,), dev),
+        _flat("advantage", advantage, f32, (M,), dev), _flat("weight", weight, f32, (M,), dev), M, V, clip_low,
+        clip_high, kl_coef, stats.data_ptr(), logp.data_ptr(), d, ld_d, scratch.data_ptr(),
+        _raw_stream(stream, dev, (stats, logp, scratch) + ((dlogits,) if grad else ()))))
     return stats, logp, dlogits
 
 
@@ -635,23 +656,22 @@ def preference_loss(logits, targets, cu_seqlens, ref_logp=None, beta=0.1, label_
     Returns (loss [], margin [pairs], seq_logp [2 pairs], logp [M], dlogits);
     rows past the last sequence keep what they held (new tensors: anything)."""
     import torch
-    M, V, code, ld, dlogits, ld_d, dev = _loss_args(logits, targets, grad, dlogits)
-    n = cu_seqlens.numel() - 1
+    M, V, code, ld, dlogits, d, ld_d, dev = _loss_rows(logits, grad, dlogits)
+    n, f32 = cu_seqlens.numel() - 1, torch.float32
     if n < 2 or n % 2:
-        raise GptError(GPT_EINVAL, "cu_seqlens must be [2 * pairs + 1]")
-    _given("cu_seqlens", cu_seqlens, torch.int32, (n + 1,), dev)
-    if ref_logp is not None:
-        _given("ref_logp", ref_logp, torch.float32, (n,), dev)
-    loss = torch.empty((), dtype=torch.float32, device=dev)
-    margin = torch.empty(n // 2, dtype=torch.float32, device=dev)
-    seq_logp = torch.empty(n, dtype=torch.float32, device=dev)
-    logp = torch.empty(M, dtype=torch.float32, device=dev)
-    scratch = torch.empty(max(lib().gpt_op_preference_loss_scratch(M, n // 2), 256), dtype=torch.uint8, device=dev)
-    _on_stream([loss, margin, seq_logp, logp, scratch] + ([dlogits] if grad else []), stream)
+        _refuse("cu_seqlens", cu_seqlens, "[2 * pairs + 1]")
+    loss = torch.empty((), dtype=f32, device=logits.device)
+    margin = torch.empty(n // 2, dtype=f32, device=logits.device)
+    seq_logp = torch.empty(n, dtype=f32, device=logits.device)
+    logp = torch.empty(M, dtype=f32, device=logits.device)
+    scratch = torch.empty(_bytes("gpt_op_preference_loss_scratch", M, n // 2), dtype=torch.uint8,
+                          device=logits.device)
     _check(lib().gpt_op_preference_loss(
-        _ptr(logits), code, ld, _ptr(targets), _ptr(cu_seqlens), n // 2, _optional_ptr(ref_logp), M, V, beta,
-        label_smoothing, _ptr(loss), _ptr(margin), _ptr(seq_logp), _ptr(logp), _optional_ptr(dlogits), ld_d,
-        _ptr(scratch), _stream(stream)))
+        logits.data_ptr(), code, ld, _flat("targets", targets, torch.int32, (M,), dev),
+        _flat("cu_seqlens", cu_seqlens, torch.int32, (n + 1,), dev), n // 2,
+        None if ref_logp is None else _flat("ref_logp", ref_logp, f32, (n,), dev), M, V, beta, label_smoothing,
+        loss.data_ptr(), margin.data_ptr(), seq_logp.data_ptr(), logp.data_ptr(), d, ld_d, scratch.data_ptr(),
+        _raw_stream(stream, dev, (loss, margin, seq_logp, logp, scratch) + ((dlogits,) if grad else ()))))
     return loss, margin, seq_logp, logp, dlogits
 
 
