@@ -20,14 +20,23 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-constexpr int kRowThreads = 512;
-constexpr float kLog2e = 1.4426950408889634f;
+// A row is worked on by G threads (a whole block), kVecs 16-byte vectors of a
+// thread at a time: all loads of a batch are issued before the first value
+// is used, so that a block keeps up to 64 KB in flight.  A row of one batch
+// stays in the registers between its two passes; a longer one is read again,
+// from L2.
+constexpr int kVecs = 8;
+
+// log2(e) in two parts: with one, exp(d) is off by 1.3e-8 |d| in the same
+// direction for every value, which sums over a sequence's positions.
+constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float exp_sum(float d) { return ex2(fmaf(d, kLog2e, d * kLog2eLow)); }
 
 // 16 bytes of a row: 8 bf16 or 4 fp32 values
 template <typename T>
@@ -81,83 +90,128 @@ struct Softmax {
   __device__ __forceinline__ static float base(float m) { return m == -INFINITY ? 0.f : m; }
   __device__ __forceinline__ void raise(float to) {
     if (to > m) {
-      s *= ex2((m - to) * kLog2e);
+      s *= exp_sum(m - to);
       m = to;
     }
   }
   __device__ __forceinline__ void add(float x) {
     raise(x);
-    s += ex2((x - base(m)) * kLog2e);
+    s += exp_sum(x - base(m));
   }
   __device__ __forceinline__ void merge(float m2, float s2) {
     const float t = fmaxf(m, m2), b = base(t);
-    s = s * ex2((m - b) * kLog2e) + s2 * ex2((m2 - b) * kLog2e);
+    s = s * exp_sum(m - b) + s2 * exp_sum(m2 - b);
     m = t;
   }
 };
 
-// m and s over a whole row, for every thread of the block.
-template <typename T>
-__device__ __forceinline__ Softmax row_softmax(const T* __restrict__ x, int V, float2* red) {
-  Softmax a;
-  const RowParts<T> part(x, V);
-  if (static_cast<int>(threadIdx.x) < part.head) a.add(to_f(x[threadIdx.x]));
-  const uint4* xv = reinterpret_cast<const uint4*>(x + part.head);
-  for (int i = threadIdx.x; i < part.vecs; i += kRowThreads) {
-    float v[Vec<T>::n];
-    unpack<T>(xv[i], v);
-    float t = v[0];
+// The thread's share of a batch: vectors first + threadIdx.x + G k.
+template <int G>
+__device__ __forceinline__ void load_batch(const uint4* __restrict__ xv, int first, int vecs, uint4 (&w)[kVecs]) {
 #pragma unroll
-    for (int k = 1; k < Vec<T>::n; ++k) t = fmaxf(t, v[k]);
+  for (int k = 0; k < kVecs; ++k) {
+    const int i = first + k * G + static_cast<int>(threadIdx.x);
+    if (i < vecs) w[k] = __ldg(xv + i);
+  }
+}
+
+// m and s over a whole row, for every thread of the block.  With one batch
+// (vecs <= G kVecs) w keeps the row.
+template <typename T, int G>
+__device__ __forceinline__ Softmax row_softmax(const T* __restrict__ x, int V, const RowParts<T>& part,
+                                               uint4 (&w)[kVecs], float2* red) {
+  Softmax a;
+  const int tid = threadIdx.x;
+  const uint4* xv = reinterpret_cast<const uint4*>(x + part.head);
+  const int tail = part.head + part.vecs * Vec<T>::n + tid;
+  for (int first = 0; first < part.vecs; first += G * kVecs) {
+    load_batch<G>(xv, first, part.vecs, w);
+    float t = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      if (first + k * G + tid < part.vecs) {
+        float v[Vec<T>::n];
+        unpack<T>(w[k], v);
+#pragma unroll
+        for (int e = 0; e < Vec<T>::n; ++e) t = fmaxf(t, v[e]);
+      }
+    }
     a.raise(t);
     const float b = Softmax::base(a.m);
 #pragma unroll
-    for (int k = 0; k < Vec<T>::n; ++k) a.s += ex2((v[k] - b) * kLog2e);
+    for (int k = 0; k < kVecs; ++k) {
+      if (first + k * G + tid < part.vecs) {
+        float v[Vec<T>::n];
+        unpack<T>(w[k], v);
+#pragma unroll
+        for (int e = 0; e < Vec<T>::n; ++e) a.s += exp_sum(v[e] - b);
+      }
+    }
   }
-  const int tail = part.head + part.vecs * Vec<T>::n + threadIdx.x;
+  if (tid < part.head) a.add(to_f(x[tid]));
   if (tail < V) a.add(to_f(x[tail]));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     a.merge(__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o));
-  if (lane_id() == 0) red[warp_id()] = make_float2(a.m, a.s);
-  __syncthreads();
-  a = Softmax();
-  for (int w = 0; w < kRowThreads / 32; ++w) a.merge(red[w].x, red[w].y);
+  if constexpr (G > 32) {
+    if (lane_id() == 0) red[warp_id()] = make_float2(a.m, a.s);
+    __syncthreads();
+    const float2 q = red[lane_id() & (G / 32 - 1)];
+    a.m = q.x;
+    a.s = q.y;
+#pragma unroll
+    for (int o = G / 64; o > 0; o >>= 1)
+      a.merge(__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o));
+  }
   return a;
 }
 
-// dx = g (1[j = y] - p), p = exp(x - m) / s; d may be x.
-template <typename T>
-__device__ __forceinline__ void row_gradient(const T* x, T* d, int V, int y, float g, float m, float s) {
+// dx = g (1[j = y] - p), p = exp(x - m) / s; d may be x.  kHeld: w holds the
+// row (one batch), otherwise it is read again.
+template <typename T, int G>
+__device__ __forceinline__ void row_gradient(const T* x, T* d, int V, const RowParts<T>& part, bool held,
+                                             uint4 (&w)[kVecs], int y, float g, float m, float s) {
   const float b = Softmax::base(m), f = -g / s;
-  const RowParts<T> part(x, V);
-  auto one = [&](int j) { from_f(d + j, f * ex2((to_f(x[j]) - b) * kLog2e) + (j == y ? g : 0.f)); };
-  if (static_cast<int>(threadIdx.x) < part.head) one(threadIdx.x);
+  const int tid = threadIdx.x;
+  // the target's own value, after which no thread may have written it in place
+  auto value = [&](float v) { return f * ex2((v - b) * kLog2e); };
   const uint4* xv = reinterpret_cast<const uint4*>(x + part.head);
   const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(d)) & 15) == 0;
-  for (int i = threadIdx.x; i < part.vecs; i += kRowThreads) {
-    float v[Vec<T>::n];
-    unpack<T>(xv[i], v);
-    const int j0 = part.head + i * Vec<T>::n;
+  for (int first = 0; first < part.vecs; first += G * kVecs) {
+    if (!held) load_batch<G>(xv, first, part.vecs, w);
 #pragma unroll
-    for (int k = 0; k < Vec<T>::n; ++k) v[k] = f * ex2((v[k] - b) * kLog2e) + (j0 + k == y ? g : 0.f);
-    if (same) {
-      *reinterpret_cast<uint4*>(d + j0) = pack<T>(v);
-    } else {
+    for (int k = 0; k < kVecs; ++k) {
+      const int i = first + k * G + tid;
+      if (i < part.vecs) {
+        float v[Vec<T>::n];
+        unpack<T>(w[k], v);
+        const int j0 = part.head + i * Vec<T>::n;
 #pragma unroll
-      for (int k = 0; k < Vec<T>::n; ++k) from_f(d + j0 + k, v[k]);
+        for (int e = 0; e < Vec<T>::n; ++e) v[e] = value(v[e]);
+        if (static_cast<unsigned>(y - j0) < static_cast<unsigned>(Vec<T>::n)) {
+#pragma unroll
+          for (int e = 0; e < Vec<T>::n; ++e) v[e] += j0 + e == y ? g : 0.f;
+        }
+        if (same) {
+          *reinterpret_cast<uint4*>(d + j0) = pack<T>(v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < Vec<T>::n; ++e) from_f(d + j0 + e, v[e]);
+        }
+      }
     }
   }
-  const int tail = part.head + part.vecs * Vec<T>::n + threadIdx.x;
+  auto one = [&](int j) { from_f(d + j, value(to_f(x[j])) + (j == y ? g : 0.f)); };
+  if (tid < part.head) one(tid);
+  const int tail = part.head + part.vecs * Vec<T>::n + tid;
   if (tail < V) one(tail);
 }
 
-template <typename T>
+template <typename T, int G>
 __device__ __forceinline__ void row_zero(T* d, int V) {
   const RowParts<T> part(d, V);
   if (static_cast<int>(threadIdx.x) < part.head) from_f(d + threadIdx.x, 0.f);
-  for (int i = threadIdx.x; i < part.vecs; i += kRowThreads)
-    reinterpret_cast<uint4*>(d + part.head)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < part.vecs; i += G) reinterpret_cast<uint4*>(d + part.head)[i] = make_uint4(0, 0, 0, 0);
   const int tail = part.head + part.vecs * Vec<T>::n + threadIdx.x;
   if (tail < V) from_f(d + tail, 0.f);
 }
@@ -172,6 +226,21 @@ __device__ __forceinline__ int row_target(const LossRows& R, int r, int* err) {
   return y;
 }
 
+// log p_y from the row's statistics, in 64 bits (one thread's work): its sum
+// over a sequence is compared with sums of nearly the same size.
+__device__ __forceinline__ double target_logp(float x, const Softmax& a) {
+  return static_cast<double>(x) - Softmax::base(a.m) - log(static_cast<double>(a.s));
+}
+
+// Calls f with the threads a row of this many bytes is given: one batch where
+// it fits (512 threads at most; more would leave one block on an SM).
+template <typename F>
+void with_row_threads(long long row_bytes, F f) {
+  if (row_bytes <= 32 * kVecs * 16) f(std::integral_constant<int, 32>());
+  else if (row_bytes <= 128 * kVecs * 16) f(std::integral_constant<int, 128>());
+  else f(std::integral_constant<int, 512>());
+}
+
 // ------------------------------------------------------------ policy loss
 //
 // Per counted token: r = exp(lp - old), the surrogate -min(r A, clip(r, 1 -
@@ -184,8 +253,8 @@ struct PolicyRow {
   float g;
   float4 term;   // w times: loss, surrogate, k, clipped
 };
-__device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& a, int r, float lp32, float w32) {
-  const double lp = lp32, w = w32, adv = a.advantage[r];
+__device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& a, int r, double lp, float w32) {
+  const double w = w32, adv = a.advantage[r];
   const double ratio = a.old_logp ? exp(lp - a.old_logp[r]) : 1.0;
   const double lo = 1.0 - a.clip_low, hi = 1.0 + a.clip_high;
   const bool cut = adv >= 0.0 ? ratio > hi : ratio < lo;
@@ -203,34 +272,37 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& a, int r, floa
   return p;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads)
+template <typename T, int G>
+__global__ void __launch_bounds__(G, 1024 / G)
     policy_row_kernel(const LossRows R, const PolicyArgs a, float4* __restrict__ terms, int* err) {
-  __shared__ float2 red[kRowThreads / 32];
+  __shared__ float2 red[G / 32];
   __shared__ float gs;
   const int r = blockIdx.x;
   const T* x = static_cast<const T*>(R.logits) + r * R.ld;
   T* d = R.dlogits ? static_cast<T*>(R.dlogits) + r * R.ld_d : nullptr;
-  const float w = a.weight[r];
-  const int y = w == 0.f ? (row_target(R, r, err), -1) : row_target(R, r, err);
-  if (y < 0) {
+  const float wt = a.weight[r];
+  const int y = row_target(R, r, err);
+  if (y < 0 || wt == 0.f) {
     if (threadIdx.x == 0) {
       a.logp[r] = 0.f;
       terms[r] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    if (d) row_zero(d, R.V);
+    if (d) row_zero<T, G>(d, R.V);
     return;
   }
-  const Softmax sm = row_softmax(x, R.V, red);
+  uint4 w[kVecs];
+  const RowParts<T> part(x, R.V);
+  const float xy = threadIdx.x == 0 ? to_f(x[y]) : 0.f;
+  const Softmax sm = row_softmax<T, G>(x, R.V, part, w, red);
   if (threadIdx.x == 0) {
-    const float lp = (to_f(x[y]) - Softmax::base(sm.m)) - logf(sm.s);
-    const PolicyRow p = policy_row(a, r, lp, w);
-    a.logp[r] = lp;
+    const double lp = target_logp(xy, sm);
+    const PolicyRow p = policy_row(a, r, lp, wt);
+    a.logp[r] = static_cast<float>(lp);
     terms[r] = p.term;
     gs = p.g;
   }
   __syncthreads();
-  if (d) row_gradient(x, d, R.V, y, gs, sm.m, sm.s);
+  if (d) row_gradient<T, G>(x, d, R.V, part, part.vecs <= G * kVecs, w, y, gs, sm.m, sm.s);
 }
 
 // stats = sums of the rows' terms, in 64 bits and a fixed order
@@ -279,36 +351,45 @@ __device__ __forceinline__ int covered_rows(const PreferenceArgs& a, int M, int*
   return bad ? -1 : a.cu[n];
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads)
-    preference_logp_kernel(const LossRows R, const PreferenceArgs a, float2* __restrict__ ms, int* err) {
-  __shared__ float2 red[kRowThreads / 32];
+template <typename T, int G>
+__global__ void __launch_bounds__(G, 1024 / G)
+    preference_logp_kernel(const LossRows R, const PreferenceArgs a, float2* __restrict__ ms, double* __restrict__ lps,
+                           int* err) {
+  __shared__ float2 red[G / 32];
   const int rows = covered_rows(a, R.M, err);
   const int r = blockIdx.x;
   if (r >= rows) return;
   const T* x = static_cast<const T*>(R.logits) + r * R.ld;
   const int y = row_target(R, r, err);
   if (y < 0) {
-    if (threadIdx.x == 0) a.logp[r] = 0.f;
+    if (threadIdx.x == 0) {
+      a.logp[r] = 0.f;
+      lps[r] = 0.0;
+    }
     return;
   }
-  const Softmax sm = row_softmax(x, R.V, red);
+  uint4 w[kVecs];
+  const RowParts<T> part(x, R.V);
+  const float xy = threadIdx.x == 0 ? to_f(x[y]) : 0.f;
+  const Softmax sm = row_softmax<T, G>(x, R.V, part, w, red);
   if (threadIdx.x == 0) {
+    const double lp = target_logp(xy, sm);
     ms[r] = make_float2(sm.m, sm.s);
-    a.logp[r] = (to_f(x[y]) - Softmax::base(sm.m)) - logf(sm.s);
+    a.logp[r] = static_cast<float>(lp);
+    lps[r] = lp;
   }
 }
 
 // The sums, margins, loss and row factors (one per sequence); one block.
 __global__ void __launch_bounds__(1024)
-    preference_pair_kernel(const LossRows R, const PreferenceArgs a, double* __restrict__ sums,
-                           float* __restrict__ g) {
+    preference_pair_kernel(const LossRows R, const PreferenceArgs a, const double* __restrict__ lps,
+                           double* __restrict__ sums, float* __restrict__ g) {
   __shared__ double red[32];
   if (covered_rows(a, R.M, nullptr) < 0) return;
   const int n = 2 * a.n_pairs;
   for (int q = warp_id(); q < n; q += 32) {
     double s = 0.0;
-    for (int r = a.cu[q] + lane_id(); r < a.cu[q + 1]; r += 32) s += a.logp[r];
+    for (int r = a.cu[q] + lane_id(); r < a.cu[q + 1]; r += 32) s += lps[r];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane_id() == 0) {
@@ -352,8 +433,8 @@ __device__ __forceinline__ int row_sequence(const int* __restrict__ cu, int n, i
   return l;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads)
+template <typename T, int G>
+__global__ void __launch_bounds__(G, 1024 / G)
     preference_grad_kernel(const LossRows R, const PreferenceArgs a, const float2* __restrict__ ms,
                            const float* __restrict__ g) {
   const int r = blockIdx.x;
@@ -361,12 +442,13 @@ __global__ void __launch_bounds__(kRowThreads)
   T* d = static_cast<T*>(R.dlogits) + r * R.ld_d;
   const int y = row_target(R, r, nullptr);
   if (y < 0) {
-    row_zero(d, R.V);
+    row_zero<T, G>(d, R.V);
     return;
   }
+  uint4 w[kVecs];
+  const T* x = static_cast<const T*>(R.logits) + r * R.ld;
   const float2 q = ms[r];
-  row_gradient(static_cast<const T*>(R.logits) + r * R.ld, d, R.V, y, g[row_sequence(a.cu, 2 * a.n_pairs, r)], q.x,
-               q.y);
+  row_gradient<T, G>(x, d, R.V, RowParts<T>(x, R.V), false, w, y, g[row_sequence(a.cu, 2 * a.n_pairs, r)], q.x, q.y);
 }
 
 constexpr size_t al256(size_t x) { return (x + 255) / 256 * 256; }
@@ -376,36 +458,54 @@ constexpr size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 size_t policy_loss_scratch(int M) { return al256(static_cast<size_t>(M) * sizeof(float4)) + 256; }
 
 size_t preference_loss_scratch(int M, int n_pairs) {
-  return al256(static_cast<size_t>(M) * sizeof(float2)) + al256(2 * static_cast<size_t>(n_pairs) * sizeof(double)) +
+  return al256(static_cast<size_t>(M) * sizeof(float2)) + al256(static_cast<size_t>(M) * sizeof(double)) +
+         al256(2 * static_cast<size_t>(n_pairs) * sizeof(double)) +
          al256(2 * static_cast<size_t>(n_pairs) * sizeof(float));
+}
+
+template <typename T>
+static void policy_rows(const LossRows& r, const PolicyArgs& a, float4* terms, int* err, cudaStream_t s) {
+  with_row_threads(1ll * r.V * sizeof(T), [&](auto g) {
+    constexpr int G = decltype(g)::value;
+    policy_row_kernel<T, G><<<r.M, G, 0, s>>>(r, a, terms, err);
+  });
 }
 
 cudaError_t launch_policy_loss(const LossRows& r, const PolicyArgs& a, void* scratch, int* err, cudaStream_t s) {
   float4* terms = static_cast<float4*>(scratch);
   if (r.M > 0) {
-    if (r.fp32) policy_row_kernel<float><<<r.M, kRowThreads, 0, s>>>(r, a, terms, err);
-    else policy_row_kernel<bf16><<<r.M, kRowThreads, 0, s>>>(r, a, terms, err);
+    if (r.fp32) policy_rows<float>(r, a, terms, err, s);
+    else policy_rows<bf16>(r, a, terms, err, s);
   }
   policy_sum_kernel<<<1, 1024, 0, s>>>(terms, r.M, a.stats);
   return cudaGetLastError();
 }
 
+template <typename T>
+static void preference_rows(const LossRows& r, const PreferenceArgs& a, void* scratch, int* err, cudaStream_t s) {
+  uint8_t* base = static_cast<uint8_t*>(scratch);
+  auto take = [&](size_t bytes) {
+    uint8_t* p = base;
+    base += al256(bytes);
+    return p;
+  };
+  float2* ms = reinterpret_cast<float2*>(take(static_cast<size_t>(r.M) * sizeof(float2)));
+  double* lps = reinterpret_cast<double*>(take(static_cast<size_t>(r.M) * sizeof(double)));
+  double* sums = reinterpret_cast<double*>(take(2 * static_cast<size_t>(a.n_pairs) * sizeof(double)));
+  float* g = reinterpret_cast<float*>(take(2 * static_cast<size_t>(a.n_pairs) * sizeof(float)));
+  with_row_threads(1ll * r.V * sizeof(T), [&](auto gs) {
+    constexpr int G = decltype(gs)::value;
+    // with no rows one block still checks the offsets
+    preference_logp_kernel<T, G><<<std::max(r.M, 1), G, 0, s>>>(r, a, ms, lps, err);
+    preference_pair_kernel<<<1, 1024, 0, s>>>(r, a, lps, sums, g);
+    if (r.dlogits && r.M > 0) preference_grad_kernel<T, G><<<r.M, G, 0, s>>>(r, a, ms, g);
+  });
+}
+
 cudaError_t launch_preference_loss(const LossRows& r, const PreferenceArgs& a, void* scratch, int* err,
                                    cudaStream_t s) {
-  uint8_t* base = static_cast<uint8_t*>(scratch);
-  float2* ms = reinterpret_cast<float2*>(base);
-  base += al256(static_cast<size_t>(r.M) * sizeof(float2));
-  double* sums = reinterpret_cast<double*>(base);
-  base += al256(2 * static_cast<size_t>(a.n_pairs) * sizeof(double));
-  float* g = reinterpret_cast<float*>(base);
-  const int grid = std::max(r.M, 1);   // with no rows one block still checks the offsets
-  if (r.fp32) preference_logp_kernel<float><<<grid, kRowThreads, 0, s>>>(r, a, ms, err);
-  else preference_logp_kernel<bf16><<<grid, kRowThreads, 0, s>>>(r, a, ms, err);
-  preference_pair_kernel<<<1, 1024, 0, s>>>(r, a, sums, g);
-  if (r.dlogits && r.M > 0) {
-    if (r.fp32) preference_grad_kernel<float><<<r.M, kRowThreads, 0, s>>>(r, a, ms, g);
-    else preference_grad_kernel<bf16><<<r.M, kRowThreads, 0, s>>>(r, a, ms, g);
-  }
+  if (r.fp32) preference_rows<float>(r, a, scratch, err, s);
+  else preference_rows<bf16>(r, a, scratch, err, s);
   return cudaGetLastError();
 }
 
