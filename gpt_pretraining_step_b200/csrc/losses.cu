@@ -12,6 +12,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "gemm.h"
 #include "losses.cuh"
 
 namespace gpt {
@@ -20,12 +21,12 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-// A row is worked on by G threads (a whole block), kVecs 16-byte vectors of a
-// thread at a time: all loads of a batch are issued before the first value
-// is used, so that a block keeps up to 64 KB in flight.  A row of one batch
-// stays in the registers between its two passes; a longer one is read again,
-// from L2.
-constexpr int kVecs = 8;
+// A block of G threads works on a row, in pieces of two 16-byte vectors a
+// thread that asynchronous copies bring to a ring of S pieces in shared
+// memory.  Each thread reads only what it copied itself, so that the ring
+// needs no barrier.  A row of at most S pieces stays there for a second pass;
+// of a longer one the last S do, and the others come again, mostly from L2.
+constexpr int kVecs = 2;   // vectors of a thread in a piece
 
 // log2(e) in two parts: with one, exp(d) is off by 1.3e-8 |d| in the same
 // direction for every value, which sums over a sequence's positions.
@@ -38,10 +39,24 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ float exp_sum(float d) { return ex2(fmaf(d, kLog2e, d * kLog2eLow)); }
 
+__device__ __forceinline__ void copy_async16(uint4* dst, const uint4* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {   // all but the last N groups have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // 16 bytes of a row: 8 bf16 or 4 fp32 values
 template <typename T>
 struct Vec {
   static constexpr int n = 16 / sizeof(T);
+  // every value -inf
+  __device__ __forceinline__ static uint4 lowest() {
+    const uint32_t u = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+    return make_uint4(u, u, u, u);
+  }
 };
 template <typename T>
 __device__ __forceinline__ void unpack(const uint4& w, float (&v)[Vec<T>::n]) {
@@ -71,8 +86,8 @@ __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ void from_f(bf16* p, float x) { *p = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void from_f(float* p, float x) { *p = x; }
 
-// A row in three parts: `head` values before the first 16-byte boundary,
-// `vecs` 16-byte vectors, and a tail.
+// V values from x on in three stretches: `head` values before the first
+// 16-byte boundary, `vecs` 16-byte vectors, and a tail.
 template <typename T>
 struct RowParts {
   int head, vecs;
@@ -98,113 +113,182 @@ struct Softmax {
     raise(x);
     s += exp_sum(x - base(m));
   }
-  __device__ __forceinline__ void merge(float m2, float s2) {
-    const float t = fmaxf(m, m2), b = base(t);
-    s = s * exp_sum(m - b) + s2 * exp_sum(m2 - b);
-    m = t;
+  // N vectors of 16 bytes
+  template <typename T, int N>
+  __device__ __forceinline__ void add(const uint4 (&w)[N]) {
+    constexpr int n = Vec<T>::n;
+    float v[N][n], t = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      unpack<T>(w[k], v[k]);
+#pragma unroll
+      for (int e = 0; e < n; e += 2) t = fmax3(t, v[k][e], v[k][e + 1]);
+    }
+    raise(t);
+    const float b = base(m);
+    const uint64_t nb = f2_pack(-b, -b), hi = f2_pack(kLog2e, kLog2e), lo = f2_pack(kLog2eLow, kLog2eLow);
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+#pragma unroll
+      for (int e = 0; e < n; e += 2) {
+#ifdef SCALAR
+        const float d0 = v[k][e] - b, d1 = v[k][e + 1] - b;
+        const float x0 = fmaf(d0, kLog2e, d0 * kLog2eLow), x1 = fmaf(d1, kLog2e, d1 * kLog2eLow);
+#else
+        const uint64_t d = f2_add(f2_pack(v[k][e], v[k][e + 1]), nb);
+        float x0, x1;
+        f2_unpack(f2_fma(d, hi, f2_mul(d, lo)), x0, x1);
+#endif
+        sum[e & 2] += ex2(x0);
+        sum[(e & 2) + 1] += ex2(x1);
+      }
+    }
+    s += (sum[0] + sum[1]) + (sum[2] + sum[3]);
   }
 };
 
-// The thread's share of a batch: vectors first + threadIdx.x + G k.
-template <int G>
-__device__ __forceinline__ void load_batch(const uint4* __restrict__ xv, int first, int vecs, uint4 (&w)[kVecs]) {
-#pragma unroll
-  for (int k = 0; k < kVecs; ++k) {
-    const int i = first + k * G + static_cast<int>(threadIdx.x);
-    if (i < vecs) w[k] = __ldg(xv + i);
-  }
+__device__ __forceinline__ float warp_max_redux(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// m and s over a whole row, for every thread of the block.  With one batch
-// (vecs <= G kVecs) w keeps the row.
-template <typename T, int G>
-__device__ __forceinline__ Softmax row_softmax(const T* __restrict__ x, int V, const RowParts<T>& part,
-                                               uint4 (&w)[kVecs], float2* red) {
-  Softmax a;
-  const int tid = threadIdx.x;
-  const uint4* xv = reinterpret_cast<const uint4*>(x + part.head);
-  const int tail = part.head + part.vecs * Vec<T>::n + tid;
-  for (int first = 0; first < part.vecs; first += G * kVecs) {
-    load_batch<G>(xv, first, part.vecs, w);
-    float t = -INFINITY;
+template <typename T, int G, int S>
+struct RowRing {
+  static constexpr int kPiece = G * kVecs;   // vectors
+  const T* x;
+  int V, head, vecs, pieces;
+  uint4* ring;
+  __device__ RowRing(const T* x_, int V_, uint4* ring_) : x(x_), V(V_), ring(ring_) {
+    const RowParts<T> row(x, V);
+    head = row.head;
+    vecs = row.vecs;
+    pieces = (vecs + kPiece - 1) / kPiece;
+  }
+  __device__ __forceinline__ void fetch(int u) const {
+    const uint4* xv = reinterpret_cast<const uint4*>(x + head);
+    const int i = (u < pieces ? u : u - pieces) * kPiece + static_cast<int>(threadIdx.x);
+    uint4* to = ring + u % S * kPiece + threadIdx.x;
 #pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-      if (first + k * G + tid < part.vecs) {
-        float v[Vec<T>::n];
-        unpack<T>(w[k], v);
+    for (int k = 0; k < kVecs; ++k)
+      if (i + k * G < vecs) copy_async16(to + k * G, xv + i + k * G);
+  }
+  // Calls one(j) for the values outside the vectors and piece(i, slot, full)
+  // for steps u0 .. u0 + pieces - 1, step u being piece u mod pieces: i is the
+  // thread's first vector of the piece, at slot, the others follow at steps of
+  // G; full: all are within the row.  held: the first S steps are in the
+  // ring already.
+  template <typename One, typename Piece>
+  __device__ __forceinline__ void pass(int u0, bool held, One one, Piece piece) const {
+    const int end = u0 + pieces, tid = threadIdx.x;
+    if (!held) {
 #pragma unroll
-        for (int e = 0; e < Vec<T>::n; ++e) t = fmaxf(t, v[e]);
+      for (int k = 0; k < S; ++k) {
+        if (u0 + k < end) fetch(u0 + k);
+        copy_commit();
       }
     }
-    a.raise(t);
-    const float b = Softmax::base(a.m);
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-      if (first + k * G + tid < part.vecs) {
-        float v[Vec<T>::n];
-        unpack<T>(w[k], v);
-#pragma unroll
-        for (int e = 0; e < Vec<T>::n; ++e) a.s += exp_sum(v[e] - b);
-      }
+    if (tid < head) one(tid);
+    const int tail = head + vecs * Vec<T>::n + tid;
+    if (tail < V) one(tail);
+    for (int u = u0; u < end; ++u) {
+      copy_wait<S - 1>();
+      const int first = (u < pieces ? u : u - pieces) * kPiece;
+      const uint4* slot = ring + u % S * kPiece + tid;
+      if (first + kPiece <= vecs) piece(first + tid, slot, std::true_type());
+      else piece(first + tid, slot, std::false_type());
+      if (u + S < end) fetch(u + S);
+      copy_commit();
     }
   }
-  if (tid < part.head) a.add(to_f(x[tid]));
-  if (tail < V) a.add(to_f(x[tail]));
+  // first step of a second pass: that of the oldest piece in the ring
+  __device__ __forceinline__ int again() const { return max(0, pieces - S); }
+};
+
+// m and s over the row, for every thread of the block.
+template <typename T, int G, int S>
+__device__ __forceinline__ Softmax row_softmax(const RowRing<T, G, S>& row, float2* red) {
+  Softmax a;
+  row.pass(
+      0, false, [&](int j) { a.add(to_f(row.x[j])); },
+      [&](int i, const uint4* slot, auto full) {
+        uint4 w[kVecs];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    a.merge(__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o));
+        for (int k = 0; k < kVecs; ++k)
+          w[k] = decltype(full)::value || i + k * G < row.vecs ? slot[k * G] : Vec<T>::lowest();
+        a.add<T>(w);
+      });
+  // over the warp, then over the warps
+  a.raise(warp_max_redux(a.m));
+  a.s = warp_sum(a.s);
   if constexpr (G > 32) {
     if (lane_id() == 0) red[warp_id()] = make_float2(a.m, a.s);
     __syncthreads();
     const float2 q = red[lane_id() & (G / 32 - 1)];
     a.m = q.x;
     a.s = q.y;
+    a.raise(warp_max_redux(a.m));
 #pragma unroll
-    for (int o = G / 64; o > 0; o >>= 1)
-      a.merge(__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o));
+    for (int o = G / 64; o > 0; o >>= 1) a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
   }
   return a;
 }
 
-// dx = g (1[j = y] - p), p = exp(x - m) / s; d may be x.  kHeld: w holds the
-// row (one batch), otherwise it is read again.
-template <typename T, int G>
-__device__ __forceinline__ void row_gradient(const T* x, T* d, int V, const RowParts<T>& part, bool held,
-                                             uint4 (&w)[kVecs], int y, float g, float m, float s) {
-  const float b = Softmax::base(m), f = -g / s;
-  const int tid = threadIdx.x;
-  // the target's own value, after which no thread may have written it in place
-  auto value = [&](float v) { return f * ex2((v - b) * kLog2e); };
-  const uint4* xv = reinterpret_cast<const uint4*>(x + part.head);
-  const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(d)) & 15) == 0;
-  for (int first = 0; first < part.vecs; first += G * kVecs) {
-    if (!held) load_batch<G>(xv, first, part.vecs, w);
+// The gradient g (1[j = y] - p), p = exp(x - m) / s, of one row.
+template <typename T>
+struct Gradient {
+  int y;
+  float xy, g, f, b;   // xy: the target's logit
+  __device__ Gradient(int y_, float xy_, float g_, float m, float s)
+      : y(y_), xy(xy_), g(g_), f(-g_ / s), b(Softmax::base(m)) {}
+  __device__ __forceinline__ float value(float x) const { return f * ex2((x - b) * kLog2e); }
+  __device__ __forceinline__ void one(const T* x, T* d, int j) const {
+    from_f(d + j, value(to_f(x[j])) + (j == y ? g : 0.f));
+  }
+  // a vector's values but for the target's g, to d
+  template <bool kWide>
+  __device__ __forceinline__ void vec(const uint4& w, T* d) const {
+    constexpr int n = Vec<T>::n;
+    float v[n];
+    unpack<T>(w, v);
+    const uint64_t nb = f2_pack(-b, -b), c = f2_pack(kLog2e, kLog2e), ff = f2_pack(f, f);
 #pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-      const int i = first + k * G + tid;
-      if (i < part.vecs) {
-        float v[Vec<T>::n];
-        unpack<T>(w[k], v);
-        const int j0 = part.head + i * Vec<T>::n;
+    for (int e = 0; e < n; e += 2) {
+      float x0, x1;
+      f2_unpack(f2_mul(f2_add(f2_pack(v[e], v[e + 1]), nb), c), x0, x1);
+      f2_unpack(f2_mul(f2_pack(ex2(x0), ex2(x1)), ff), v[e], v[e + 1]);
+    }
+    if constexpr (kWide) {
+      *reinterpret_cast<uint4*>(d) = pack<T>(v);
+    } else {
 #pragma unroll
-        for (int e = 0; e < Vec<T>::n; ++e) v[e] = value(v[e]);
-        if (static_cast<unsigned>(y - j0) < static_cast<unsigned>(Vec<T>::n)) {
-#pragma unroll
-          for (int e = 0; e < Vec<T>::n; ++e) v[e] += j0 + e == y ? g : 0.f;
-        }
-        if (same) {
-          *reinterpret_cast<uint4*>(d + j0) = pack<T>(v);
-        } else {
-#pragma unroll
-          for (int e = 0; e < Vec<T>::n; ++e) from_f(d + j0 + e, v[e]);
-        }
-      }
+      for (int e = 0; e < n; ++e) from_f(d + e, v[e]);
     }
   }
-  auto one = [&](int j) { from_f(d + j, value(to_f(x[j])) + (j == y ? g : 0.f)); };
-  if (tid < part.head) one(tid);
-  const int tail = part.head + part.vecs * Vec<T>::n + tid;
-  if (tail < V) one(tail);
+};
+
+// The row's gradient; d may be x.  held: after row_softmax.
+template <typename T, int G, int S>
+__device__ __forceinline__ void row_gradient(const RowRing<T, G, S>& row, T* d, bool held, const Gradient<T>& grad) {
+  constexpr int n = Vec<T>::n;
+  auto all = [&](auto wide) {
+    row.pass(
+        held ? row.again() : 0, held, [&](int j) { grad.one(row.x, d, j); },
+        [&](int i, const uint4* slot, auto full) {
+          T* to = d + row.head + i * n;
+#pragma unroll
+          for (int k = 0; k < kVecs; ++k)
+            if (decltype(full)::value || i + k * G < row.vecs)
+              grad.template vec<decltype(wide)::value>(slot[k * G], to + k * G * n);
+        });
+  };
+  if (((reinterpret_cast<uintptr_t>(row.x) ^ reinterpret_cast<uintptr_t>(d)) & 15) == 0) all(std::true_type());
+  else all(std::false_type());
+  // the target's value again, by the thread that wrote its vector
+  const int at = grad.y - row.head;
+  if (at >= 0 && at < row.vecs * n && at / n % G == static_cast<int>(threadIdx.x))
+    from_f(d + grad.y, grad.value(grad.xy) + grad.g);
 }
 
 template <typename T, int G>
@@ -220,7 +304,7 @@ __device__ __forceinline__ void row_zero(T* d, int V) {
 __device__ __forceinline__ int row_target(const LossRows& R, int r, int* err) {
   const int y = R.targets[r];
   if (y < -1 || y >= R.V) {
-    if (threadIdx.x == 0 && err) atomicOr(err, ERRF_TOKEN_RANGE);
+    if (err) atomicOr(err, ERRF_TOKEN_RANGE);
     return -1;
   }
   return y;
@@ -232,13 +316,26 @@ __device__ __forceinline__ double target_logp(float x, const Softmax& a) {
   return static_cast<double>(x) - Softmax::base(a.m) - log(static_cast<double>(a.s));
 }
 
-// Calls f with the threads a row of this many bytes is given: one batch where
-// it fits (512 threads at most; more would leave one block on an SM).
-template <typename F>
-void with_row_threads(long long row_bytes, F f) {
-  if (row_bytes <= 32 * kVecs * 16) f(std::integral_constant<int, 32>());
-  else if (row_bytes <= 128 * kVecs * 16) f(std::integral_constant<int, 128>());
-  else f(std::integral_constant<int, 512>());
+// Launches pick(G, S) over the rows.  G follows the row's bytes: 8 vectors of
+// a thread at 64 KB, fewer threads where a row would leave most of them idle.
+template <typename T, int S, typename Pick, typename... Args>
+cudaError_t launch_rows(const LossRows& r, cudaStream_t s, Pick pick, Args... args) {
+  const long long bytes = 1ll * r.V * sizeof(T);
+  auto launch = [&](auto kG) -> cudaError_t {
+    constexpr int G = decltype(kG)::value, kPieceBytes = G * kVecs * 16;
+    auto kern = pick(kG, std::integral_constant<int, S>());
+    const int slots = static_cast<int>(std::min<long long>((bytes + kPieceBytes - 1) / kPieceBytes, S));
+    if constexpr (S * kPieceBytes > 47 * 1024) {   // with the static words, over the default limit
+      static std::atomic<unsigned long long> configured{0};
+      const cudaError_t e = set_smem_limit_once(kern, S * kPieceBytes, configured);
+      if (e != cudaSuccess) return e;
+    }
+    kern<<<std::max(r.M, 1), G, slots * kPieceBytes, s>>>(args...);
+    return cudaGetLastError();
+  };
+  if (bytes <= 4096) return launch(std::integral_constant<int, 32>());
+  if (bytes <= 16384) return launch(std::integral_constant<int, 128>());
+  return launch(std::integral_constant<int, 512>());
 }
 
 // ------------------------------------------------------------ policy loss
@@ -272,9 +369,10 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& a, int r, doub
   return p;
 }
 
-template <typename T, int G>
-__global__ void __launch_bounds__(G, 1024 / G)
+template <typename T, int G, int S>
+__global__ void __launch_bounds__(G)
     policy_row_kernel(const LossRows R, const PolicyArgs a, float4* __restrict__ terms, int* err) {
+  extern __shared__ uint4 ring[];
   __shared__ float2 red[G / 32];
   __shared__ float gs;
   const int r = blockIdx.x;
@@ -290,10 +388,9 @@ __global__ void __launch_bounds__(G, 1024 / G)
     if (d) row_zero<T, G>(d, R.V);
     return;
   }
-  uint4 w[kVecs];
-  const RowParts<T> part(x, R.V);
-  const float xy = threadIdx.x == 0 ? to_f(x[y]) : 0.f;
-  const Softmax sm = row_softmax<T, G>(x, R.V, part, w, red);
+  const RowRing<T, G, S> row(x, R.V, ring);
+  const float xy = to_f(x[y]);
+  const Softmax sm = row_softmax(row, red);
   if (threadIdx.x == 0) {
     const double lp = target_logp(xy, sm);
     const PolicyRow p = policy_row(a, r, lp, wt);
@@ -301,8 +398,9 @@ __global__ void __launch_bounds__(G, 1024 / G)
     terms[r] = p.term;
     gs = p.g;
   }
+  if (!d) return;
   __syncthreads();
-  if (d) row_gradient<T, G>(x, d, R.V, part, part.vecs <= G * kVecs, w, y, gs, sm.m, sm.s);
+  row_gradient(row, d, true, Gradient<T>(y, xy, gs, sm.m, sm.s));
 }
 
 // stats = sums of the rows' terms, in 64 bits and a fixed order
@@ -340,68 +438,93 @@ __global__ void __launch_bounds__(1024) policy_sum_kernel(const float4* __restri
 // the row factor g of every counted position of the sequence.
 // L, R and z are sums and differences of large numbers: 64 bits.
 
-// Whether the offsets start at 0, do not decrease and end within M rows; the
-// rows they cover.
-__device__ __forceinline__ int covered_rows(const PreferenceArgs& a, int M, int* err) {
-  const int n = 2 * a.n_pairs;
-  int bad = a.cu[0] != 0 || a.cu[n] > M;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) bad |= a.cu[i + 1] < a.cu[i];
-  bad = __syncthreads_or(bad);
-  if (bad && blockIdx.x == 0 && threadIdx.x == 0 && err) atomicOr(err, ERRF_SEQUENCE);
-  return bad ? -1 : a.cu[n];
-}
+// Rows that the sequences cover, if their offsets are in order.
+__device__ __forceinline__ int last_row(const PreferenceArgs& a, int M) { return min(a.cu[2 * a.n_pairs], M); }
 
-template <typename T, int G>
-__global__ void __launch_bounds__(G, 1024 / G)
+// Words that the kernels of a call share: blocks of the sums' kernel that are
+// done, and the rows that the sequences cover (0 if their offsets are bad).
+struct PairWords {
+  int done, rows;
+};
+
+// Statistics and log-probability of every row, into scratch alone: whether
+// the offsets are in order is for the next kernel to say.
+template <typename T, int G, int S>
+__global__ void __launch_bounds__(G)
     preference_logp_kernel(const LossRows R, const PreferenceArgs a, float2* __restrict__ ms, double* __restrict__ lps,
-                           int* err) {
+                           PairWords* words) {
+  extern __shared__ uint4 ring[];
   __shared__ float2 red[G / 32];
-  const int rows = covered_rows(a, R.M, err);
   const int r = blockIdx.x;
-  if (r >= rows) return;
+  if (r == 0 && threadIdx.x == 0) words->done = 0;
+  if (r >= R.M) return;
+  const int y = R.targets[r];
+  if (r >= last_row(a, R.M) || y < 0 || y >= R.V) return;
   const T* x = static_cast<const T*>(R.logits) + r * R.ld;
-  const int y = row_target(R, r, err);
-  if (y < 0) {
-    if (threadIdx.x == 0) {
-      a.logp[r] = 0.f;
-      lps[r] = 0.0;
-    }
-    return;
-  }
-  uint4 w[kVecs];
-  const RowParts<T> part(x, R.V);
   const float xy = threadIdx.x == 0 ? to_f(x[y]) : 0.f;
-  const Softmax sm = row_softmax<T, G>(x, R.V, part, w, red);
+  const Softmax sm = row_softmax(RowRing<T, G, S>(x, R.V, ring), red);
   if (threadIdx.x == 0) {
-    const double lp = target_logp(xy, sm);
     ms[r] = make_float2(sm.m, sm.s);
-    a.logp[r] = static_cast<float>(lp);
-    lps[r] = lp;
+    lps[r] = target_logp(xy, sm);
   }
 }
 
-// The sums, margins, loss and row factors (one per sequence); one block.
-__global__ void __launch_bounds__(1024)
-    preference_pair_kernel(const LossRows R, const PreferenceArgs a, const double* __restrict__ lps,
-                           double* __restrict__ sums, float* __restrict__ g) {
-  __shared__ double red[32];
-  if (covered_rows(a, R.M, nullptr) < 0) return;
-  const int n = 2 * a.n_pairs;
-  for (int q = warp_id(); q < n; q += 32) {
-    double s = 0.0;
-    for (int r = a.cu[q] + lane_id(); r < a.cu[q + 1]; r += 32) s += lps[r];
+// Checks the offsets: from 0, not decreasing, ending within the rows.  Then
+// each block adds up some sequences (a block for a sequence where there are
+// few: with a warp for each, long ones took 15 us), and the last one to finish
+// computes the margins, the loss and the row factors (one per sequence).  The
+// order of every sum is fixed.
+constexpr int kSumThreads = 256;
+__device__ __forceinline__ double block_sum(double s, double* red) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane_id() == 0) {
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  __syncthreads();
+  if (lane_id() == 0) red[warp_id()] = s;
+  __syncthreads();
+  double t = 0.0;
+#pragma unroll
+  for (int w = 0; w < kSumThreads / 32; ++w) t += red[w];
+  return t;
+}
+__global__ void __launch_bounds__(kSumThreads)
+    preference_sum_kernel(const LossRows R, const PreferenceArgs a, const double* __restrict__ lps, double* sums,
+                          float* __restrict__ g, PairWords* words, int* err) {
+  __shared__ double red[kSumThreads / 32];
+  __shared__ bool last;
+  const int n = 2 * a.n_pairs, tid = threadIdx.x;
+  int bad = a.cu[0] != 0 || a.cu[n] > R.M;
+  for (int i = tid; i < n; i += kSumThreads) bad |= a.cu[i + 1] < a.cu[i];
+  bad = __syncthreads_or(bad);
+  if (blockIdx.x == 0 && tid == 0) {
+    words->rows = bad ? 0 : a.cu[n];
+    if (bad && err) atomicOr(err, ERRF_SEQUENCE);
+  }
+  if (bad) return;
+  for (int q = blockIdx.x; q < n; q += gridDim.x) {
+    const int r1 = a.cu[q + 1];
+    double s = 0.0;
+    for (int r = a.cu[q] + tid; r < r1; r += kSumThreads) {
+      const double lp = row_target(R, r, err) < 0 ? 0.0 : lps[r];
+      a.logp[r] = static_cast<float>(lp);
+      s += lp;
+    }
+    s = block_sum(s, red);
+    if (tid == 0) {
       sums[q] = s;
       a.seq_logp[q] = static_cast<float>(s);
     }
   }
+  if (tid == 0) {
+    __threadfence();
+    last = atomicAdd(&words->done, 1) == static_cast<int>(gridDim.x) - 1;
+  }
   __syncthreads();
+  if (!last) return;
+  __threadfence();
   double loss = 0.0;
-  for (int i = threadIdx.x; i < a.n_pairs; i += 1024) {
+  for (int i = tid; i < a.n_pairs; i += kSumThreads) {
     const double ref = a.ref_logp ? static_cast<double>(a.ref_logp[2 * i]) - a.ref_logp[2 * i + 1] : 0.0;
-    const double z = a.beta * (sums[2 * i] - sums[2 * i + 1] - ref);
+    const double z = a.beta * (__ldcg(sums + 2 * i) - __ldcg(sums + 2 * i + 1) - ref);
     // sigmoid(-|z|), and log sigmoid(+-z) = min(+-z, 0) - log(1 + exp(-|z|))
     const double t = exp(-fabs(z)), soft = log1p(t), less = t / (1.0 + t);
     const double sig_pos = z >= 0.0 ? 1.0 - less : less, sig_neg = z >= 0.0 ? less : 1.0 - less;
@@ -411,15 +534,8 @@ __global__ void __launch_bounds__(1024)
     g[2 * i] = static_cast<float>(dz);
     g[2 * i + 1] = static_cast<float>(-dz);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
-  if (lane_id() == 0) red[warp_id()] = loss;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double t = 0.0;
-    for (int w = 0; w < 32; ++w) t += red[w];
-    *a.loss = static_cast<float>(t / a.n_pairs);
-  }
+  loss = block_sum(loss, red);
+  if (tid == 0) *a.loss = static_cast<float>(loss / a.n_pairs);
 }
 
 // The sequence that holds row r: the last one that starts at or before it.
@@ -433,22 +549,24 @@ __device__ __forceinline__ int row_sequence(const int* __restrict__ cu, int n, i
   return l;
 }
 
-template <typename T, int G>
-__global__ void __launch_bounds__(G, 1024 / G)
+template <typename T, int G, int S>
+__global__ void __launch_bounds__(G)
     preference_grad_kernel(const LossRows R, const PreferenceArgs a, const float2* __restrict__ ms,
-                           const float* __restrict__ g) {
+                           const float* __restrict__ g, const PairWords* __restrict__ words) {
+  extern __shared__ uint4 ring[];
   const int r = blockIdx.x;
-  if (r >= covered_rows(a, R.M, nullptr)) return;
+  if (r >= words->rows) return;
   T* d = static_cast<T*>(R.dlogits) + r * R.ld_d;
   const int y = row_target(R, r, nullptr);
   if (y < 0) {
     row_zero<T, G>(d, R.V);
     return;
   }
-  uint4 w[kVecs];
   const T* x = static_cast<const T*>(R.logits) + r * R.ld;
   const float2 q = ms[r];
-  row_gradient<T, G>(x, d, R.V, RowParts<T>(x, R.V), false, w, y, g[row_sequence(a.cu, 2 * a.n_pairs, r)], q.x, q.y);
+  const float gr = g[row_sequence(a.cu, 2 * a.n_pairs, r)];
+  const float xy = to_f(x[y]);
+  row_gradient(RowRing<T, G, S>(x, R.V, ring), d, false, Gradient<T>(y, xy, gr, q.x, q.y));
 }
 
 constexpr size_t al256(size_t x) { return (x + 255) / 256 * 256; }
@@ -458,55 +576,61 @@ constexpr size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 size_t policy_loss_scratch(int M) { return al256(static_cast<size_t>(M) * sizeof(float4)) + 256; }
 
 size_t preference_loss_scratch(int M, int n_pairs) {
-  return al256(static_cast<size_t>(M) * sizeof(float2)) + al256(static_cast<size_t>(M) * sizeof(double)) +
+  return 256 + al256(static_cast<size_t>(M) * sizeof(float2)) + al256(static_cast<size_t>(M) * sizeof(double)) +
          al256(2 * static_cast<size_t>(n_pairs) * sizeof(double)) +
          al256(2 * static_cast<size_t>(n_pairs) * sizeof(float));
 }
 
 template <typename T>
-static void policy_rows(const LossRows& r, const PolicyArgs& a, float4* terms, int* err, cudaStream_t s) {
-  with_row_threads(1ll * r.V * sizeof(T), [&](auto g) {
-    constexpr int G = decltype(g)::value;
-    policy_row_kernel<T, G><<<r.M, G, 0, s>>>(r, a, terms, err);
-  });
+static cudaError_t policy_rows(const LossRows& r, const PolicyArgs& a, float4* terms, int* err, cudaStream_t s) {
+  auto pick = [](auto g, auto slots) { return policy_row_kernel<T, decltype(g)::value, decltype(slots)::value>; };
+  if (1ll * r.V * sizeof(T) <= 65536) return launch_rows<T, 4>(r, s, pick, r, a, terms, err);
+  return launch_rows<T, 6>(r, s, pick, r, a, terms, err);
 }
 
 cudaError_t launch_policy_loss(const LossRows& r, const PolicyArgs& a, void* scratch, int* err, cudaStream_t s) {
   float4* terms = static_cast<float4*>(scratch);
   if (r.M > 0) {
-    if (r.fp32) policy_rows<float>(r, a, terms, err, s);
-    else policy_rows<bf16>(r, a, terms, err, s);
+    const cudaError_t e = r.fp32 ? policy_rows<float>(r, a, terms, err, s) : policy_rows<bf16>(r, a, terms, err, s);
+    if (e != cudaSuccess) return e;
   }
   policy_sum_kernel<<<1, 1024, 0, s>>>(terms, r.M, a.stats);
   return cudaGetLastError();
 }
 
 template <typename T>
-static void preference_rows(const LossRows& r, const PreferenceArgs& a, void* scratch, int* err, cudaStream_t s) {
+static cudaError_t preference_rows(const LossRows& r, const PreferenceArgs& a, void* scratch, int* err,
+                                   cudaStream_t s) {
   uint8_t* base = static_cast<uint8_t*>(scratch);
   auto take = [&](size_t bytes) {
     uint8_t* p = base;
     base += al256(bytes);
     return p;
   };
+  PairWords* words = reinterpret_cast<PairWords*>(take(sizeof(PairWords)));
   float2* ms = reinterpret_cast<float2*>(take(static_cast<size_t>(r.M) * sizeof(float2)));
   double* lps = reinterpret_cast<double*>(take(static_cast<size_t>(r.M) * sizeof(double)));
   double* sums = reinterpret_cast<double*>(take(2 * static_cast<size_t>(a.n_pairs) * sizeof(double)));
   float* g = reinterpret_cast<float*>(take(2 * static_cast<size_t>(a.n_pairs) * sizeof(float)));
-  with_row_threads(1ll * r.V * sizeof(T), [&](auto gs) {
-    constexpr int G = decltype(gs)::value;
-    // with no rows one block still checks the offsets
-    preference_logp_kernel<T, G><<<std::max(r.M, 1), G, 0, s>>>(r, a, ms, lps, err);
-    preference_pair_kernel<<<1, 1024, 0, s>>>(r, a, lps, sums, g);
-    if (r.dlogits && r.M > 0) preference_grad_kernel<T, G><<<r.M, G, 0, s>>>(r, a, ms, g);
-  });
+  cudaError_t e = launch_rows<T, 2>(
+      r, s, [](auto g, auto slots) { return preference_logp_kernel<T, decltype(g)::value, decltype(slots)::value>; },
+      r, a, ms, lps, words);
+  if (e != cudaSuccess) return e;
+  const int blocks = std::min(2 * a.n_pairs, 2 * device_sm_count());
+  preference_sum_kernel<<<blocks, kSumThreads, 0, s>>>(r, a, lps, sums, g, words, err);
+  if (r.dlogits && r.M > 0)
+    e = launch_rows<T, 4>(
+        r, s,
+        [](auto g, auto slots) { return preference_grad_kernel<T, decltype(g)::value, decltype(slots)::value>; }, r, a,
+        ms, g, words);
+  return e;
 }
 
 cudaError_t launch_preference_loss(const LossRows& r, const PreferenceArgs& a, void* scratch, int* err,
                                    cudaStream_t s) {
-  if (r.fp32) preference_rows<float>(r, a, scratch, err, s);
-  else preference_rows<bf16>(r, a, scratch, err, s);
-  return cudaGetLastError();
+  const cudaError_t e =
+      r.fp32 ? preference_rows<float>(r, a, scratch, err, s) : preference_rows<bf16>(r, a, scratch, err, s);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace gpt
