@@ -204,6 +204,27 @@ __device__ __forceinline__ void causal_mask_row(uint32_t (&sr)[128], int lane) {
   for (int k = 32 * (Q + 1); k < 128; ++k) sr[k] = __float_as_uint(-INFINITY);
 }
 
+// 64 bf16 values of each lane's row (w: packed pairs) to rows dst + row * pitch
+// (elements), row = 0 .. n_rows - 1 of the warp's 32, through 4 KB of shared
+// memory: eight lanes write one row's 128 bytes together.
+__device__ __forceinline__ void store_rows_64(uint8_t* stage, const uint32_t (&w)[32], bf16* dst, long long pitch,
+                                              int n_rows) {
+  const int lane = lane_id();
+  __syncwarp();   // the previous contents have been read
+#pragma unroll
+  for (int u = 0; u < 8; ++u)
+    *reinterpret_cast<uint4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) =
+        make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+  __syncwarp();
+  const int u = lane & 7;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = 4 * i + (lane >> 3);
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 128 + ((u ^ (row & 7)) << 4));
+    if (row < n_rows) *reinterpret_cast<uint4*>(dst + row * pitch + u * 8) = v;
+  }
+}
+
 // bits 0 .. n - 1
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
@@ -864,7 +885,8 @@ __global__ void __launch_bounds__(512, 1)
                        const float* __restrict__ Dv, bf16* __restrict__ dk, bf16* __restrict__ dv, int H, int Hkv,
                        int kvs, int T, int wl, float scale, int n_units, int* sched, int* err,
                        long long wait_cycles, const float* __restrict__ rk, const float2* __restrict__ rope,
-                       bf16* __restrict__ dqkv, const PackedArgs pa) {
+                       bf16* __restrict__ dqkv_arg, const PackedArgs pa) {
+  bf16* const dqkv = kPacked ? nullptr : dqkv_arg;   // packed: not built
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // the 128-byte-swizzled tiles need a 1024-byte-aligned base, which the
   // dynamic shared memory window provides; refuse to run otherwise
@@ -1333,7 +1355,7 @@ __global__ void __launch_bounds__(512, 1)
           // mask (ragged keys, window edge).  A per-element mask inside one loop
           // was if-converted into every block's path and cost more than the
           // exponentials.
-          auto run_chunk = [&](auto kCC, auto kMode) {
+          auto run_chunk = [&](auto kCC, auto kMode, uint32_t seen = 0u) {
             constexpr int cc = decltype(kCC)::value, mode = decltype(kMode)::value;
             const int c = 2 * half + cc;
             const uint32_t (&sr)[32] = cc == 0 ? sa : sb;
@@ -1362,18 +1384,18 @@ __global__ void __launch_bounds__(512, 1)
                     f2_unpack(f2_exp2_poly(f2_pack(fmaxf(x0, -126.f), fmaxf(x1, -126.f))), p[e], p[e + 1]);
                   }
                 }
-                if constexpr (mode == 1) {
+                if constexpr (mode == 1 && kPacked) {
+#pragma unroll
+                  for (int e = 0; e < 8; ++e)
+                    if (!(seen & (1u << (kq + e)))) p[e] = 0.f;
+                } else if constexpr (mode == 1) {
 #pragma unroll
                   for (int e = 0; e < 8; ++e)
                     if (kq + e < lane) p[e] = 0.f;
                 } else if constexpr (mode == 2) {
 #pragma unroll
                   for (int e = 0; e < 8; ++e)
-                    if constexpr (kPacked) {
-                      if ((diag && key > q0 + c * 32 + kq + e) || hi < q0 + c * 32 + kq + e) p[e] = 0.f;
-                    } else {
-                      if (!key_ok || (diag && key > q0 + c * 32 + kq + e) || key < q0 + c * 32 + kq + e - wl) p[e] = 0.f;
-                    }
+                    if (!key_ok || (diag && key > q0 + c * 32 + kq + e) || key < q0 + c * 32 + kq + e - wl) p[e] = 0.f;
                 }
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) pk[16 * cc + ((kq + e) >> 1)] = pack_bf16x2(p[e], p[e + 1]);
@@ -1387,14 +1409,12 @@ __global__ void __launch_bounds__(512, 1)
           auto do_chunk = [&](auto kCC) {
             const int c = 2 * half + decltype(kCC)::value;
             if constexpr (kPacked) {
-              // the same forms by the warp's keys' last queries
+              // the queries qc .. qc + 31 that see this key, key .. hi, as bits
               const int qc = q0 + c * 32;
               if (qc > hi_max || (diag && c < quarter))
                 run_chunk(kCC, M3{});
-              else if (qc + 31 > hi_min)
-                run_chunk(kCC, M2{});
-              else if (diag && c == quarter)
-                run_chunk(kCC, M1{});
+              else if (qc + 31 > hi_min || (diag && c == quarter))
+                run_chunk(kCC, M1{}, low_bits(hi + 1 - qc) & ~low_bits(key - qc));
               else
                 run_chunk(kCC, M0{});
             } else if (diag && !edge) {
@@ -1582,33 +1602,27 @@ __global__ void __launch_bounds__(512, 1)
           tc_fence_before();
         } else if (ok) {
           tc_fence_after();
-          bf16* dkrow = kPacked ? dk + (static_cast<long long>(kb.b) * T + key) * pa.o_tok + kb.hk * pa.o_head
-                                : dk + (static_cast<long long>(bkv) * T + key) * 128;
-          bf16* dvrow = kPacked ? dv + (static_cast<long long>(kb.b) * T + key) * pa.dv_tok + kb.hk * pa.dv_head
-                                : dv + (static_cast<long long>(bkv) * T + key) * 128;
+          const int w0 = k0 + quarter * 32, rows = min(32, Tv - w0);   // the warp's first key row, its rows
+          // dS of the last block has been read: its tile stages the rows, each
+          // warp in the part that it writes itself; dV, then dK
 #pragma unroll 1
-          for (int c = 2 * half; c < 2 * half + 2; ++c) {
-            uint32_t vr[32], kr[32];
-            tmem_load32_async(tmem + lane_base + 256 + c * 32, vr);
-            tmem_load32_async(tmem + lane_base + 384 + c * 32, kr);
-            tmem_wait_ld();
-            if (key_ok) {
+          for (int c = 0; c < 2; ++c) {
+            const long long pitch = kPacked ? (c ? pa.o_tok : pa.dv_tok) : 128;
+            bf16* row = (c ? dk : dv) + (kPacked ? static_cast<long long>(w0) * pitch + kb.hk * (c ? pa.o_head : pa.dv_head)
+                                                 : (static_cast<long long>(bkv) * T + w0) * 128);
+            const float f = c ? scale : 1.f;
+            uint32_t x[32], w[32];
 #pragma unroll
-              for (int gg = 0; gg < 32; gg += 8) {
-                uint4 wv, wk;
-                wv.x = pack_bf16x2(__uint_as_float(vr[gg]), __uint_as_float(vr[gg + 1]));
-                wv.y = pack_bf16x2(__uint_as_float(vr[gg + 2]), __uint_as_float(vr[gg + 3]));
-                wv.z = pack_bf16x2(__uint_as_float(vr[gg + 4]), __uint_as_float(vr[gg + 5]));
-                wv.w = pack_bf16x2(__uint_as_float(vr[gg + 6]), __uint_as_float(vr[gg + 7]));
-                wk.x = pack_bf16x2(__uint_as_float(kr[gg]) * scale, __uint_as_float(kr[gg + 1]) * scale);
-                wk.y = pack_bf16x2(__uint_as_float(kr[gg + 2]) * scale, __uint_as_float(kr[gg + 3]) * scale);
-                wk.z = pack_bf16x2(__uint_as_float(kr[gg + 4]) * scale, __uint_as_float(kr[gg + 5]) * scale);
-                wk.w = pack_bf16x2(__uint_as_float(kr[gg + 6]) * scale, __uint_as_float(kr[gg + 7]) * scale);
-                *reinterpret_cast<uint4*>(dvrow + c * 32 + gg) = wv;
-                *reinterpret_cast<uint4*>(dkrow + c * 32 + gg) = wk;
-              }
+            for (int hh = 0; hh < 2; ++hh) {
+              tmem_load32_async(tmem + lane_base + 256 + 128 * c + 64 * half + 32 * hh, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                w[16 * hh + k] = pack_bf16x2(__uint_as_float(x[2 * k]) * f, __uint_as_float(x[2 * k + 1]) * f);
             }
+            store_rows_64(sdSt + half * TF_TILE + quarter * 4096, w, row + 64 * half, pitch, rows);
           }
+          __syncwarp();   // read before the next item's dS goes there
           // dK and dV have been read: the next key block's first products may
           // overwrite them (they follow this thread's next p_ready / ds_ready)
           tc_fence_before();
