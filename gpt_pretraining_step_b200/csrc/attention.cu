@@ -408,8 +408,15 @@ __global__ void __launch_bounds__(384, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    {
       // -------------------------------------------------------------- MMA
+      // the whole warp, converged; one lane issues
+      const bool leader = elect_lane();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      auto wait1 = [&](uint64_t* bar, uint32_t par) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait_t<kFine>(bar, par, abort_flag, err, wlim));
+      };
+      auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
       constexpr uint32_t IDESC_S = make_idesc(1, 128, false, false);
       constexpr uint32_t IDESC_O = make_idesc(1, 128, false, true);
       // The descriptors of a product are its first one plus the byte offset / 16
@@ -419,50 +426,53 @@ __global__ void __launch_bounds__(384, 1)
       auto issue_s = [&](int t, int ks) {
         uint64_t dq = smem_desc_sw128(smem_u32(sQ + t * TF_BUF), 16, 1024);
         uint64_t dk = smem_desc_sw128(smem_u32(sK + ks * TF_BUF), 16, 1024);
-        asm volatile("" : "+l"(dq), "+l"(dk));
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
           const uint32_t off16 = ((kk >> 2) * TF_TILE + (kk & 3) * 32) >> 4;
-          umma_f16(tmem + t * 128, dq + off16, dk + off16, IDESC_S, kk > 0 ? 1u : 0u);
+          umma_f16_by(leader, tm + t * 128, dq + off16, dk + off16, IDESC_S, kk > 0 ? 1u : 0u);
         }
-        umma_commit(&s_full[t]);
+        umma_commit_by(leader, &s_full[t]);
       };
       // O_t (+)= P_t V (V in ring slot vs), P_t from TMEM (16 keys = 8 packed columns per step)
       auto issue_pv = [&](int t, int vs, bool acc) {
         uint64_t dv = smem_desc_sw128(smem_u32(sV + vs * TF_BUF), TF_TILE, 1024);
-        asm volatile("" : "+l"(dv));
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          umma_f16_tmem_a(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, dv + ((kk * 2048) >> 4), IDESC_O,
+          umma_f16_tmem_a_by(leader, tm + 256 + t * 128, tm + t * 128 + kk * 8, dv + ((kk * 2048) >> 4), IDESC_O,
                           (acc || kk > 0) ? 1u : 0u);
-        umma_commit(&pv_done[t]);
+        umma_commit_by(leader, &pv_done[t]);
       };
       bool ok = true;
       int g0 = 0;                  // ring position of the item's first key block
       uint32_t npv[2] = {0u, 0u};  // P V products issued per tile so far
       for (int n = 0; ok; ++n) {
-        if (!mbar_wait_t<kFine>(q_full, n & 1, abort_flag, err, wlim)) { ok = false; break; }
-        const int idx = item_ring[n & 3];
+        if (!wait1(q_full, n & 1)) { ok = false; break; }
+        const int idx = uniform(item_ring[n & 3]);
         if (idx < 0) break;
-        const FwdItem it = item_of(n, idx);
+        FwdItem it = item_of(n, idx);
+        it.nkvA = uniform(it.nkvA);
+        it.nkvB = uniform(it.nkvB);
+        it.nkv = uniform(it.nkv);
+        it.oB = uniform(it.oB);
+        it.hasB = uniform(it.hasB) != 0;
         // S of the first block on both tiles, each once its previous P V (which
         // reads P from the same columns) has completed
-        if (!mbar_wait_t<kFine>(&k_full[g0 & 1], (g0 >> 1) & 1, abort_flag, err, wlim)) { ok = false; break; }
+        if (!wait1(&k_full[g0 & 1], (g0 >> 1) & 1)) { ok = false; break; }
         for (int t = 0; t < 2 && ok; ++t) {
           if (t == 1 && (!it.hasB || (kPacked && it.oB > 0))) break;
-          if (npv[t] > 0 && !mbar_wait_t<kFine>(&pv_done[t], (npv[t] - 1) & 1, abort_flag, err, wlim)) { ok = false; break; }
+          if (npv[t] > 0 && !wait1(&pv_done[t], (npv[t] - 1) & 1)) { ok = false; break; }
           tc_fence_after();
           issue_s(t, g0 & 1);
         }
         if (!ok) break;
-        if (it.nkv == 1) umma_commit(q_empty);   // the item's last S
-        umma_commit(&k_empty[g0 & 1]);
+        if (it.nkv == 1) umma_commit_by(leader, q_empty);   // the item's last S
+        umma_commit_by(leader, &k_empty[g0 & 1]);
         for (int j = 0; j < it.nkv && ok; ++j) {
           const int gj = g0 + j;
           const int s = gj & 1;
           const int s1 = (gj + 1) & 1;
-          if (!mbar_wait_t<kFine>(&v_full[s], (gj >> 1) & 1, abort_flag, err, wlim)) { ok = false; break; }
-          if (j + 1 < it.nkv && !mbar_wait_t<kFine>(&k_full[s1], ((gj + 1) >> 1) & 1, abort_flag, err, wlim)) { ok = false; break; }
+          if (!wait1(&v_full[s], (gj >> 1) & 1)) { ok = false; break; }
+          if (j + 1 < it.nkv && !wait1(&k_full[s1], ((gj + 1) >> 1) & 1)) { ok = false; break; }
           // per tile: O += P V_j, then S of the next block over P once that product
           // has read it (tile B's softmax trails tile A's, so A goes first)
           for (int t = 0; t < 2; ++t) {
@@ -470,25 +480,25 @@ __global__ void __launch_bounds__(384, 1)
             if (j >= nkv_t) continue;
             const int o_t = kPacked && t ? it.oB : 0;   // the tile's first block
             if (!kPacked || j >= o_t) {
-              if (!mbar_wait_t<kFine>(&p_full[t], npv[t] & 1, abort_flag, err, wlim)) { ok = false; break; }
+              if (!wait1(&p_full[t], npv[t] & 1)) { ok = false; break; }
               tc_fence_after();
               issue_pv(t, s, j > o_t);
               ++npv[t];
             }
             if (j + 1 < nkv_t && (!kPacked || j + 1 >= o_t)) {
-              if ((!kPacked || npv[t] > 0) && !mbar_wait_t<kFine>(&pv_done[t], (npv[t] - 1) & 1, abort_flag, err, wlim)) { ok = false; break; }
+              if ((!kPacked || npv[t] > 0) && !wait1(&pv_done[t], (npv[t] - 1) & 1)) { ok = false; break; }
               tc_fence_after();
               issue_s(t, s1);
-              if (j + 1 == it.nkv - 1) umma_commit(q_empty);   // the item's last S
+              if (j + 1 == it.nkv - 1) umma_commit_by(leader, q_empty);   // the item's last S
             }
           }
           if (!ok) break;
-          umma_commit(&v_empty[s]);
-          if (j + 1 < it.nkv) umma_commit(&k_empty[s1]);
+          umma_commit_by(leader, &v_empty[s]);
+          if (j + 1 < it.nkv) umma_commit_by(leader, &k_empty[s1]);
         }
         g0 += it.nkv;
       }
-      umma_commit(drain);
+      umma_commit_by(leader, drain);
       for (uint32_t i = 0; i < (1u << 22) && !mbar_try_wait(drain, 0); ++i) {}
     }
   } else if (warp >= 4) {
@@ -1072,8 +1082,15 @@ __global__ void __launch_bounds__(512, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    {
       // -------------------------------------------------------------- MMA
+      // the whole warp, converged; one lane issues
+      const bool leader = elect_lane();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      auto wait1 = [&](uint64_t* bar, uint32_t par) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait_t<kFine>(bar, par, abort_flag, err, wlim));
+      };
+      auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
       constexpr uint32_t IDESC_KK = make_idesc(1, 128, false, false);   // S^T, dP^T
       constexpr uint32_t IDESC_KM = make_idesc(1, 128, false, true);    // dV (A in TMEM), dK
       constexpr uint32_t IDESC_MM = make_idesc(1, 128, true, true);     // dQ
@@ -1083,117 +1100,113 @@ __global__ void __launch_bounds__(512, 1)
       // asm keeps the descriptors from being hoisted into registers
       auto qk_product = [&](uint32_t d_tmem, uint32_t a_addr, uint32_t b_addr) {
         uint64_t da = smem_desc_sw128(a_addr, 16, 1024), db = smem_desc_sw128(b_addr, 16, 1024);
-        asm volatile("" : "+l"(da), "+l"(db));
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
           const uint32_t off16 = ((kk >> 2) * TF_TILE + (kk & 3) * 32) >> 4;
-          umma_f16(d_tmem, da + off16, db + off16, IDESC_KK, kk > 0 ? 1u : 0u);
+          umma_f16_by(leader, d_tmem, da + off16, db + off16, IDESC_KK, kk > 0 ? 1u : 0u);
         }
       };
       bool ok = true;
       int g0 = 0;   // query blocks done so far
       for (int n = 0; ok; ++n) {
-        if (!mbar_wait_t<kFine>(kv_full, n & 1, abort_flag, err, wlim)) { ok = false; break; }
-        const int idx = item_ring[n & 3];
+        if (!wait1(kv_full, n & 1)) { ok = false; break; }
+        const int idx = uniform(item_ring[n & 3]);
         if (idx < 0) break;
         {
           const BwdBlock kb = block_of(n, idx);
-          const int n_it = kb.n_it;
+          const int n_it = uniform(kb.n_it);
           // S^T of the first query block goes where the previous key block's
           // last dQ was (wait until the dQ warps have read it), dP^T where
           // its last P was (wait until that dV is done)
-          ok = mbar_wait_t<kFine>(&q_full[g0 & 1], (g0 >> 1) & 1, abort_flag, err, wlim) &&
-               (g0 == 0 || mbar_wait_t<kFine>(dq_free, (g0 - 1) & 1, abort_flag, err, wlim));
+          ok = wait1(&q_full[g0 & 1], (g0 >> 1) & 1) &&
+               (g0 == 0 || wait1(dq_free, (g0 - 1) & 1));
           if (!ok) break;
           tc_fence_after();
-          qk_product(tmem, k_addr, smem_u32(sQ + (g0 & 1) * TF_BUF));   // S^T of the first block
-          umma_commit(s_full);
-          ok = mbar_wait_t<kFine>(do_full, g0 & 1, abort_flag, err, wlim) &&
-               (g0 == 0 || mbar_wait_t<kFine>(do_empty, (g0 - 1) & 1, abort_flag, err, wlim));
+          qk_product(tm, k_addr, smem_u32(sQ + (g0 & 1) * TF_BUF));   // S^T of the first block
+          umma_commit_by(leader, s_full);
+          ok = wait1(do_full, g0 & 1) &&
+               (g0 == 0 || wait1(do_empty, (g0 - 1) & 1));
           if (!ok) break;
           tc_fence_after();
-          qk_product(tmem + 128, v_addr, do_addr);   // dP^T of the first block
-          umma_commit(dp_full);
+          qk_product(tm + 128, v_addr, do_addr);   // dP^T of the first block
+          umma_commit_by(leader, dp_full);
           if (n_it > 1) {
-            ok = mbar_wait_t<kFine>(s_free, g0 & 1, abort_flag, err, wlim) &&
-                 mbar_wait_t<kFine>(&q_full[(g0 + 1) & 1], ((g0 + 1) >> 1) & 1, abort_flag, err, wlim);
+            ok = wait1(s_free, g0 & 1) &&
+                 wait1(&q_full[(g0 + 1) & 1], ((g0 + 1) >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            qk_product(tmem, k_addr, smem_u32(sQ + ((g0 + 1) & 1) * TF_BUF));   // S^T of the second block
-            umma_commit(s_full);
+            qk_product(tm, k_addr, smem_u32(sQ + ((g0 + 1) & 1) * TF_BUF));   // S^T of the second block
+            umma_commit_by(leader, s_full);
           }
           for (int it = 0; it < n_it && ok; ++it) {
             const int gi = g0 + it;
             const int s = gi & 1;
-            if (!mbar_wait_t<kFine>(p_ready, gi & 1, abort_flag, err, wlim)) { ok = false; break; }
+            if (!wait1(p_ready, gi & 1)) { ok = false; break; }
             tc_fence_after();
             const uint32_t q_addr = smem_u32(sQ + s * TF_BUF);
             // dV += P^T dO: A = P^T from TMEM, 16 queries = 8 packed columns per
             // step; queries 0..63 at columns 128.., 64..127 at columns 192..
             {
               uint64_t ddo = smem_desc_sw128(do_addr, TF_TILE, 1024);
-              asm volatile("" : "+l"(ddo));
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)
-                umma_f16_tmem_a(tmem + 256, tmem + 128 + (kk >> 2) * 64 + (kk & 3) * 8, ddo + ((kk * 2048) >> 4),
+                umma_f16_tmem_a_by(leader, tm + 256, tm + 128 + (kk >> 2) * 64 + (kk & 3) * 8, ddo + ((kk * 2048) >> 4),
                                 IDESC_KM, (it > 0 || kk > 0) ? 1u : 0u);
             }
-            umma_commit(do_empty);
+            umma_commit_by(leader, do_empty);
             // dK and dQ once dS_i is in shared memory (the softmax warps compute it
             // while dV runs)
-            if (!mbar_wait_t<kFine>(ds_ready, gi & 1, abort_flag, err, wlim)) { ok = false; break; }
+            if (!wait1(ds_ready, gi & 1)) { ok = false; break; }
             tc_fence_after();
             {
               uint64_t dsa = smem_desc_sw128(dst_addr, 16, 1024), dqb = smem_desc_sw128(q_addr, TF_TILE, 1024);
-              asm volatile("" : "+l"(dsa), "+l"(dqb));
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk) {
                 const uint32_t aoff16 = ((kk >> 2) * TF_TILE + (kk & 3) * 32) >> 4;   // K-major A: 16 queries per step
                 const uint32_t boff16 = (kk * 2048) >> 4;                            // MN-major B: 16 query rows per step
-                umma_f16(tmem + 384, dsa + aoff16, dqb + boff16, IDESC_KM, (it > 0 || kk > 0) ? 1u : 0u);
+                umma_f16_by(leader, tm + 384, dsa + aoff16, dqb + boff16, IDESC_KM, (it > 0 || kk > 0) ? 1u : 0u);
               }
             }
-            umma_commit(&q_empty[s]);
+            umma_commit_by(leader, &q_empty[s]);
             // dQ_i goes to [0,128), which holds S^T_{i+1} (wait until the softmax
             // warps have read it) or, for the last block, dQ_{i-1} (wait until
             // the dQ warps have read it)
             if (it + 1 < n_it) {
-              if (!mbar_wait_t<kFine>(s_free, (gi + 1) & 1, abort_flag, err, wlim)) { ok = false; break; }
+              if (!wait1(s_free, (gi + 1) & 1)) { ok = false; break; }
             } else if (it > 0) {
-              if (!mbar_wait_t<kFine>(dq_free, (gi - 1) & 1, abort_flag, err, wlim)) { ok = false; break; }
+              if (!wait1(dq_free, (gi - 1) & 1)) { ok = false; break; }
             }
             tc_fence_after();
             {
               uint64_t dka = smem_desc_sw128(k_addr, TF_TILE, 1024), dsb = smem_desc_sw128(dst_addr, TF_TILE, 1024);
-              asm volatile("" : "+l"(dka), "+l"(dsb));
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk) {
                 const uint32_t off16 = (kk * 2048) >> 4;   // 16 keys per step, both operands MN-major
-                umma_f16(tmem, dsb + off16, dka + off16, IDESC_MM, kk > 0 ? 1u : 0u);   // dQ = dS K
+                umma_f16_by(leader, tm, dsb + off16, dka + off16, IDESC_MM, kk > 0 ? 1u : 0u);   // dQ = dS K
               }
             }
-            umma_commit(mm_done);
-            if (it + 1 == n_it) umma_commit(kv_empty);   // K and V of this key block are free
+            umma_commit_by(leader, mm_done);
+            if (it + 1 == n_it) umma_commit_by(leader, kv_empty);   // K and V of this key block are free
             if (it + 1 < n_it) {
               // dP^T_{i+1} overwrites P^T_i: dV_i must have completed
-              if (!mbar_wait_t<kFine>(do_empty, gi & 1, abort_flag, err, wlim) ||
-                  !mbar_wait_t<kFine>(do_full, (gi + 1) & 1, abort_flag, err, wlim)) { ok = false; break; }
+              if (!wait1(do_empty, gi & 1) ||
+                  !wait1(do_full, (gi + 1) & 1)) { ok = false; break; }
               tc_fence_after();
-              qk_product(tmem + 128, v_addr, do_addr);
-              umma_commit(dp_full);
+              qk_product(tm + 128, v_addr, do_addr);
+              umma_commit_by(leader, dp_full);
             }
             if (it + 2 < n_it) {
-              if (!mbar_wait_t<kFine>(dq_free, gi & 1, abort_flag, err, wlim) ||
-                  !mbar_wait_t<kFine>(&q_full[s], ((gi + 2) >> 1) & 1, abort_flag, err, wlim)) { ok = false; break; }
+              if (!wait1(dq_free, gi & 1) ||
+                  !wait1(&q_full[s], ((gi + 2) >> 1) & 1)) { ok = false; break; }
               tc_fence_after();
-              qk_product(tmem, k_addr, q_addr);   // S^T_{i+2} (same Q slot as block i)
-              umma_commit(s_full);
+              qk_product(tm, k_addr, q_addr);   // S^T_{i+2} (same Q slot as block i)
+              umma_commit_by(leader, s_full);
             }
           }
           g0 += n_it;
         }
       }
-      umma_commit(drain);
+      umma_commit_by(leader, drain);
       for (uint32_t x = 0; x < (1u << 22) && !mbar_try_wait(drain, 0); ++x) {}
     }
   } else if (warp >= 12) {
@@ -1863,47 +1876,64 @@ __global__ void __launch_bounds__(32)
 }
 
 // Backward: D[b, h, t] = sum_i dO * O of the rows that hold sequences and
-// zeros in the fp32 dq accumulator, one warp per (t, h) row; the first block
-// also does the setup.
+// zeros in the fp32 dq accumulator, some (t, h) rows a warp, whose loads are
+// issued together; the first block does the setup.
+constexpr int kRowsPerWarp = 4;
 __global__ void __launch_bounds__(256)
     attention_packed_pre_kernel(const __grid_constant__ SetupMaps in, CUtensorMap* out, int* ctl, const int* meta,
                                 const bf16* __restrict__ o, long long o_tok, long long o_head,
                                 const bf16* __restrict__ dout, long long do_tok, long long do_head,
-                                float* __restrict__ Dv, float* __restrict__ dq, int B, int H, int T, int* err) {
+                                float* __restrict__ Dv, float* __restrict__ dq, int H, int T, int* err) {
   __shared__ __align__(128) CUtensorMap stage[4];
   if (blockIdx.x == 0) {
-    if (warp_id() == 0) packed_setup(in, 4, out, ctl, meta, B, T, 1, err, stage);
+    if (warp_id() == 0) packed_setup(in, 4, out, ctl, meta, 1, T, 1, err, stage);
     return;
   }
-  const long long w = static_cast<long long>(blockIdx.x - 1) * 8 + warp_id();
-  const int h = static_cast<int>(w % H);
-  const long long p = w / H;
-  if (p >= static_cast<long long>(B) * T) return;
-  const int b = static_cast<int>(p / T), t = static_cast<int>(p - static_cast<long long>(b) * T);
-  if (meta[kMetaMagic] != kPlanMagic || meta[kMetaB] != B || meta[kMetaT] != T || p >= meta[kMetaTotal]) return;
-  const long long row = (static_cast<long long>(b) * H + h) * T + t;
-  const uint2 x = *reinterpret_cast<const uint2*>(o + p * o_tok + h * o_head + lane_id() * 4);
-  const uint2 y = *reinterpret_cast<const uint2*>(dout + p * do_tok + h * do_head + lane_id() * 4);
-  reinterpret_cast<float4*>(dq + row * HD)[lane_id()] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float s = bf16_lo(x.x) * bf16_lo(y.x) + bf16_hi(x.x) * bf16_hi(y.x) + bf16_lo(x.y) * bf16_lo(y.y) +
-            bf16_hi(x.y) * bf16_hi(y.y);
-  s = warp_sum(s);
-  if (lane_id() == 0) Dv[row] = s;
+  if (meta[kMetaMagic] != kPlanMagic || meta[kMetaT] != T) return;
+  const long long rows = static_cast<long long>(meta[kMetaTotal]) * H;
+  const long long w = (static_cast<long long>(blockIdx.x - 1) * 8 + warp_id()) * kRowsPerWarp;
+  uint2 x[kRowsPerWarp], y[kRowsPerWarp];
+#pragma unroll
+  for (int i = 0; i < kRowsPerWarp; ++i) {
+    if (w + i >= rows) break;
+    const long long t = (w + i) / H, h = w + i - t * H;
+    x[i] = *reinterpret_cast<const uint2*>(o + t * o_tok + h * o_head + lane_id() * 4);
+    y[i] = *reinterpret_cast<const uint2*>(dout + t * do_tok + h * do_head + lane_id() * 4);
+  }
+#pragma unroll
+  for (int i = 0; i < kRowsPerWarp; ++i) {
+    if (w + i >= rows) break;
+    const long long t = (w + i) / H, h = w + i - t * H, row = h * T + t;
+    reinterpret_cast<float4*>(dq + row * HD)[lane_id()] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float s = bf16_lo(x[i].x) * bf16_lo(y[i].x) + bf16_hi(x[i].x) * bf16_hi(y[i].x) + bf16_lo(x[i].y) * bf16_lo(y[i].y) +
+              bf16_hi(x[i].y) * bf16_hi(y[i].y);
+    s = warp_sum(s);
+    if (lane_id() == 0) Dv[row] = s;
+  }
 }
 
-// dq in bf16 from the fp32 sums, rows that hold sequences; one warp per (t, h).
+// dq in bf16 from the fp32 sums, rows that hold sequences.
 __global__ void __launch_bounds__(256)
     attention_packed_dq_kernel(const float* __restrict__ acc, bf16* __restrict__ dq, long long dq_tok,
                                long long dq_head, const int* ctl, int H, int T) {
-  const long long w = static_cast<long long>(blockIdx.x) * 8 + warp_id();
-  const int h = static_cast<int>(w % H);
-  const long long t = w / H;
-  if (t >= ctl[kCtlValid]) return;
-  const float4 v = reinterpret_cast<const float4*>(acc + (static_cast<long long>(h) * T + t) * HD)[lane_id()];
-  uint2 u;
-  u.x = pack_bf16x2(v.x, v.y);
-  u.y = pack_bf16x2(v.z, v.w);
-  *reinterpret_cast<uint2*>(dq + t * dq_tok + h * dq_head + lane_id() * 4) = u;
+  const long long rows = static_cast<long long>(ctl[kCtlValid]) * H;
+  const long long w = (static_cast<long long>(blockIdx.x) * 8 + warp_id()) * kRowsPerWarp;
+  float4 v[kRowsPerWarp];
+#pragma unroll
+  for (int i = 0; i < kRowsPerWarp; ++i) {
+    if (w + i >= rows) break;
+    const long long t = (w + i) / H, h = w + i - t * H;
+    v[i] = reinterpret_cast<const float4*>(acc + (h * T + t) * HD)[lane_id()];
+  }
+#pragma unroll
+  for (int i = 0; i < kRowsPerWarp; ++i) {
+    if (w + i >= rows) break;
+    const long long t = (w + i) / H, h = w + i - t * H;
+    uint2 u;
+    u.x = pack_bf16x2(v[i].x, v[i].y);
+    u.y = pack_bf16x2(v[i].z, v[i].w);
+    *reinterpret_cast<uint2*>(dq + t * dq_tok + h * dq_head + lane_id() * 4) = u;
+  }
 }
 
 }  // namespace
@@ -2088,10 +2118,10 @@ cudaError_t launch_attn_packed_bwd(const PackedTensor& q, const PackedTensor& k,
       !make_map(&mdq, acc, 4, HD, T, H, HD, 1ll * T * HD, 32, 32))
     return cudaErrorInvalidValue;
   const PlanView P = plan_view(const_cast<void*>(plan), 1, T);
-  const int row_blocks = static_cast<int>((rows + 7) / 8);
+  const int row_blocks = static_cast<int>((rows + 8 * kRowsPerWarp - 1) / (8 * kRowsPerWarp));
   attention_packed_pre_kernel<<<1 + row_blocks, 256, 0, s>>>(
       maps, dmaps, ctl, P.meta, static_cast<const bf16*>(o.ptr), o.tok, o.head, static_cast<const bf16*>(dout.ptr),
-      dout.tok, dout.head, Dv, acc, 1, H, T, err);
+      dout.tok, dout.head, Dv, acc, H, T, err);
   PackedArgs pa = {};
   pa.lo = P.lo;
   pa.hi = P.hi;
