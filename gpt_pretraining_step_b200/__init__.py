@@ -33,8 +33,8 @@ ABI_FUNCTIONS = [
     "gpt_op_newton_schulz_noalloc", "gpt_get_adam_step", "gpt_set_adam_step", "gpt_set_wait_limit",
     "gpt_op_check", "gpt_op_set_wait_limit", "gpt_op_embedding_bwd_scratch", "gpt_op_embedding_bwd",
     "adamw_step_shard", "gpt_tensor_region", "gpt_grad_bucket", "gpt_set_grad_events",
-    "gpt_op_attention_plan_bytes", "gpt_op_attention_plan", "gpt_op_attention_packed_scratch",
-    "gpt_op_attention_packed_fwd", "gpt_op_attention_packed_bwd", "gpt_op_policy_loss_scratch",
+    "gpt_op_attention_plan_bytes", "gpt_op_attention_plan", "gpt_op_attention_packed_fwd",
+    "gpt_op_attention_packed_bwd_scratch", "gpt_op_attention_packed_bwd", "gpt_op_policy_loss_scratch",
     "gpt_op_policy_loss", "gpt_op_preference_loss_scratch", "gpt_op_preference_loss",
 ]
 DTYPE_BF16, DTYPE_FP32 = 0, 1
@@ -128,8 +128,8 @@ def lib():
             "gpt_op_newton_schulz_noalloc": (i32, [vp, vp, i32, i32, i32, i32, vp]),
             "gpt_op_attention_plan_bytes": (sz, [i32]),
             "gpt_op_attention_plan": (i32, [vp, i32, i32, i32, vp, vp]),
-            "gpt_op_attention_packed_scratch": (sz, [i32, i32, i32]),
-            "gpt_op_attention_packed_fwd": (i32, [hp, hp, hp, hp, vp, i32, i32, i32, f32, vp, vp, vp]),
+            "gpt_op_attention_packed_bwd_scratch": (sz, [i32, i32]),
+            "gpt_op_attention_packed_fwd": (i32, [hp, hp, hp, hp, vp, i32, i32, i32, f32, vp, vp]),
             "gpt_op_attention_packed_bwd": (i32, [hp, hp, hp, hp, vp, hp, hp, hp, hp, i32, i32, i32, f32, vp, vp,
                                                   vp]),
             "gpt_op_policy_loss_scratch": (sz, [i32]),
@@ -561,11 +561,10 @@ def attention_packed_fwd(q, k, v, plan, scale=0.0, o=None, lse=None, stream=None
         o = torch.empty((n, H, 128), dtype=bf16, device=q.device)
     if lse is None:
         lse = torch.empty((H, n), dtype=torch.float32, device=q.device)
-    scratch = torch.empty(_bytes("gpt_op_attention_packed_scratch", n, H, 0), dtype=torch.uint8, device=q.device)
     _check(lib().gpt_op_attention_packed_fwd(
         _heads("q", q, n, H, dev, bf16), _heads("k", k, n, Hkv, dev, bf16), _heads("v", v, n, Hkv, dev, bf16),
         _heads("o", o, n, H, dev, bf16), _flat("lse", lse, torch.float32, (H, n), dev), n, H, Hkv, scale,
-        plan.buf.data_ptr(), scratch.data_ptr(), _raw_stream(stream, dev, (o, lse, scratch))))
+        plan.buf.data_ptr(), _raw_stream(stream, dev, (o, lse))))
     return o, lse
 
 
@@ -581,7 +580,7 @@ def attention_packed_bwd(q, k, v, o, lse, dout, plan, scale=0.0, dq=None, dk=Non
         dk = torch.empty((n, Hkv, 128), dtype=bf16, device=q.device)
     if dv is None:
         dv = torch.empty((n, Hkv, 128), dtype=bf16, device=q.device)
-    scratch = torch.empty(_bytes("gpt_op_attention_packed_scratch", n, H, 1), dtype=torch.uint8, device=q.device)
+    scratch = torch.empty(_bytes("gpt_op_attention_packed_bwd_scratch", n, H), dtype=torch.uint8, device=q.device)
     _check(lib().gpt_op_attention_packed_bwd(
         _heads("q", q, n, H, dev, bf16), _heads("k", k, n, Hkv, dev, bf16), _heads("v", v, n, Hkv, dev, bf16),
         _heads("o", o, n, H, dev, bf16), _flat("lse", lse, torch.float32, (H, n), dev),

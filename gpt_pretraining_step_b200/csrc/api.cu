@@ -1776,18 +1776,17 @@ static int heads_arg(const gpt_heads* t, const char* name, long long tokens, lon
   return GPT_OK;
 }
 
-static int packed_shape(int n_tokens, int H, int Hkv, float scale, const void* plan, const void* scratch) {
+static int packed_shape(int n_tokens, int H, int Hkv, float scale, const void* plan) {
   if (n_tokens < 0 || H < 1) return fail(GPT_EINVAL, "bad attention shape");
   if (Hkv < 1 || H % Hkv) return fail(GPT_EINVAL, "kv heads must divide the query heads");
   if (static_cast<long long>(n_tokens) * H > (1ll << 31) - 1) return fail(GPT_EINVAL, "attention too large");
   if (!(scale >= 0.f) || std::isinf(scale)) return fail(GPT_EINVAL, "scale must be positive (0: 1 / sqrt(128))");
-  if (!plan || !scratch) return fail(GPT_EINVAL, "null pointer");
-  if (!aligned_scratch(plan) || !aligned_scratch(scratch))
-    return fail(GPT_EINVAL, "plan and scratch must be 256-byte aligned");
+  if (!plan) return fail(GPT_EINVAL, "null pointer: plan");
+  if (!aligned_scratch(plan)) return fail(GPT_EINVAL, "plan must be 256-byte aligned");
   return GPT_OK;
 }
 
-size_t gpt_op_attention_plan_bytes(int n_tokens) { return n_tokens < 0 ? 0 : attention_plan_bytes(1, n_tokens); }
+size_t gpt_op_attention_plan_bytes(int n_tokens) { return n_tokens < 0 ? 0 : attention_plan_bytes(n_tokens); }
 
 int gpt_op_attention_plan(const int32_t* cu_seqlens, int n_seq, int n_tokens, int window, void* plan, void* stream) {
   if (!cu_seqlens || !plan) return fail(GPT_EINVAL, "null pointer");
@@ -1796,19 +1795,15 @@ int gpt_op_attention_plan(const int32_t* cu_seqlens, int n_seq, int n_tokens, in
   int* err = nullptr;
   int rc = op_err(&err);
   if (rc) return rc;
-  launch_attention_plan(cu_seqlens, n_seq, 1, n_tokens, window, false, plan, err, static_cast<cudaStream_t>(stream));
+  launch_attention_plan(cu_seqlens, n_seq, n_tokens, window, plan, err, static_cast<cudaStream_t>(stream));
   GPT_CK(cudaGetLastError());
   return GPT_OK;
 }
 
-size_t gpt_op_attention_packed_scratch(int n_tokens, int H, int backward) {
-  return n_tokens < 0 || H < 1 ? 0 : attention_packed_scratch(n_tokens, H, backward != 0);
-}
-
 int gpt_op_attention_packed_fwd(const gpt_heads* q, const gpt_heads* k, const gpt_heads* v, const gpt_heads* o,
                                 float* lse, int n_tokens, int H, int Hkv, float scale, const void* plan,
-                                void* scratch, void* stream) {
-  int rc = packed_shape(n_tokens, H, Hkv, scale, plan, scratch);
+                                void* stream) {
+  int rc = packed_shape(n_tokens, H, Hkv, scale, plan);
   if (rc || n_tokens == 0) return rc;
   if (!lse) return fail(GPT_EINVAL, "null pointer: lse");
   PackedTensor tq, tk, tv, to;
@@ -1818,16 +1813,21 @@ int gpt_op_attention_packed_fwd(const gpt_heads* q, const gpt_heads* k, const gp
   int* err = nullptr;
   if ((rc = op_err(&err))) return rc;
   GPT_CK(launch_attn_packed_fwd(tq, tk, tv, to, lse, H, Hkv, n_tokens, scale > 0.f ? scale : 1.f / sqrtf(128.f), plan,
-                                scratch, static_cast<cudaStream_t>(stream), err, g_op_wait_cycles.load()));
+                                static_cast<cudaStream_t>(stream), err, g_op_wait_cycles.load()));
   return GPT_OK;
+}
+
+size_t gpt_op_attention_packed_bwd_scratch(int n_tokens, int H) {
+  return n_tokens < 0 || H < 1 ? 0 : attention_packed_bwd_scratch(n_tokens, H);
 }
 
 int gpt_op_attention_packed_bwd(const gpt_heads* q, const gpt_heads* k, const gpt_heads* v, const gpt_heads* o,
                                 const float* lse, const gpt_heads* dout, const gpt_heads* dq, const gpt_heads* dk,
                                 const gpt_heads* dv, int n_tokens, int H, int Hkv, float scale, const void* plan,
                                 void* scratch, void* stream) {
-  int rc = packed_shape(n_tokens, H, Hkv, scale, plan, scratch);
+  int rc = packed_shape(n_tokens, H, Hkv, scale, plan);
   if (rc || n_tokens == 0) return rc;
+  if (!scratch || !aligned_scratch(scratch)) return fail(GPT_EINVAL, "scratch must be 256-byte aligned");
   if (!lse) return fail(GPT_EINVAL, "null pointer: lse");
   PackedTensor tq, tk, tv, to, tdo, tdq, tdk, tdv;
   if ((rc = heads_arg(q, "q", n_tokens, H, false, &tq)) || (rc = heads_arg(k, "k", n_tokens, Hkv, false, &tk)) ||

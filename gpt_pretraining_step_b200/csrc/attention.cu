@@ -28,7 +28,7 @@ constexpr int HD = 128;
 
 // ------------------------------------------------------- packed sequences
 //
-// The second build of both kernels (kPacked): every row of T positions holds
+// The second build of both kernels (kPacked): one row of T positions holds
 // sequences of different lengths end to end, and query t sees the keys
 // lo[t] .. t, lo[t] = max(start of t's sequence, t - window).  lo does not
 // decrease with t, so a tile of 128 queries sees the key blocks from that of
@@ -38,21 +38,60 @@ constexpr int HD = 128;
 // and the softmax masks by lo per row.  The other way round the queries that
 // see key t are t .. hi[t], hi[t] = min(end of the sequence - 1, t + window).
 // The plan (attention_plan_kernel, once per batch) holds lo, hi and the work
-// items sorted by their number of blocks, longest first, which a counter
-// hands out.  Positions past the last sequence are neither read nor written:
-// attention_setup_kernel copies the tensor maps to device memory with their
-// token extent cut to the sequences' end, so TMA fills those rows with zeros
-// (their memory may hold NaN, which a zero probability would not remove).
+// items sorted by their number of blocks, longest first.  (Tiles that start
+// with their sequence would need 6% fewer blocks on documents of 128 to 2048
+// tokens, 14% on chats of 24 to 1024, but more tiles.)
+// Positions past the last sequence are neither read nor written.  Their
+// memory may hold NaN, which a zero probability would not remove: the forward
+// clears those rows of a V tile in shared memory (K and Q there reach only
+// scores that are masked and rows that are not stored), the backward copies
+// the tensor maps to device memory with their token extent cut to the
+// sequences' end, so that TMA fills the rows of all four operands with zeros.
 struct PackedArgs {
-  const int* lo;            // [B * T], row-local
-  const int* hi;            // [B * T], row-local; -1 past the last sequence
-  const int* order;         // work entries: forward b * npairs + pair, backward b * nblocks + key block
-  const int* ctl;           // kCtl* words
-  const CUtensorMap* maps;  // q, k, v (and dO) with the extent patched in
+  const int* meta;          // forward: the plan's kMeta* words
+  const int* lo;            // [T]
+  const int* hi;            // [T]; -1 past the last sequence
+  const int4* fwd;          // forward entries: first query tile, first key block of it and of the next tile (-1: none)
+  const int2* bwd;          // backward entries: key block, number of query blocks that see it
+  const int* ctl;           // backward: kCtl* words
+  const CUtensorMap* maps;  // backward: q, k, v, dO with the extent patched in
   long long o_tok, o_head;    // forward: strides of o in elements; backward: of dk
   long long dv_tok, dv_head;  // backward: strides of dv
 };
-enum { kCtlSched = 0, kCtlEntries = 1, kCtlValid = 2, kCtlWords = 8 };
+enum { kCtlSched = 0, kCtlEntries = 1, kCtlValid = 2 };
+// Words of a plan: positions that the sequences hold, forward and backward
+// entries, T.
+enum { kMetaTotal = 0, kMetaFwd = 1, kMetaBwd = 2, kMetaT = 3, kMetaMagic = 4, kPlanMeta = 64 };
+constexpr int kPlanMagic = 0x5e91a7e;
+
+// The packed forward takes its items from the grid: it is launched with a
+// block for each, and a running block asks for the index of one that has not
+// started, which is then never started (cluster launch control).  So items go
+// out in order, without a counter in memory that something would have to
+// zero first.
+__device__ __forceinline__ void next_block_ask(uint4* answer, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(answer)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// Its answer, once the barrier has completed: a block index, -1 if all have started.
+__device__ __forceinline__ int next_block_answer(const uint4* answer) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "mov.s32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+      : "=r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  fence_proxy_async_smem();   // read before the next answer is written there
+  return x;
+}
 
 // makes a tensor map that a kernel wrote to device memory usable by this
 // thread's TMA instructions
@@ -111,7 +150,7 @@ __device__ __forceinline__ void tensormap_acquire(const CUtensorMap* m) {
 
 constexpr int TF_TILE = 16384;                // one [128 rows][128 B] swizzled tile
 constexpr int TF_BUF = 2 * TF_TILE;           // 128 x 128 bf16 as two 64-column tiles
-constexpr int TF_SMEM = 6 * TF_BUF + 256;
+constexpr int TF_SMEM = 6 * TF_BUF + 288;
 constexpr float TF_RESCALE = 8.f;
 
 __device__ __forceinline__ float ex2_approx(float x) {
@@ -175,17 +214,16 @@ __device__ __forceinline__ FwdItem fwd_item(int n, int nq, int H, int Hkv, int k
   return it;
 }
 
-// A packed item as the TMA thread published it: batch row, head, first query
-// tile, first key block of tile A and of tile B (-1: no tile B).
-__device__ __forceinline__ FwdItem fwd_item_packed(const volatile int* f, int H, int Hkv, int kvs) {
+// A packed item as the TMA thread published it: head, first query tile, first
+// key block of tile A and of tile B (-1: no tile B).
+__device__ __forceinline__ FwdItem fwd_item_packed(const volatile int* f, int H, int Hkv) {
   FwdItem it;
-  const int b = f[0], h = f[1];
-  it.bh = b * H + h;
-  it.bkv = b * kvs + h / (H / Hkv);
-  it.qtA = f[2];
-  it.j0 = f[3];
-  it.hasB = f[4] >= 0;
-  it.oB = it.hasB ? f[4] - it.j0 : 0;
+  it.bh = f[0];
+  it.bkv = it.bh / (H / Hkv);
+  it.qtA = f[1];
+  it.j0 = f[2];
+  it.hasB = f[3] >= 0;
+  it.oB = it.hasB ? f[3] - it.j0 : 0;
   it.nkvA = it.qtA + 1 - it.j0;
   it.nkvB = it.hasB ? it.qtA + 2 - it.j0 : 0;
   it.nkv = it.hasB ? it.nkvB : it.nkvA;
@@ -279,14 +317,18 @@ __global__ void __launch_bounds__(384, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 17);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* item_ring = reinterpret_cast<volatile int*>(tmem_holder + 2);   // [4]
-  volatile int* item_info = item_ring + 4;   // [4][6], packed items: fwd_item_packed's fields
+  volatile int* item_info = item_ring + 4;   // [4][4], packed items: fwd_item_packed's fields
+  uint4* answer = reinterpret_cast<uint4*>(sm + 6 * TF_BUF + 256);   // packed: next_block_ask's
+  uint64_t* answered = reinterpret_cast<uint64_t*>(answer + 1);
 
   const int warp = warp_id(), lane = lane_id();
   const int nq = (T + 127) / 128;
   const long long wlim = wait_limit_or_default(wait_cycles);
-  const int Tv = kPacked ? pk.ctl[kCtlValid] : T;   // positions of a row that hold sequences
+  // positions that hold sequences; a plan of another T is refused
+  const bool fits = !kPacked || (pk.meta[kMetaMagic] == kPlanMagic && pk.meta[kMetaT] == T);
+  const int Tv = !kPacked ? T : fits ? pk.meta[kMetaTotal] : 0;
   auto item_of = [&](int n, int idx) -> FwdItem {
-    if constexpr (kPacked) return fwd_item_packed(item_info + 6 * (n & 3), H, Hkv, kvs);
+    if constexpr (kPacked) return fwd_item_packed(item_info + 4 * (n & 3), H, Hkv);
     else return fwd_item(idx, nq, H, Hkv, kvs, wl);
   };
 
@@ -299,13 +341,15 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 128); mbar_init(&pv_done[i], 1);
     }
     mbar_init(drain, 1);
+    if constexpr (kPacked) {
+      mbar_init(answered, 1);
+      if (!fits && blockIdx.x == 0 && err) atomicOr(err, ERRF_SHAPE);
+    }
     *abort_flag = 0;
     fence_barrier_init();
-    if constexpr (!kPacked) {
-      tma_prefetch_desc(&tq);
-      tma_prefetch_desc(&tk);
-      tma_prefetch_desc(&tv);
-    }
+    tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
   }
   if (warp == 1) {
     tmem_alloc(tmem_holder, 512);
@@ -320,33 +364,37 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 0) {
     if (lane == 0) {
       // -------------------------------------------------------------- TMA
-      const CUtensorMap* mq = kPacked ? pk.maps : &tq;
-      const CUtensorMap* mk = kPacked ? pk.maps + 1 : &tk;
-      const CUtensorMap* mv = kPacked ? pk.maps + 2 : &tv;
-      int entries = 0;
-      if constexpr (kPacked) {
-        tensormap_acquire(mq);
-        tensormap_acquire(mk);
-        tensormap_acquire(mv);
-        entries = pk.ctl[kCtlEntries];
-        n_items = entries * H;
-      }
       // Packed: item number and fields are fetched one item ahead, so that the
-      // counter's and the plan's latency hides behind the previous item's loads.
-      int nx_idx = -1, nx_qt = 0, nx_b = 0, nx_h = 0, nx_a = 0, nx_c = -1;
-      auto take = [&] {
-        nx_idx = atomicAdd(sched, 1);
-        if (nx_idx >= n_items) { nx_idx = -1; return; }
-        const int npairs = (nq + 1) / 2;
-        nx_h = nx_idx / entries;
-        const int e = pk.order[nx_idx - nx_h * entries];
-        nx_b = e / npairs;
-        nx_qt = 2 * (e - nx_b * npairs);
-        const int* lor = pk.lo + static_cast<long long>(nx_b) * T + nx_qt * 128;
-        nx_a = lor[0] >> 7;
-        nx_c = (nx_qt + 1) * 128 < Tv ? lor[128] >> 7 : -1;
+      // answer's and the plan's latency hides behind the current item's loads.
+      int nx_idx = -1, nx_h = 0, entries = 0;
+      int4 nx = make_int4(0, 0, -1, 0);
+      bool asked = false;
+      uint32_t answers = 0;
+      auto fetch = [&](int idx) {   // false: a block without work (more pairs than the sequences fill)
+        if (idx >= n_items) return false;
+        nx_idx = idx;
+        nx_h = idx / entries;
+        nx = __ldg(pk.fwd + (idx - nx_h * entries));
+        return true;
       };
-      if constexpr (kPacked) take();
+      auto take = [&] {   // false: the wait expired
+        nx_idx = -1;
+        while (asked) {
+          if (!mbar_wait_t<kFine>(answered, answers & 1, abort_flag, err, wlim)) return false;
+          ++answers;
+          asked = false;
+          const int idx = next_block_answer(answer);
+          if (idx < 0 || fetch(idx)) break;
+          next_block_ask(answer, answered);
+          asked = true;
+        }
+        return true;
+      };
+      if constexpr (kPacked) {
+        entries = fits ? pk.meta[kMetaFwd] : 0;
+        n_items = entries * H;
+        fetch(blockIdx.x);
+      }
       bool ok = true;
       int g = 0, last_q = -1;   // ring position of the next K/V block; last item whose Q was loaded
       for (int n = 0;; ++n) {
@@ -355,8 +403,12 @@ __global__ void __launch_bounds__(384, 1)
         int idx;
         if constexpr (kPacked) {
           idx = nx_idx;
-          volatile int* f = item_info + 6 * (n & 3);
-          f[0] = nx_b; f[1] = nx_h; f[2] = nx_qt; f[3] = nx_a; f[4] = nx_c;
+          volatile int* f = item_info + 4 * (n & 3);
+          f[0] = nx_h; f[1] = nx.x; f[2] = nx.y; f[3] = nx.z;
+          if (idx >= 0) {
+            next_block_ask(answer, answered);
+            asked = true;
+          }
         } else {
           idx = sched ? atomicAdd(sched, 1) : n * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
           if (idx >= n_items) idx = -1;
@@ -368,22 +420,21 @@ __global__ void __launch_bounds__(384, 1)
         }
         const FwdItem it = item_of(n, idx);
         mbar_arrive_expect_tx(q_full, it.hasB ? 2 * TF_BUF : TF_BUF);
-        tma_load_3d(sQ, mq, q_full, 0, it.qtA * 128, it.bh);
-        tma_load_3d(sQ + TF_TILE, mq, q_full, 64, it.qtA * 128, it.bh);
+        tma_load_3d(sQ, &tq, q_full, 0, it.qtA * 128, it.bh);
+        tma_load_3d(sQ + TF_TILE, &tq, q_full, 64, it.qtA * 128, it.bh);
         if (it.hasB) {
-          tma_load_3d(sQ + TF_BUF, mq, q_full, 0, it.qtA * 128 + 128, it.bh);
-          tma_load_3d(sQ + TF_BUF + TF_TILE, mq, q_full, 64, it.qtA * 128 + 128, it.bh);
+          tma_load_3d(sQ + TF_BUF, &tq, q_full, 0, it.qtA * 128 + 128, it.bh);
+          tma_load_3d(sQ + TF_BUF + TF_TILE, &tq, q_full, 64, it.qtA * 128 + 128, it.bh);
         }
         last_q = n;
-        if constexpr (kPacked) take();
         for (int j = 0; j < it.nkv; ++j) {
           const int s = g & 1;
           const uint32_t par = (g >> 1) & 1;
           const int kc = (it.j0 + j) * 128;
           if (!mbar_wait_t<kFine>(&k_empty[s], par ^ 1u, abort_flag, err, wlim)) { ok = false; break; }
           mbar_arrive_expect_tx(&k_full[s], TF_BUF);
-          tma_load_3d(sK + s * TF_BUF, mk, &k_full[s], 0, kc, it.bkv);
-          tma_load_3d(sK + s * TF_BUF + TF_TILE, mk, &k_full[s], 64, kc, it.bkv);
+          tma_load_3d(sK + s * TF_BUF, &tk, &k_full[s], 0, kc, it.bkv);
+          tma_load_3d(sK + s * TF_BUF + TF_TILE, &tk, &k_full[s], 64, kc, it.bkv);
           if (!mbar_wait_t<kFine>(&v_empty[s], par ^ 1u, abort_flag, err, wlim)) {
             // K of this block is in flight: count it, V is not
             for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(&k_full[s], par); ++i) {}
@@ -391,14 +442,19 @@ __global__ void __launch_bounds__(384, 1)
             break;
           }
           mbar_arrive_expect_tx(&v_full[s], TF_BUF);
-          tma_load_3d(sV + s * TF_BUF, mv, &v_full[s], 0, kc, it.bkv);
-          tma_load_3d(sV + s * TF_BUF + TF_TILE, mv, &v_full[s], 64, kc, it.bkv);
+          tma_load_3d(sV + s * TF_BUF, &tv, &v_full[s], 0, kc, it.bkv);
+          tma_load_3d(sV + s * TF_BUF + TF_TILE, &tv, &v_full[s], 64, kc, it.bkv);
           ++g;
+          if constexpr (kPacked)
+            if (j == 0 && !take()) { ok = false; break; }
         }
         if (!ok) break;
       }
       if (!ok) {
         // let the copies already started land before the CTA exits
+        if constexpr (kPacked)
+          if (asked)
+            for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(answered, answers & 1); ++i) {}
         if (last_q >= 0)
           for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(q_full, last_q & 1); ++i) {}
         for (int x = (g > 2 ? g - 2 : 0); x < g; ++x) {
@@ -472,6 +528,16 @@ __global__ void __launch_bounds__(384, 1)
           const int s = gj & 1;
           const int s1 = (gj + 1) & 1;
           if (!wait1(&v_full[s], (gj >> 1) & 1)) { ok = false; break; }
+          if constexpr (kPacked) {
+            const int past = Tv - (it.j0 + j) * 128;   // rows of V from here on belong to no sequence
+            if (Tv < T && past < 128) {
+              for (int x = past * 16 + lane; x < 128 * 16; x += 32)
+                *reinterpret_cast<uint4*>(sV + s * TF_BUF + ((x >> 3) & 1) * TF_TILE + (x >> 4) * 128 + (x & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
           if (j + 1 < it.nkv && !wait1(&k_full[s1], ((gj + 1) >> 1) & 1)) { ok = false; break; }
           // per tile: O += P V_j, then S of the next block over P once that product
           // has read it (tile B's softmax trails tile A's, so A goes first)
@@ -533,7 +599,7 @@ __global__ void __launch_bounds__(384, 1)
       const int j_first = kPacked && tile ? it.oB : 0;
       int lo = 0, lo_max = 0;   // packed: first key of this row, and the largest of the warp's rows
       if constexpr (kPacked) {
-        if (q < Tv) lo = __ldg(pk.lo + static_cast<long long>(it.bh / H) * T + q);
+        if (q < Tv) lo = __ldg(pk.lo + q);
         lo_max = __reduce_max_sync(0xffffffffu, lo);
       }
       float m_ref = -INFINITY, l = 0.f;   // reference max (log2 units) and row sum relative to it
@@ -871,17 +937,16 @@ __device__ __forceinline__ BwdBlock bwd_block(int idx, int H, int Hkv, int kvs, 
   return k;
 }
 
-// A packed item as the TMA thread published it: batch row, kv head, key
-// block, number of query blocks that see it.
-__device__ __forceinline__ BwdBlock bwd_block_packed(const volatile int* f, int H, int Hkv, int kvs) {
+// A packed item as the TMA thread published it: kv head, key block, number of
+// query blocks that see it.
+__device__ __forceinline__ BwdBlock bwd_block_packed(const volatile int* f, int H, int Hkv) {
   BwdBlock k;
-  k.b = f[0];
-  k.hk = f[1];
-  k.j = f[2];
-  k.nb = f[3];
+  k.b = 0;
+  k.hk = f[0];
+  k.j = f[1];
+  k.nb = f[2];
   k.k0 = k.j * 128;
-  k.bkv = k.b * Hkv + k.hk;
-  k.kvrow = k.b * kvs + k.hk;
+  k.bkv = k.kvrow = k.hk;
   k.G = H / Hkv;
   k.n_it = k.G * k.nb;
   return k;
@@ -938,7 +1003,7 @@ __global__ void __launch_bounds__(512, 1)
   const long long wlim = wait_limit_or_default(wait_cycles);
   const int Tv = kPacked ? pa.ctl[kCtlValid] : T;   // positions of a row that hold sequences
   auto block_of = [&](int n, int idx) -> BwdBlock {
-    if constexpr (kPacked) return bwd_block_packed(item_info + 4 * (n & 3), H, Hkv, kvs);
+    if constexpr (kPacked) return bwd_block_packed(item_info + 4 * (n & 3), H, Hkv);
     else return bwd_block(idx, H, Hkv, kvs, nq, wl);
   };
 
@@ -996,16 +1061,13 @@ __global__ void __launch_bounds__(512, 1)
         n_units = entries * Hkv;
       }
       // packed: fetched one item ahead, as in the forward
-      int nx_idx = -1, nx_b = 0, nx_hk = 0, nx_j = 0, nx_nb = 0;
+      int nx_idx = -1, nx_hk = 0;
+      int2 nx = make_int2(0, 0);
       auto take = [&] {
         nx_idx = atomicAdd(sched, 1);
         if (nx_idx >= n_units) { nx_idx = -1; return; }
         nx_hk = nx_idx / entries;
-        const int e = pa.order[nx_idx - nx_hk * entries];
-        nx_b = e / nq;
-        nx_j = e - nx_b * nq;
-        // hi grows with the key: the block's last key is seen furthest
-        nx_nb = (pa.hi[static_cast<long long>(nx_b) * T + min(nx_j * 128 + 127, Tv - 1)] >> 7) - nx_j + 1;
+        nx = __ldg(pa.bwd + (nx_idx - nx_hk * entries));
       };
       if constexpr (kPacked) take();
       bool ok = true;
@@ -1038,7 +1100,7 @@ __global__ void __launch_bounds__(512, 1)
         if constexpr (kPacked) {
           idx = nx_idx;
           volatile int* f = item_info + 4 * (n & 3);
-          f[0] = nx_b; f[1] = nx_hk; f[2] = nx_j; f[3] = nx_nb;
+          f[0] = nx_hk; f[1] = nx.x; f[2] = nx.y;
         } else if (idx < 0) {
           const int unit = sched ? atomicAdd(sched, 1) : taken * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
           ++taken;
@@ -1319,7 +1381,7 @@ __global__ void __launch_bounds__(512, 1)
         const bool key_ok = key < Tv;
         int hi = 0, hi_min = 0, hi_max = 0;   // packed: last query that sees this key, and over the warp's keys
         if constexpr (kPacked) {
-          hi = key_ok ? __ldg(pa.hi + static_cast<long long>(kb.b) * T + key) : -1;
+          hi = key_ok ? __ldg(pa.hi + key) : -1;
           hi_min = __reduce_min_sync(0xffffffffu, hi);
           hi_max = __reduce_max_sync(0xffffffffu, hi);
         }
@@ -1674,193 +1736,156 @@ __global__ void attn_bwd_dot_kernel(const bf16* __restrict__ o, const bf16* __re
 
 // --------------------------------------------------- packed: plan and setup
 
-// The plan's layout in int32 words: kPlanMeta words (total positions held by
-// sequences, forward and backward entry counts, B, T, positions past the
-// sequences covered), lo and hi [B * T], forward order [B * npairs], backward
-// order [B * nblocks].
-enum { kMetaTotal = 0, kMetaFwd = 1, kMetaBwd = 2, kMetaB = 3, kMetaT = 4, kMetaMagic = 5, kPlanMeta = 64 };
-constexpr int kPlanMagic = 0x5e91a7e;
+// A plan: kPlanMeta words, lo and hi [T], forward entries [pairs of tiles],
+// backward entries [key blocks].
 struct PlanView {
   int* meta;
   int* lo;
   int* hi;
-  int* fwd;
-  int* bwd;
-  size_t words;
+  int4* fwd;
+  int2* bwd;
+  size_t bytes;
 };
-__host__ __device__ inline PlanView plan_view(void* base, int B, int T) {
-  const size_t n = static_cast<size_t>(B) * T, nq = (T + 127) / 128;
+__host__ __device__ inline PlanView plan_view(void* base, int T) {
+  const size_t n = (static_cast<size_t>(T) + 3) / 4 * 4, nq = (static_cast<size_t>(T) + 127) / 128;
   int* p = static_cast<int*>(base);
   PlanView v;
   v.meta = p;
   v.lo = p + kPlanMeta;
   v.hi = v.lo + n;
-  v.fwd = v.hi + n;
-  v.bwd = v.fwd + B * ((nq + 1) / 2);
-  v.words = kPlanMeta + 2 * n + B * ((nq + 1) / 2) + B * nq;
+  v.fwd = reinterpret_cast<int4*>(v.hi + n);
+  v.bwd = reinterpret_cast<int2*>(v.fwd + (nq + 1) / 2);
+  v.bytes = (kPlanMeta + 2 * n) * sizeof(int) + (nq + 1) / 2 * sizeof(int4) + nq * sizeof(int2);
   return v;
 }
 
-// Sequence of position p, row-local: [start, end) within p's row of T
-// positions (a sequence that crosses a row's end is split there).  Offsets
-// that are not in order give some range that still holds p.
+// Sequence [start, end) of position p < total.  Offsets that are not in order
+// give some range that still holds p.
 struct SeqRange { int start, end; };
-__device__ __forceinline__ SeqRange seq_range(const int* __restrict__ cu, int n_seq, int total, int B, int T, int p) {
-  int a = total, b = B * T;   // past the last sequence: one more
-  if (p < total && n_seq > 0) {
-    int l = 0, r = n_seq - 1;   // the last s with cu[s] <= p
-    while (l < r) {
-      const int m = (l + r + 1) >> 1;
-      if (__ldg(cu + m) <= p) l = m;
-      else r = m - 1;
-    }
-    a = __ldg(cu + l);
-    b = __ldg(cu + l + 1);
+__device__ __forceinline__ SeqRange seq_range(const int* cu, int n_seq, int T, int p) {
+  int l = 0, r = n_seq - 1;   // the last s with cu[s] <= p
+  while (l < r) {
+    const int m = (l + r + 1) >> 1;
+    if (cu[m] <= p) l = m;
+    else r = m - 1;
   }
-  const int row = p / T * T;
-  SeqRange s;
-  s.start = max(0, min(a, p) - row);
-  s.end = min(T, max(b, p + 1) - row);
-  return s;
+  return SeqRange{max(0, min(cu[l], p)), min(T, max(cu[l + 1], p + 1))};
 }
 
-// Blocks past the first fill lo and hi; the first checks the offsets (in
-// order, from 0, at most B * T; otherwise nothing is covered and the error is
-// latched), and sorts the work entries of both directions by their number of
-// 128 x 128 blocks with a counting sort (longest first; entries of one length
-// in no fixed order, which no output of the forward depends on).
+// Blocks from the third on fill lo and hi; the first two check the offsets (in
+// order, from 0, at most T; otherwise nothing is covered and the error is
+// latched) and sort the work entries, the first the forward's, the second the
+// backward's, by their number of 128 x 128 steps with a counting sort (longest
+// first; entries of one length in no fixed order, which no output of the
+// forward depends on).  Bound by latency: the offsets are searched in shared
+// memory (up to kPlanSeqs; 4.4 us instead of 7.5 for 46 sequences).
+constexpr int kPlanSeqs = 4095;
 __global__ void __launch_bounds__(1024)
-    attention_plan_kernel(const int* __restrict__ cu, int n_seq, int B, int T, int window, int cover, void* plan,
-                          int* err) {
-  const PlanView P = plan_view(plan, B, T);
-  const int n = B * T;
-  const int last = n_seq > 0 ? __ldg(cu + n_seq) : 0;
-  const int total = max(0, min(last, n));
-  const int wl = window < 0 ? n : window;
-  if (blockIdx.x > 0) {
-    const int p = (blockIdx.x - 1) * blockDim.x + threadIdx.x;
-    if (p >= n) return;
-    const int t = p % T;
-    int lo = 0, hi = -1;
-    if (p < total || cover) {
-      const SeqRange s = seq_range(cu, n_seq, total, B, T, p);
-      lo = max(s.start, t - min(wl, t));
-      hi = min(s.end - 1, t + min(wl, T - 1 - t));
-    }
-    P.lo[p] = lo;
-    P.hi[p] = hi;
-    return;
-  }
+    attention_plan_kernel(const int* __restrict__ cu_arg, int n_seq, int T, int window, void* plan, int* err) {
   constexpr int kBuckets = 1024;
+  __shared__ int cu_s[kPlanSeqs + 1];
   __shared__ int hist[kBuckets];
   __shared__ int warp_total[32];
-  int bad = (n_seq > 0 && __ldg(cu) != 0) || last > n;
-  for (int i = threadIdx.x; i < n_seq; i += blockDim.x) bad |= __ldg(cu + i + 1) < __ldg(cu + i);
+  const PlanView P = plan_view(plan, T);
+  const int wl = window < 0 ? T : window, tid = threadIdx.x;
+  const int* cu = cu_arg;
+  if (n_seq <= kPlanSeqs) {
+    for (int i = tid; i <= n_seq; i += 1024) cu_s[i] = cu_arg[i];
+    hist[tid] = 0;
+    __syncthreads();
+    cu = cu_s;
+  } else {
+    hist[tid] = 0;
+  }
+  const int last = n_seq > 0 ? cu[n_seq] : 0, total = max(0, min(last, T));
+  auto lo_of = [&](int t) { return max(seq_range(cu, n_seq, T, t).start, t - min(wl, t)); };
+  auto hi_of = [&](int t) { return min(seq_range(cu, n_seq, T, t).end - 1, t + min(wl, T - 1 - t)); };
+  if (blockIdx.x > 1) {
+    const int t = (blockIdx.x - 2) * 1024 + tid;
+    if (t >= T) return;
+    P.lo[t] = t < total ? lo_of(t) : 0;
+    P.hi[t] = t < total ? hi_of(t) : -1;
+    return;
+  }
+  const int dir = blockIdx.x;
+  int bad = (n_seq > 0 && cu[0] != 0) || last > T;
+  for (int i = tid; i < n_seq; i += 1024) bad |= cu[i + 1] < cu[i];
   bad = __syncthreads_or(bad);
-  const int valid = bad ? 0 : cover ? n : total;
-  if (threadIdx.x == 0) {
+  const int valid = bad ? 0 : total;
+  if (dir == 0 && tid == 0) {
     if (bad && err) atomicOr(err, ERRF_SEQUENCE);
     P.meta[kMetaTotal] = valid;
-    P.meta[kMetaB] = B;
     P.meta[kMetaT] = T;
     P.meta[kMetaMagic] = kPlanMagic;
   }
-  const int nq = (T + 127) / 128, npairs = (nq + 1) / 2;
-  for (int dir = 0; dir < 2; ++dir) {
-    const int per_row = dir ? nq : npairs, count = B * per_row;
-    // blocks of entry e: 0 if it holds no position of a sequence
-    auto cost = [&](int e) -> int {
-      const int b = e / per_row, i = e - b * per_row, r0 = b * T;
-      const int tv = max(0, min(T, valid - r0));
-      if (dir) {
-        const int k0 = i * 128;
-        if (k0 >= tv) return 0;
-        const int k = min(k0 + 127, tv - 1);
-        const SeqRange s = seq_range(cu, n_seq, total, B, T, r0 + k);
-        return (min(s.end - 1, k + min(wl, T - 1 - k)) >> 7) - i + 1;
-      }
-      int c = 0;
-      for (int qt = 2 * i; qt < 2 * i + 2; ++qt) {
-        const int q = qt * 128;
-        if (q >= tv) break;
-        const SeqRange s = seq_range(cu, n_seq, total, B, T, r0 + q);
-        c += qt + 1 - (max(s.start, q - min(wl, q)) >> 7);
-      }
-      return c;
-    };
-    for (int i = threadIdx.x; i < kBuckets; i += blockDim.x) hist[i] = 0;
-    __syncthreads();
-    for (int e = threadIdx.x; e < count; e += blockDim.x) {
-      const int c = cost(e);
-      if (c > 0) atomicAdd(&hist[kBuckets - min(c, kBuckets)], 1);
+  const int nb = (valid + 127) / 128, count = dir ? nb : (nb + 1) / 2;
+  // entry e; w: its steps
+  auto entry = [&](int e) -> int4 {
+    if (dir) {
+      const int n = (hi_of(min(e * 128 + 127, valid - 1)) >> 7) - e + 1;   // hi grows with the key
+      return make_int4(e, n, 0, n);
     }
-    __syncthreads();
-    // exclusive sums of the 1024 buckets, one per thread
-    const int mine = hist[threadIdx.x];
-    int x = mine;
+    const int qt = 2 * e, a = lo_of(qt * 128) >> 7, b = qt + 1 < nb ? lo_of(qt * 128 + 128) >> 7 : -1;
+    return make_int4(qt, a, b, (b >= 0 ? qt + 2 : qt + 1) - a);
+  };
+  const int4 mine = tid < count ? entry(tid) : make_int4(0, 0, 0, 0);
+  for (int e = tid; e < count; e += 1024)
+    atomicAdd(&hist[kBuckets - min((e == tid ? mine : entry(e)).w, kBuckets)], 1);
+  __syncthreads();
+  // exclusive sums of the 1024 buckets, one per thread
+  const int in_bucket = hist[tid];
+  int x = in_bucket;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane_id() >= o) x += y;
-    }
-    if (lane_id() == 31) warp_total[warp_id()] = x;
-    __syncthreads();
-    if (warp_id() == 0) {
-      int w = warp_total[lane_id()];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane_id() >= o) w += y;
-      }
-      warp_total[lane_id()] = w;
-    }
-    __syncthreads();
-    const int before = x - mine + (warp_id() ? warp_total[warp_id() - 1] : 0);
-    if (threadIdx.x == 0) P.meta[dir ? kMetaBwd : kMetaFwd] = warp_total[31];
-    hist[threadIdx.x] = before;
-    __syncthreads();
-    int* order = dir ? P.bwd : P.fwd;
-    for (int e = threadIdx.x; e < count; e += blockDim.x) {
-      const int c = cost(e);
-      if (c > 0) order[atomicAdd(&hist[kBuckets - min(c, kBuckets)], 1)] = e;
-    }
-    __syncthreads();
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane_id() >= o) x += y;
+  }
+  if (lane_id() == 31) warp_total[warp_id()] = x;
+  __syncthreads();
+  int before = x - in_bucket;
+  for (int w = 0; w < warp_id(); ++w) before += warp_total[w];
+  if (tid == 0) P.meta[dir ? kMetaBwd : kMetaFwd] = count;
+  hist[tid] = before;
+  __syncthreads();
+  for (int e = tid; e < count; e += 1024) {
+    const int4 v = e == tid ? mine : entry(e);
+    const int at = atomicAdd(&hist[kBuckets - min(v.w, kBuckets)], 1);
+    if (dir) P.bwd[at] = make_int2(v.x, v.y);
+    else P.fwd[at] = make_int4(v.x, v.y, v.z, 0);
   }
 }
 
-// Control words and tensor maps of one packed launch, by one warp.  A plan
-// made for another shape is refused: no entries, the error latched.
+// Control words and tensor maps of one packed backward, by one warp.  A plan
+// made for another T is refused: no entries, the error latched.
 struct SetupMaps {
   CUtensorMap m[4];
 };
-__device__ __forceinline__ void packed_setup(const SetupMaps& in, int n_maps, CUtensorMap* out, int* ctl,
-                                             const int* meta, int B, int T, int dir, int* err,
-                                             CUtensorMap* stage) {
+__device__ __forceinline__ void packed_setup(const SetupMaps& in, CUtensorMap* out, int* ctl, const int* meta, int T,
+                                             int* err, CUtensorMap* stage) {
   const int lane = lane_id();
-  const bool fits = meta[kMetaMagic] == kPlanMagic && meta[kMetaB] == B && meta[kMetaT] == T;
-  const int valid = fits ? (B == 1 ? meta[kMetaTotal] : T) : 0;
+  const bool fits = meta[kMetaMagic] == kPlanMagic && meta[kMetaT] == T;
+  const int valid = fits ? meta[kMetaTotal] : 0;
   if (lane == 0) {
     if (!fits && err) atomicOr(err, ERRF_SHAPE);
     ctl[kCtlSched] = 0;
-    ctl[kCtlEntries] = fits ? meta[dir ? kMetaBwd : kMetaFwd] : 0;
+    ctl[kCtlEntries] = fits ? meta[kMetaBwd] : 0;
     ctl[kCtlValid] = valid;
   }
-  for (int i = 0; i < n_maps; ++i)
+  for (int i = 0; i < 4; ++i)
     reinterpret_cast<uint32_t*>(&stage[i])[lane] = reinterpret_cast<const uint32_t*>(&in.m[i])[lane];
   __syncwarp();
-  if (lane == 0 && B == 1 && valid > 0 && valid < T) {
+  if (lane == 0 && valid > 0 && valid < T) {
     // the token extent (dimension 1 of q, k, v; 2 of dO) ends with the sequences
-    for (int i = 0; i < n_maps; ++i) {
-      if (i < 3)
-        asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(
-                         smem_u32(&stage[i])), "r"(valid) : "memory");
-      else
-        asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 2, %1;" ::"r"(
-                         smem_u32(&stage[i])), "r"(valid) : "memory");
-    }
+    for (int i = 0; i < 3; ++i)
+      asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(smem_u32(&stage[i])),
+                   "r"(valid)
+                   : "memory");
+    asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 2, %1;" ::"r"(smem_u32(&stage[3])),
+                 "r"(valid)
+                 : "memory");
   }
   __syncwarp();
-  for (int i = 0; i < n_maps; ++i)
+  for (int i = 0; i < 4; ++i)
     asm volatile(
         "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::"l"(
             out + i),
@@ -1868,14 +1893,7 @@ __device__ __forceinline__ void packed_setup(const SetupMaps& in, int n_maps, CU
         : "memory");
 }
 
-__global__ void __launch_bounds__(32)
-    attention_setup_kernel(const __grid_constant__ SetupMaps in, CUtensorMap* out, int* ctl, const int* meta, int B,
-                           int T, int* err) {
-  __shared__ __align__(128) CUtensorMap stage[4];
-  packed_setup(in, 3, out, ctl, meta, B, T, 0, err, stage);
-}
-
-// Backward: D[b, h, t] = sum_i dO * O of the rows that hold sequences and
+// Backward: D[h, t] = sum_i dO * O of the rows that hold sequences and
 // zeros in the fp32 dq accumulator, some (t, h) rows a warp, whose loads are
 // issued together; the first block does the setup.
 constexpr int kRowsPerWarp = 4;
@@ -1886,25 +1904,25 @@ __global__ void __launch_bounds__(256)
                                 float* __restrict__ Dv, float* __restrict__ dq, int H, int T, int* err) {
   __shared__ __align__(128) CUtensorMap stage[4];
   if (blockIdx.x == 0) {
-    if (warp_id() == 0) packed_setup(in, 4, out, ctl, meta, 1, T, 1, err, stage);
+    if (warp_id() == 0) packed_setup(in, out, ctl, meta, T, err, stage);
     return;
   }
   if (meta[kMetaMagic] != kPlanMagic || meta[kMetaT] != T) return;
-  const long long rows = static_cast<long long>(meta[kMetaTotal]) * H;
-  const long long w = (static_cast<long long>(blockIdx.x - 1) * 8 + warp_id()) * kRowsPerWarp;
+  // T * H fits in an int
+  const int rows = meta[kMetaTotal] * H, w = ((blockIdx.x - 1) * 8 + warp_id()) * kRowsPerWarp;
   uint2 x[kRowsPerWarp], y[kRowsPerWarp];
 #pragma unroll
   for (int i = 0; i < kRowsPerWarp; ++i) {
-    if (w + i >= rows) break;
-    const long long t = (w + i) / H, h = w + i - t * H;
+    if (w >= rows - i) break;
+    const int t = (w + i) / H, h = w + i - t * H;
     x[i] = *reinterpret_cast<const uint2*>(o + t * o_tok + h * o_head + lane_id() * 4);
     y[i] = *reinterpret_cast<const uint2*>(dout + t * do_tok + h * do_head + lane_id() * 4);
   }
 #pragma unroll
   for (int i = 0; i < kRowsPerWarp; ++i) {
-    if (w + i >= rows) break;
-    const long long t = (w + i) / H, h = w + i - t * H, row = h * T + t;
-    reinterpret_cast<float4*>(dq + row * HD)[lane_id()] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (w >= rows - i) break;
+    const int t = (w + i) / H, h = w + i - t * H, row = h * T + t;
+    reinterpret_cast<float4*>(dq + static_cast<long long>(row) * HD)[lane_id()] = make_float4(0.f, 0.f, 0.f, 0.f);
     float s = bf16_lo(x[i].x) * bf16_lo(y[i].x) + bf16_hi(x[i].x) * bf16_hi(y[i].x) + bf16_lo(x[i].y) * bf16_lo(y[i].y) +
               bf16_hi(x[i].y) * bf16_hi(y[i].y);
     s = warp_sum(s);
@@ -1916,19 +1934,18 @@ __global__ void __launch_bounds__(256)
 __global__ void __launch_bounds__(256)
     attention_packed_dq_kernel(const float* __restrict__ acc, bf16* __restrict__ dq, long long dq_tok,
                                long long dq_head, const int* ctl, int H, int T) {
-  const long long rows = static_cast<long long>(ctl[kCtlValid]) * H;
-  const long long w = (static_cast<long long>(blockIdx.x) * 8 + warp_id()) * kRowsPerWarp;
+  const int rows = ctl[kCtlValid] * H, w = (blockIdx.x * 8 + warp_id()) * kRowsPerWarp;
   float4 v[kRowsPerWarp];
 #pragma unroll
   for (int i = 0; i < kRowsPerWarp; ++i) {
-    if (w + i >= rows) break;
-    const long long t = (w + i) / H, h = w + i - t * H;
-    v[i] = reinterpret_cast<const float4*>(acc + (h * T + t) * HD)[lane_id()];
+    if (w >= rows - i) break;
+    const int t = (w + i) / H, h = w + i - t * H;
+    v[i] = reinterpret_cast<const float4*>(acc + static_cast<long long>(h * T + t) * HD)[lane_id()];
   }
 #pragma unroll
   for (int i = 0; i < kRowsPerWarp; ++i) {
-    if (w + i >= rows) break;
-    const long long t = (w + i) / H, h = w + i - t * H;
+    if (w >= rows - i) break;
+    const int t = (w + i) / H, h = w + i - t * H;
     uint2 u;
     u.x = pack_bf16x2(v[i].x, v[i].y);
     u.y = pack_bf16x2(v[i].z, v[i].w);
@@ -2049,46 +2066,38 @@ bool map_heads(CUtensorMap* m, const PackedTensor& t, long long tokens, long lon
 
 }  // namespace
 
-size_t attention_plan_bytes(int B, int T) { return al256(plan_view(nullptr, B, T).words * sizeof(int)); }
+size_t attention_plan_bytes(int T) { return al256(plan_view(nullptr, T).bytes); }
 
-size_t attention_packed_scratch(int T, int H, bool backward) {
+size_t attention_packed_bwd_scratch(int T, int H) {
   const size_t rows = static_cast<size_t>(T) * H;
-  return al256(kPackedHead) + (backward ? al256(rows * sizeof(float)) + al256(rows * HD * sizeof(float)) : 0);
+  return al256(kPackedHead) + al256(rows * sizeof(float)) + al256(rows * HD * sizeof(float));
 }
 
-void launch_attention_plan(const int* cu, int n_seq, int B, int T, int window, bool cover, void* plan, int* err,
-                           cudaStream_t s) {
-  const int blocks = 1 + static_cast<int>((static_cast<long long>(B) * T + 1023) / 1024);
-  attention_plan_kernel<<<blocks, 1024, 0, s>>>(cu, n_seq, B, T, window, cover ? 1 : 0, plan, err);
+void launch_attention_plan(const int* cu, int n_seq, int T, int window, void* plan, int* err, cudaStream_t s) {
+  attention_plan_kernel<<<2 + (T + 1023) / 1024, 1024, 0, s>>>(cu, n_seq, T, window, plan, err);
 }
 
 cudaError_t launch_attn_packed_fwd(const PackedTensor& q, const PackedTensor& k, const PackedTensor& v,
                                    const PackedTensor& o, float* lse, int H, int Hkv, int T, float scale,
-                                   const void* plan, void* scratch, cudaStream_t s, int* err, long long wait_cycles) {
+                                   const void* plan, cudaStream_t s, int* err, long long wait_cycles) {
   const bool fine = wait_limit_or_default(wait_cycles) < kShortWaitCycles;
   auto kern = fine ? attn_fwd_tc_kernel<true, true> : attn_fwd_tc_kernel<false, true>;
   static std::atomic<unsigned long long> configured[2] = {};
   cudaError_t e = set_smem_limit_once(kern, TF_SMEM, configured[fine ? 1 : 0]);
   if (e != cudaSuccess) return e;
-  SetupMaps maps = {};
-  if (!map_heads(&maps.m[0], q, T, H) || !map_heads(&maps.m[1], k, T, Hkv) || !map_heads(&maps.m[2], v, T, Hkv))
+  CUtensorMap mq, mk, mv;
+  if (!map_heads(&mq, q, T, H) || !map_heads(&mk, k, T, Hkv) || !map_heads(&mv, v, T, Hkv))
     return cudaErrorInvalidValue;
-  const PlanView P = plan_view(const_cast<void*>(plan), 1, T);
-  int* ctl = static_cast<int*>(scratch);
-  CUtensorMap* dmaps = reinterpret_cast<CUtensorMap*>(static_cast<uint8_t*>(scratch) + 256);
-  attention_setup_kernel<<<1, 32, 0, s>>>(maps, dmaps, ctl, P.meta, 1, T, err);
+  const PlanView P = plan_view(const_cast<void*>(plan), T);
   PackedArgs pa = {};
+  pa.meta = P.meta;
   pa.lo = P.lo;
-  pa.hi = P.hi;
-  pa.order = P.fwd;
-  pa.ctl = ctl;
-  pa.maps = dmaps;
+  pa.fwd = P.fwd;
   pa.o_tok = o.tok;
   pa.o_head = o.head;
-  const long long items = 1ll * ((T + 127) / 128 + 1) / 2 * H;
-  const int grid = static_cast<int>(std::min<long long>(items, device_sm_count()));
-  kern<<<grid, 384, TF_SMEM, s>>>(maps.m[0], maps.m[1], maps.m[2], static_cast<bf16*>(const_cast<void*>(o.ptr)), lse, H, Hkv, Hkv, T, 1 << 30,
-                                  scale * 1.4426950408889634f, 0, ctl + kCtlSched, err, wait_cycles, pa);
+  const int items = ((T + 127) / 128 + 1) / 2 * H;   // a block each; most are taken over before they start
+  kern<<<items, 384, TF_SMEM, s>>>(mq, mk, mv, static_cast<bf16*>(const_cast<void*>(o.ptr)), lse, H, Hkv, Hkv, T,
+                                   1 << 30, scale * 1.4426950408889634f, 0, nullptr, err, wait_cycles, pa);
   return cudaGetLastError();
 }
 
@@ -2117,15 +2126,14 @@ cudaError_t launch_attn_packed_bwd(const PackedTensor& q, const PackedTensor& k,
       !make_map_4d(&maps.m[3], dout.ptr, dims, strides, box) ||
       !make_map(&mdq, acc, 4, HD, T, H, HD, 1ll * T * HD, 32, 32))
     return cudaErrorInvalidValue;
-  const PlanView P = plan_view(const_cast<void*>(plan), 1, T);
+  const PlanView P = plan_view(const_cast<void*>(plan), T);
   const int row_blocks = static_cast<int>((rows + 8 * kRowsPerWarp - 1) / (8 * kRowsPerWarp));
   attention_packed_pre_kernel<<<1 + row_blocks, 256, 0, s>>>(
       maps, dmaps, ctl, P.meta, static_cast<const bf16*>(o.ptr), o.tok, o.head, static_cast<const bf16*>(dout.ptr),
       dout.tok, dout.head, Dv, acc, H, T, err);
   PackedArgs pa = {};
-  pa.lo = P.lo;
   pa.hi = P.hi;
-  pa.order = P.bwd;
+  pa.bwd = P.bwd;
   pa.ctl = ctl;
   pa.maps = dmaps;
   pa.o_tok = dk.tok;

@@ -48,20 +48,18 @@ struct PackedTensor {
 };
 
 // The plan of a batch of sequences (cu [n_seq + 1], int32, device) that lie
-// end to end in B rows of T positions: masks and work order for the packed
-// kernels.  cover: positions past cu[n_seq] form one more sequence; otherwise
-// they are left alone.  Offsets that do not start at 0, decrease, or pass
-// B * T latch ERRF_SEQUENCE and plan no work.
-size_t attention_plan_bytes(int B, int T);
-void launch_attention_plan(const int* cu, int n_seq, int B, int T, int window, bool cover, void* plan, int* err,
-                           cudaStream_t s);
+// end to end in T positions: masks and work order for the packed kernels.
+// Positions past cu[n_seq] are left alone.  Offsets that do not start at 0,
+// decrease, or pass T latch ERRF_SEQUENCE and plan no work.
+size_t attention_plan_bytes(int T);
+void launch_attention_plan(const int* cu, int n_seq, int T, int window, void* plan, int* err, cudaStream_t s);
 
-// Packed attention over one row of T positions with a plan of B = 1.
+// Packed attention over the T positions of a plan.  T * H fits in an int.
 // cudaErrorInvalidValue: a tensor whose base or strides TMA cannot take.
-size_t attention_packed_scratch(int T, int H, bool backward);
 cudaError_t launch_attn_packed_fwd(const PackedTensor& q, const PackedTensor& k, const PackedTensor& v,
                                    const PackedTensor& o, float* lse, int H, int Hkv, int T, float scale,
-                                   const void* plan, void* scratch, cudaStream_t s, int* err, long long wait_cycles);
+                                   const void* plan, cudaStream_t s, int* err, long long wait_cycles);
+size_t attention_packed_bwd_scratch(int T, int H);
 cudaError_t launch_attn_packed_bwd(const PackedTensor& q, const PackedTensor& k, const PackedTensor& v,
                                    const PackedTensor& o, const PackedTensor& dout, const float* lse,
                                    const PackedTensor& dq, const PackedTensor& dk, const PackedTensor& dv, int H,

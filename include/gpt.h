@@ -471,23 +471,22 @@ int gpt_op_attention_plan(const int32_t* cu_seqlens, int n_seq, int n_tokens, in
  * (kv head h / (H / Hkv)) o_t = sum_j softmax_j(scale q_t . k_j) v_j over the
  * keys that t sees, and lse fp32 [H, n_tokens], the natural log of the
  * softmax denominator.  Rows past the last sequence are neither read nor
- * written.  Within a 128-position tile a NaN or infinity in k or v of one
- * sequence may reach the others of the tile.
+ * written.  Within a 128-position tile a NaN or infinity in an input of one
+ * sequence may reach the others of the tile, here and in the backward.
  *   scale    > 0, or 0 for 1 / sqrt(128)
  *   plan     made for the same n_tokens (another plan: nothing is written and
- *            gpt_op_check reports it)
- *   scratch  device buffer of gpt_op_attention_packed_scratch(n_tokens, H, 0)
- *            bytes, 256-byte aligned, of this call alone while it runs */
-size_t gpt_op_attention_packed_scratch(int n_tokens, int H, int backward);
+ *            gpt_op_check reports it) */
 int gpt_op_attention_packed_fwd(const gpt_heads* q, const gpt_heads* k, const gpt_heads* v, const gpt_heads* o,
                                 float* lse, int n_tokens, int H, int Hkv, float scale, const void* plan,
-                                void* scratch, void* stream);
+                                void* stream);
 
 /* Its backward: gradients of q, k and v (bf16; dk and dv summed over the
  * query heads of a kv head) from dout, with o and lse of the forward.  Sums
  * are held in fp32; those of dq add up in no fixed order, so two runs may
- * differ in its last bit.  scratch: gpt_op_attention_packed_scratch(n_tokens,
- * H, 1) bytes.  Outputs must not overlap each other or the inputs. */
+ * differ in its last bit.  Outputs must not overlap each other or the inputs.
+ *   scratch  device buffer of gpt_op_attention_packed_bwd_scratch(n_tokens, H)
+ *            bytes, 256-byte aligned, of this call alone while it runs */
+size_t gpt_op_attention_packed_bwd_scratch(int n_tokens, int H);
 int gpt_op_attention_packed_bwd(const gpt_heads* q, const gpt_heads* k, const gpt_heads* v, const gpt_heads* o,
                                 const float* lse, const gpt_heads* dout, const gpt_heads* dq, const gpt_heads* dk,
                                 const gpt_heads* dv, int n_tokens, int H, int Hkv, float scale, const void* plan,
