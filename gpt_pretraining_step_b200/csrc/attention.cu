@@ -150,7 +150,8 @@ __device__ __forceinline__ void tensormap_acquire(const CUtensorMap* m) {
 
 constexpr int TF_TILE = 16384;                // one [128 rows][128 B] swizzled tile
 constexpr int TF_BUF = 2 * TF_TILE;           // 128 x 128 bf16 as two 64-column tiles
-constexpr int TF_SMEM = 6 * TF_BUF + 288;
+constexpr int TF_STAGE = 16384;               // output rows, 2 KB for each softmax warp
+constexpr int TF_SMEM = 6 * TF_BUF + TF_STAGE + 288;
 constexpr float TF_RESCALE = 8.f;
 
 __device__ __forceinline__ float ex2_approx(float x) {
@@ -242,23 +243,38 @@ __device__ __forceinline__ void causal_mask_row(uint32_t (&sr)[128], int lane) {
   for (int k = 32 * (Q + 1); k < 128; ++k) sr[k] = __float_as_uint(-INFINITY);
 }
 
-// 64 bf16 values of each lane's row (w: packed pairs) to rows dst + row * pitch
-// (elements), row = 0 .. n_rows - 1 of the warp's 32, through 4 KB of shared
-// memory: eight lanes write one row's 128 bytes together.
-__device__ __forceinline__ void store_rows_64(uint8_t* stage, const uint32_t (&w)[32], bf16* dst, long long pitch,
-                                              int n_rows) {
+// kCols fp32 columns from TMEM times f, in bf16, of each lane's row to rows
+// dst + row * pitch (elements), row = 0 .. n_rows - 1 of the warp's 32, through
+// 64 kCols bytes of shared memory: kCols / 8 lanes write one row's values
+// together.  (With a lane for each row a store touched 32 cache lines.)
+template <int kCols>
+__device__ __forceinline__ void store_rows(uint32_t taddr, float f, uint8_t* stage, bf16* dst, long long pitch,
+                                           int n_rows) {
+  constexpr int kUnits = kCols / 8, kBytes = kCols * 2;   // of 16 bytes in a row; of a row
   const int lane = lane_id();
+  // unit u of row r lies at u ^ swap(r): eight lanes, or rows, meet 32 different banks
+  auto swap = [](int r) { return kUnits == 8 ? r & 7 : (r >> 1) & 3; };
+  uint32_t w[kCols / 2];
+#pragma unroll
+  for (int c = 0; c < kCols; c += 32) {
+    uint32_t x[32];
+    tmem_load32_async(taddr + c, x);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      w[c / 2 + k] = pack_bf16x2(__uint_as_float(x[2 * k]) * f, __uint_as_float(x[2 * k + 1]) * f);
+  }
   __syncwarp();   // the previous contents have been read
 #pragma unroll
-  for (int u = 0; u < 8; ++u)
-    *reinterpret_cast<uint4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) =
+  for (int u = 0; u < kUnits; ++u)
+    *reinterpret_cast<uint4*>(stage + lane * kBytes + ((u ^ swap(lane)) << 4)) =
         make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
   __syncwarp();
-  const int u = lane & 7;
+  const int u = lane % kUnits;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = 4 * i + (lane >> 3);
-    const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 128 + ((u ^ (row & 7)) << 4));
+  for (int i = 0; i < kUnits; ++i) {
+    const int row = 32 / kUnits * i + lane / kUnits;
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + row * kBytes + ((u ^ swap(row)) << 4));
     if (row < n_rows) *reinterpret_cast<uint4*>(dst + row * pitch + u * 8) = v;
   }
 }
@@ -303,7 +319,8 @@ __global__ void __launch_bounds__(384, 1)
   uint8_t* sQ = sm;                  // two tiles: A, B
   uint8_t* sK = sm + 2 * TF_BUF;     // two slots
   uint8_t* sV = sm + 4 * TF_BUF;     // two slots
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + 6 * TF_BUF);
+  uint8_t* sOut = sm + 6 * TF_BUF;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + 6 * TF_BUF + TF_STAGE);
   uint64_t* q_full = bars + 0;    // Q of item n landed (or the end marker)
   uint64_t* q_empty = bars + 1;   // item n's S products done and every warp has its number
   uint64_t* k_full = bars + 2;    // [2]
@@ -318,7 +335,7 @@ __global__ void __launch_bounds__(384, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* item_ring = reinterpret_cast<volatile int*>(tmem_holder + 2);   // [4]
   volatile int* item_info = item_ring + 4;   // [4][4], packed items: fwd_item_packed's fields
-  uint4* answer = reinterpret_cast<uint4*>(sm + 6 * TF_BUF + 256);   // packed: next_block_ask's
+  uint4* answer = reinterpret_cast<uint4*>(sm + 6 * TF_BUF + TF_STAGE + 256);   // packed: next_block_ask's
   uint64_t* answered = reinterpret_cast<uint64_t*>(answer + 1);
 
   const int warp = warp_id(), lane = lane_id();
@@ -814,25 +831,12 @@ __global__ void __launch_bounds__(384, 1)
         tc_fence_after();
         const int b = it.bh / H, h = it.bh - (it.bh / H) * H;
         const float inv = 1.f / l;
-        bf16* orow = kPacked ? o + (static_cast<long long>(b) * T + q) * pk.o_tok + h * pk.o_head
-                             : o + (static_cast<long long>(b) * T + q) * (static_cast<long long>(H) * 128) + h * 128;
+        const int w0 = q0 + quarter * 32;   // the warp's first row
+        const long long pitch = kPacked ? pk.o_tok : static_cast<long long>(H) * 128;
+        bf16* orow = o + (static_cast<long long>(b) * T + w0) * pitch + h * (kPacked ? pk.o_head : 128);
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t ra[32];
-          tmem_load32_async(t_o + c * 32, ra);
-          tmem_wait_ld();
-          if (q < Tv) {
-#pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-              uint4 w;
-              w.x = pack_bf16x2(__uint_as_float(ra[k]) * inv, __uint_as_float(ra[k + 1]) * inv);
-              w.y = pack_bf16x2(__uint_as_float(ra[k + 2]) * inv, __uint_as_float(ra[k + 3]) * inv);
-              w.z = pack_bf16x2(__uint_as_float(ra[k + 4]) * inv, __uint_as_float(ra[k + 5]) * inv);
-              w.w = pack_bf16x2(__uint_as_float(ra[k + 6]) * inv, __uint_as_float(ra[k + 7]) * inv);
-              *reinterpret_cast<uint4*>(orow + c * 32 + k) = w;
-            }
-          }
-        }
+        for (int c = 0; c < 128; c += 32)
+          store_rows<32>(t_o + c, inv, sOut + (warp - 4) * 2048, orow + c, pitch, Tv - w0);
         if (q < Tv) lse[static_cast<long long>(it.bh) * T + q] = (m_ref + log2f(l)) * 0.69314718055994531f;
         // O of this tile has been read: the next item's first P V may overwrite it
         tc_fence_before();
@@ -1683,19 +1687,10 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll 1
           for (int c = 0; c < 2; ++c) {
             const long long pitch = kPacked ? (c ? pa.o_tok : pa.dv_tok) : 128;
-            bf16* row = (c ? dk : dv) + (kPacked ? static_cast<long long>(w0) * pitch + kb.hk * (c ? pa.o_head : pa.dv_head)
+            bf16* row = (c ? dk : dv) + (kPacked ? w0 * pitch + kb.hk * (c ? pa.o_head : pa.dv_head)
                                                  : (static_cast<long long>(bkv) * T + w0) * 128);
-            const float f = c ? scale : 1.f;
-            uint32_t x[32], w[32];
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              tmem_load32_async(tmem + lane_base + 256 + 128 * c + 64 * half + 32 * hh, x);
-              tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                w[16 * hh + k] = pack_bf16x2(__uint_as_float(x[2 * k]) * f, __uint_as_float(x[2 * k + 1]) * f);
-            }
-            store_rows_64(sdSt + half * TF_TILE + quarter * 4096, w, row + 64 * half, pitch, rows);
+            store_rows<64>(tmem + lane_base + 256 + 128 * c + 64 * half, c ? scale : 1.f,
+                           sdSt + half * TF_TILE + quarter * 4096, row + 64 * half, pitch, rows);
           }
           __syncwarp();   // read before the next item's dS goes there
           // dK and dV have been read: the next key block's first products may
