@@ -28,7 +28,7 @@ constexpr int HD = 128;
 
 // ------------------------------------------------------- packed sequences
 //
-// The second build of both kernels (kPacked): one row of T positions holds
+// The packed forward and the packed build of the backward (kPacked): one row of T positions holds
 // sequences of different lengths end to end, and query t sees the keys
 // lo[t] .. t, lo[t] = max(start of t's sequence, t - window).  lo does not
 // decrease with t, so a tile of 128 queries sees the key blocks from that of
@@ -51,7 +51,7 @@ struct PackedArgs {
   const int* meta;          // forward: the plan's kMeta* words
   const int* lo;            // [T]
   const int* hi;            // [T]; -1 past the last sequence
-  const int4* fwd;          // forward entries: first query tile, first key block of it and of the next tile (-1: none)
+  const int2* fwd;          // forward entries: query tile, first key block that it sees
   const int2* bwd;          // backward entries: key block, number of query blocks that see it
   const int* ctl;           // backward: kCtl* words
   const CUtensorMap* maps;  // backward: q, k, v, dO with the extent patched in
@@ -151,7 +151,7 @@ __device__ __forceinline__ void tensormap_acquire(const CUtensorMap* m) {
 constexpr int TF_TILE = 16384;                // one [128 rows][128 B] swizzled tile
 constexpr int TF_BUF = 2 * TF_TILE;           // 128 x 128 bf16 as two 64-column tiles
 constexpr int TF_STAGE = 16384;               // output rows, 2 KB for each softmax warp
-constexpr int TF_SMEM = 6 * TF_BUF + TF_STAGE + 288;
+constexpr int TF_SMEM = 6 * TF_BUF + TF_STAGE + 256;
 constexpr float TF_RESCALE = 8.f;
 
 __device__ __forceinline__ float ex2_approx(float x) {
@@ -192,7 +192,6 @@ __device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&r)
 // (causal end), per tile counts nkvA, nkvB (0: tile B past the sequence).
 struct FwdItem {
   int bh, bkv, qtA, j0, nkvA, nkvB, nkv;
-  int oB;   // tile B's first key block, counted from j0 (0 unless packed)
   bool hasB;
 };
 
@@ -208,23 +207,6 @@ __device__ __forceinline__ FwdItem fwd_item(int n, int nq, int H, int Hkv, int k
   // both tiles start at the first key block any row of tile A sees; rows for
   // which a block lies wholly outside their window see only masked scores
   it.j0 = max(0, it.qtA * 128 - wl) / 128;
-  it.nkvA = it.qtA + 1 - it.j0;
-  it.nkvB = it.hasB ? it.qtA + 2 - it.j0 : 0;
-  it.nkv = it.hasB ? it.nkvB : it.nkvA;
-  it.oB = 0;
-  return it;
-}
-
-// A packed item as the TMA thread published it: head, first query tile, first
-// key block of tile A and of tile B (-1: no tile B).
-__device__ __forceinline__ FwdItem fwd_item_packed(const volatile int* f, int H, int Hkv) {
-  FwdItem it;
-  it.bh = f[0];
-  it.bkv = it.bh / (H / Hkv);
-  it.qtA = f[1];
-  it.j0 = f[2];
-  it.hasB = f[3] >= 0;
-  it.oB = it.hasB ? f[3] - it.j0 : 0;
   it.nkvA = it.qtA + 1 - it.j0;
   it.nkvB = it.hasB ? it.qtA + 2 - it.j0 : 0;
   it.nkv = it.hasB ? it.nkvB : it.nkvA;
@@ -279,35 +261,12 @@ __device__ __forceinline__ void store_rows(uint32_t taddr, float f, uint8_t* sta
   }
 }
 
-// bits 0 .. n - 1
-__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
-
-// Scores whose bit is clear become -inf.
-__device__ __forceinline__ void mask_scores(uint32_t (&x)[32], uint32_t seen) {
-#pragma unroll
-  for (int k = 0; k < 32; ++k)
-    if (!(seen & (1u << k))) x[k] = __float_as_uint(-INFINITY);
-}
-
-// Maximum of 32 scores, four chains of three-input maxima.
-__device__ __forceinline__ float max32(const uint32_t (&x)[32], float m) {
-  float c[4];
-#pragma unroll
-  for (int t = 0; t < 4; ++t) c[t] = fmaxf(__uint_as_float(x[2 * t]), __uint_as_float(x[2 * t + 1]));
-#pragma unroll
-  for (int k = 8; k < 32; k += 8) {
-#pragma unroll
-    for (int t = 0; t < 4; ++t) c[t] = fmax3(c[t], __uint_as_float(x[k + 2 * t]), __uint_as_float(x[k + 2 * t + 1]));
-  }
-  return fmax3(fmax3(c[0], c[1], c[2]), c[3], m);
-}
-
-template <bool kFine, bool kPacked>
+template <bool kFine>
 __global__ void __launch_bounds__(384, 1)
     attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, bf16* __restrict__ o, float* __restrict__ lse,
                        int H, int Hkv, int kvs, int T, int wl, float scale_log2, int n_items, int* sched,
-                       int* err, long long wait_cycles, const PackedArgs pk) {
+                       int* err, long long wait_cycles) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // the 128-byte-swizzled tiles need a 1024-byte-aligned base, which the
   // dynamic shared memory window provides; refuse to run otherwise
@@ -334,20 +293,10 @@ __global__ void __launch_bounds__(384, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 17);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* item_ring = reinterpret_cast<volatile int*>(tmem_holder + 2);   // [4]
-  volatile int* item_info = item_ring + 4;   // [4][4], packed items: fwd_item_packed's fields
-  uint4* answer = reinterpret_cast<uint4*>(sm + 6 * TF_BUF + TF_STAGE + 256);   // packed: next_block_ask's
-  uint64_t* answered = reinterpret_cast<uint64_t*>(answer + 1);
 
   const int warp = warp_id(), lane = lane_id();
   const int nq = (T + 127) / 128;
   const long long wlim = wait_limit_or_default(wait_cycles);
-  // positions that hold sequences; a plan of another T is refused
-  const bool fits = !kPacked || (pk.meta[kMetaMagic] == kPlanMagic && pk.meta[kMetaT] == T);
-  const int Tv = !kPacked ? T : fits ? pk.meta[kMetaTotal] : 0;
-  auto item_of = [&](int n, int idx) -> FwdItem {
-    if constexpr (kPacked) return fwd_item_packed(item_info + 4 * (n & 3), H, Hkv);
-    else return fwd_item(idx, nq, H, Hkv, kvs, wl);
-  };
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -358,10 +307,6 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 128); mbar_init(&pv_done[i], 1);
     }
     mbar_init(drain, 1);
-    if constexpr (kPacked) {
-      mbar_init(answered, 1);
-      if (!fits && blockIdx.x == 0 && err) atomicOr(err, ERRF_SHAPE);
-    }
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tq);
@@ -381,61 +326,19 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 0) {
     if (lane == 0) {
       // -------------------------------------------------------------- TMA
-      // Packed: item number and fields are fetched one item ahead, so that the
-      // answer's and the plan's latency hides behind the current item's loads.
-      int nx_idx = -1, nx_h = 0, entries = 0;
-      int4 nx = make_int4(0, 0, -1, 0);
-      bool asked = false;
-      uint32_t answers = 0;
-      auto fetch = [&](int idx) {   // false: a block without work (more pairs than the sequences fill)
-        if (idx >= n_items) return false;
-        nx_idx = idx;
-        nx_h = idx / entries;
-        nx = __ldg(pk.fwd + (idx - nx_h * entries));
-        return true;
-      };
-      auto take = [&] {   // false: the wait expired
-        nx_idx = -1;
-        while (asked) {
-          if (!mbar_wait_t<kFine>(answered, answers & 1, abort_flag, err, wlim)) return false;
-          ++answers;
-          asked = false;
-          const int idx = next_block_answer(answer);
-          if (idx < 0 || fetch(idx)) break;
-          next_block_ask(answer, answered);
-          asked = true;
-        }
-        return true;
-      };
-      if constexpr (kPacked) {
-        entries = fits ? pk.meta[kMetaFwd] : 0;
-        n_items = entries * H;
-        fetch(blockIdx.x);
-      }
       bool ok = true;
       int g = 0, last_q = -1;   // ring position of the next K/V block; last item whose Q was loaded
       for (int n = 0;; ++n) {
         // the previous item's Q is no longer read and every warp has its number
         if (n > 0 && !mbar_wait_t<kFine>(q_empty, (n - 1) & 1, abort_flag, err, wlim)) { ok = false; break; }
-        int idx;
-        if constexpr (kPacked) {
-          idx = nx_idx;
-          volatile int* f = item_info + 4 * (n & 3);
-          f[0] = nx_h; f[1] = nx.x; f[2] = nx.y; f[3] = nx.z;
-          if (idx >= 0) {
-            next_block_ask(answer, answered);
-            asked = true;
-          }
-        } else {
-          idx = sched ? atomicAdd(sched, 1) : n * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-          if (idx >= n_items) idx = -1;
-        }
+        int idx = sched ? atomicAdd(sched, 1) : n * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+        if (idx >= n_items) idx = -1;
         item_ring[n & 3] = idx;
         if (idx < 0) {
           mbar_arrive(q_full);   // end marker: releases the ring entry
           break;
         }
-        const FwdItem it = item_of(n, idx);
+        const FwdItem it = fwd_item(idx, nq, H, Hkv, kvs, wl);
         mbar_arrive_expect_tx(q_full, it.hasB ? 2 * TF_BUF : TF_BUF);
         tma_load_3d(sQ, &tq, q_full, 0, it.qtA * 128, it.bh);
         tma_load_3d(sQ + TF_TILE, &tq, q_full, 64, it.qtA * 128, it.bh);
@@ -462,16 +365,11 @@ __global__ void __launch_bounds__(384, 1)
           tma_load_3d(sV + s * TF_BUF, &tv, &v_full[s], 0, kc, it.bkv);
           tma_load_3d(sV + s * TF_BUF + TF_TILE, &tv, &v_full[s], 64, kc, it.bkv);
           ++g;
-          if constexpr (kPacked)
-            if (j == 0 && !take()) { ok = false; break; }
         }
         if (!ok) break;
       }
       if (!ok) {
         // let the copies already started land before the CTA exits
-        if constexpr (kPacked)
-          if (asked)
-            for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(answered, answers & 1); ++i) {}
         if (last_q >= 0)
           for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(q_full, last_q & 1); ++i) {}
         for (int x = (g > 2 ? g - 2 : 0); x < g; ++x) {
@@ -481,109 +379,87 @@ __global__ void __launch_bounds__(384, 1)
       }
     }
   } else if (warp == 1) {
-    {
-      // -------------------------------------------------------------- MMA
-      // the whole warp, converged; one lane issues
-      const bool leader = elect_lane();
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      auto wait1 = [&](uint64_t* bar, uint32_t par) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait_t<kFine>(bar, par, abort_flag, err, wlim));
-      };
-      auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
-      constexpr uint32_t IDESC_S = make_idesc(1, 128, false, false);
-      constexpr uint32_t IDESC_O = make_idesc(1, 128, false, true);
-      // The descriptors of a product are its first one plus the byte offset / 16
-      // (the start address field); the empty asm keeps the compiler from
-      // hoisting every descriptor of the kernel into registers.
-      // S_t = Q_t K^T (K in ring slot ks) into TMEM columns 128 t
-      auto issue_s = [&](int t, int ks) {
-        uint64_t dq = smem_desc_sw128(smem_u32(sQ + t * TF_BUF), 16, 1024);
-        uint64_t dk = smem_desc_sw128(smem_u32(sK + ks * TF_BUF), 16, 1024);
+    // -------------------------------------------------------------- MMA
+    // the whole warp, converged; one lane issues
+    const bool leader = elect_lane();
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    auto wait1 = [&](uint64_t* bar, uint32_t par) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait_t<kFine>(bar, par, abort_flag, err, wlim));
+    };
+    constexpr uint32_t IDESC_S = make_idesc(1, 128, false, false);
+    constexpr uint32_t IDESC_O = make_idesc(1, 128, false, true);
+    // The descriptors of a product are its first one plus the byte offset / 16
+    // (the start address field).
+    // S_t = Q_t K^T (K in ring slot ks) into TMEM columns 128 t
+    auto issue_s = [&](int t, int ks) {
+      uint64_t dq = smem_desc_sw128(smem_u32(sQ + t * TF_BUF), 16, 1024);
+      uint64_t dk = smem_desc_sw128(smem_u32(sK + ks * TF_BUF), 16, 1024);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off16 = ((kk >> 2) * TF_TILE + (kk & 3) * 32) >> 4;
-          umma_f16_by(leader, tm + t * 128, dq + off16, dk + off16, IDESC_S, kk > 0 ? 1u : 0u);
-        }
-        umma_commit_by(leader, &s_full[t]);
-      };
-      // O_t (+)= P_t V (V in ring slot vs), P_t from TMEM (16 keys = 8 packed columns per step)
-      auto issue_pv = [&](int t, int vs, bool acc) {
-        uint64_t dv = smem_desc_sw128(smem_u32(sV + vs * TF_BUF), TF_TILE, 1024);
+      for (int kk = 0; kk < 8; ++kk) {
+        const uint32_t off16 = ((kk >> 2) * TF_TILE + (kk & 3) * 32) >> 4;
+        umma_f16_by(leader, tm + t * 128, dq + off16, dk + off16, IDESC_S, kk > 0 ? 1u : 0u);
+      }
+      umma_commit_by(leader, &s_full[t]);
+    };
+    // O_t (+)= P_t V (V in ring slot vs), P_t from TMEM (16 keys = 8 packed columns per step)
+    auto issue_pv = [&](int t, int vs, bool acc) {
+      uint64_t dv = smem_desc_sw128(smem_u32(sV + vs * TF_BUF), TF_TILE, 1024);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_f16_tmem_a_by(leader, tm + 256 + t * 128, tm + t * 128 + kk * 8, dv + ((kk * 2048) >> 4), IDESC_O,
-                          (acc || kk > 0) ? 1u : 0u);
-        umma_commit_by(leader, &pv_done[t]);
-      };
-      bool ok = true;
-      int g0 = 0;                  // ring position of the item's first key block
-      uint32_t npv[2] = {0u, 0u};  // P V products issued per tile so far
-      for (int n = 0; ok; ++n) {
-        if (!wait1(q_full, n & 1)) { ok = false; break; }
-        const int idx = uniform(item_ring[n & 3]);
-        if (idx < 0) break;
-        FwdItem it = item_of(n, idx);
-        it.nkvA = uniform(it.nkvA);
-        it.nkvB = uniform(it.nkvB);
-        it.nkv = uniform(it.nkv);
-        it.oB = uniform(it.oB);
-        it.hasB = uniform(it.hasB) != 0;
-        // S of the first block on both tiles, each once its previous P V (which
-        // reads P from the same columns) has completed
-        if (!wait1(&k_full[g0 & 1], (g0 >> 1) & 1)) { ok = false; break; }
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (t == 1 && (!it.hasB || (kPacked && it.oB > 0))) break;
-          if (npv[t] > 0 && !wait1(&pv_done[t], (npv[t] - 1) & 1)) { ok = false; break; }
+      for (int kk = 0; kk < 8; ++kk)
+        umma_f16_tmem_a_by(leader, tm + 256 + t * 128, tm + t * 128 + kk * 8, dv + ((kk * 2048) >> 4), IDESC_O,
+                        (acc || kk > 0) ? 1u : 0u);
+      umma_commit_by(leader, &pv_done[t]);
+    };
+    bool ok = true;
+    int g0 = 0;                  // ring position of the item's first key block
+    uint32_t npv[2] = {0u, 0u};  // P V products issued per tile so far
+    for (int n = 0; ok; ++n) {
+      if (!wait1(q_full, n & 1)) { ok = false; break; }
+      const int idx = __shfl_sync(0xffffffffu, item_ring[n & 3], 0);
+      if (idx < 0) break;
+      const FwdItem it = fwd_item(idx, nq, H, Hkv, kvs, wl);
+      // S of the first block on both tiles, each once its previous P V (which
+      // reads P from the same columns) has completed
+      if (!wait1(&k_full[g0 & 1], (g0 >> 1) & 1)) { ok = false; break; }
+      for (int t = 0; t < 2 && ok; ++t) {
+        if (t == 1 && !it.hasB) break;
+        if (npv[t] > 0 && !wait1(&pv_done[t], (npv[t] - 1) & 1)) { ok = false; break; }
+        tc_fence_after();
+        issue_s(t, g0 & 1);
+      }
+      if (!ok) break;
+      if (it.nkv == 1) umma_commit_by(leader, q_empty);   // the item's last S
+      umma_commit_by(leader, &k_empty[g0 & 1]);
+      for (int j = 0; j < it.nkv && ok; ++j) {
+        const int gj = g0 + j;
+        const int s = gj & 1;
+        const int s1 = (gj + 1) & 1;
+        if (!wait1(&v_full[s], (gj >> 1) & 1)) { ok = false; break; }
+        if (j + 1 < it.nkv && !wait1(&k_full[s1], ((gj + 1) >> 1) & 1)) { ok = false; break; }
+        // per tile: O += P V_j, then S of the next block over P once that product
+        // has read it (tile B's softmax trails tile A's, so A goes first)
+        for (int t = 0; t < 2; ++t) {
+          const int nkv_t = t ? it.nkvB : it.nkvA;
+          if (j >= nkv_t) continue;
+          if (!wait1(&p_full[t], npv[t] & 1)) { ok = false; break; }
           tc_fence_after();
-          issue_s(t, g0 & 1);
+          issue_pv(t, s, j > 0);
+          ++npv[t];
+          if (j + 1 < nkv_t) {
+            if (!wait1(&pv_done[t], (npv[t] - 1) & 1)) { ok = false; break; }
+            tc_fence_after();
+            issue_s(t, s1);
+            if (j + 1 == it.nkv - 1) umma_commit_by(leader, q_empty);   // the item's last S
+          }
         }
         if (!ok) break;
-        if (it.nkv == 1) umma_commit_by(leader, q_empty);   // the item's last S
-        umma_commit_by(leader, &k_empty[g0 & 1]);
-        for (int j = 0; j < it.nkv && ok; ++j) {
-          const int gj = g0 + j;
-          const int s = gj & 1;
-          const int s1 = (gj + 1) & 1;
-          if (!wait1(&v_full[s], (gj >> 1) & 1)) { ok = false; break; }
-          if constexpr (kPacked) {
-            const int past = Tv - (it.j0 + j) * 128;   // rows of V from here on belong to no sequence
-            if (Tv < T && past < 128) {
-              for (int x = past * 16 + lane; x < 128 * 16; x += 32)
-                *reinterpret_cast<uint4*>(sV + s * TF_BUF + ((x >> 3) & 1) * TF_TILE + (x >> 4) * 128 + (x & 7) * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
-          }
-          if (j + 1 < it.nkv && !wait1(&k_full[s1], ((gj + 1) >> 1) & 1)) { ok = false; break; }
-          // per tile: O += P V_j, then S of the next block over P once that product
-          // has read it (tile B's softmax trails tile A's, so A goes first)
-          for (int t = 0; t < 2; ++t) {
-            const int nkv_t = t ? it.nkvB : it.nkvA;
-            if (j >= nkv_t) continue;
-            const int o_t = kPacked && t ? it.oB : 0;   // the tile's first block
-            if (!kPacked || j >= o_t) {
-              if (!wait1(&p_full[t], npv[t] & 1)) { ok = false; break; }
-              tc_fence_after();
-              issue_pv(t, s, j > o_t);
-              ++npv[t];
-            }
-            if (j + 1 < nkv_t && (!kPacked || j + 1 >= o_t)) {
-              if ((!kPacked || npv[t] > 0) && !wait1(&pv_done[t], (npv[t] - 1) & 1)) { ok = false; break; }
-              tc_fence_after();
-              issue_s(t, s1);
-              if (j + 1 == it.nkv - 1) umma_commit_by(leader, q_empty);   // the item's last S
-            }
-          }
-          if (!ok) break;
-          umma_commit_by(leader, &v_empty[s]);
-          if (j + 1 < it.nkv) umma_commit_by(leader, &k_empty[s1]);
-        }
-        g0 += it.nkv;
+        umma_commit_by(leader, &v_empty[s]);
+        if (j + 1 < it.nkv) umma_commit_by(leader, &k_empty[s1]);
       }
-      umma_commit_by(leader, drain);
-      for (uint32_t i = 0; i < (1u << 22) && !mbar_try_wait(drain, 0); ++i) {}
+      g0 += it.nkv;
     }
+    umma_commit_by(leader, drain);
+    for (uint32_t i = 0; i < (1u << 22) && !mbar_try_wait(drain, 0); ++i) {}
   } else if (warp >= 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;\n" ::: "memory");
     // ---------------------------------------------------------- softmax
@@ -607,106 +483,61 @@ __global__ void __launch_bounds__(384, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(q_empty);   // this warp has the item number
       if (idx < 0) break;
-      const FwdItem it = item_of(n, idx);
+      const FwdItem it = fwd_item(idx, nq, H, Hkv, kvs, wl);
       if (tile == 1 && !it.hasB) continue;
       const int qt = it.qtA + tile;
       const int q0 = qt * 128;
       const int q = q0 + r;
       const int nkv_t = tile ? it.nkvB : it.nkvA;
-      const int j_first = kPacked && tile ? it.oB : 0;
-      int lo = 0, lo_max = 0;   // packed: first key of this row, and the largest of the warp's rows
-      if constexpr (kPacked) {
-        if (q < Tv) lo = __ldg(pk.lo + q);
-        lo_max = __reduce_max_sync(0xffffffffu, lo);
-      }
       float m_ref = -INFINITY, l = 0.f;   // reference max (log2 units) and row sum relative to it
-      for (int j = j_first; j < nkv_t && ok; ++j) {
+      for (int j = 0; j < nkv_t && ok; ++j) {
         if (!wait_all(&s_full[tile], nblk & 1)) { ok = false; break; }
         ++nblk;
         tc_fence_after();
-        const int kbase = (it.j0 + j) * 128;
-        const bool diag = it.j0 + j == qt;
-        float mraw = -INFINITY;           // block max of the raw scores (the scale is positive)
-        uint32_t sr[kPacked ? 1 : 128];   // not packed: the whole S row at once
-        // Packed rows meet masked blocks at every sequence boundary.  Straight-
-        // line code for a row and for each kind of mask, as below, left the
-        // softmax warps a fifth of their time without instructions, so here the
-        // row is read from TMEM 32 scores at a time, now and again for P, by
-        // loops that stay in the instruction cache, mask by bits and skip the
-        // chunks that no row of the warp sees (16,384 tokens of chats, 10 heads:
-        // 91 us instead of 103; whole rows of 2048: 229 instead of 217).
-        // Keys past the last sequence lie above every row of the diagonal block.
-        const bool masked = kPacked && (diag || kbase < lo_max);
-        // keys that this row sees, from kbase on: first .. end - 1
-        const int first = lo - kbase, end = q + 1 - kbase;
-        auto seen_of = [&](int c) { return low_bits(end - 32 * c) & ~low_bits(first - 32 * c); };
-        if constexpr (kPacked) {
-          if (!masked) {
-            uint32_t xa[32], xb[32];
-#pragma unroll 1
-            for (int c = 0; c < 4; c += 2) {
-              tmem_load32_async(t_s + 32 * c, xa);
-              tmem_load32_async(t_s + 32 * c + 32, xb);
-              tmem_wait_ld();
-              mraw = max32(xb, max32(xa, mraw));
-            }
-          } else {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t seen = seen_of(c);
-              if (__any_sync(0xffffffffu, seen != 0)) {
-                uint32_t x[32];
-                tmem_load32_async(t_s + 32 * c, x);
-                tmem_wait_ld();
-                mask_scores(x, seen);
-                mraw = max32(x, mraw);
-              }
-            }
-          }
-        } else {
-          // the whole S row at once
-          {
-            uint32_t (&r0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[0]);
-            uint32_t (&r1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[32]);
-            uint32_t (&r2)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[64]);
-            uint32_t (&r3)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[96]);
-            tmem_load32_async(t_s, r0);
-            tmem_load32_async(t_s + 32, r1);
-            tmem_load32_async(t_s + 64, r2);
-            tmem_load32_async(t_s + 96, r3);
-            tmem_wait_ld();
-          }
-          const bool edge = (kbase + 128 > T) || (kbase < q0 + 127 - wl);
-          if (diag && !edge) {
-            // causal diagonal block: only the keys above the row are masked, so
-            // per element in one 32-key chunk, whole chunks beyond it
-            switch (quarter) {
-              case 0: causal_mask_row<0>(sr, lane); break;
-              case 1: causal_mask_row<1>(sr, lane); break;
-              case 2: causal_mask_row<2>(sr, lane); break;
-              default: causal_mask_row<3>(sr, lane); break;
-            }
-          } else if (diag || edge) {
-            // ragged tail or window edge: masked scores become -inf
-#pragma unroll
-            for (int k = 0; k < 128; ++k) {
-              const int key = kbase + k;
-              if (key > q || key >= T || key < q - wl) sr[k] = __float_as_uint(-INFINITY);
-            }
-          }
-          // block max of the raw scores (the scale is positive), eight independent
-          // chains of three-input maxima (two new scores per instruction)
-          float mx8[8];
-#pragma unroll
-          for (int t = 0; t < 8; ++t) mx8[t] = fmaxf(__uint_as_float(sr[2 * t]), __uint_as_float(sr[2 * t + 1]));
-#pragma unroll
-          for (int k = 16; k < 128; k += 16) {
-#pragma unroll
-            for (int t = 0; t < 8; ++t)
-              mx8[t] = fmax3(mx8[t], __uint_as_float(sr[k + 2 * t]), __uint_as_float(sr[k + 2 * t + 1]));
-          }
-          mraw = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
+        // the whole S row at once
+        uint32_t sr[128];
+        {
+          uint32_t (&r0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[0]);
+          uint32_t (&r1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[32]);
+          uint32_t (&r2)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[64]);
+          uint32_t (&r3)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[96]);
+          tmem_load32_async(t_s, r0);
+          tmem_load32_async(t_s + 32, r1);
+          tmem_load32_async(t_s + 64, r2);
+          tmem_load32_async(t_s + 96, r3);
+          tmem_wait_ld();
         }
+        const int kbase = (it.j0 + j) * 128;
+        const bool diag = it.j0 + j == qt, edge = (kbase + 128 > T) || (kbase < q0 + 127 - wl);
+        if (diag && !edge) {
+          // causal diagonal block: only the keys above the row are masked, so
+          // per element in one 32-key chunk, whole chunks beyond it
+          switch (quarter) {
+            case 0: causal_mask_row<0>(sr, lane); break;
+            case 1: causal_mask_row<1>(sr, lane); break;
+            case 2: causal_mask_row<2>(sr, lane); break;
+            default: causal_mask_row<3>(sr, lane); break;
+          }
+        } else if (diag || edge) {
+          // ragged tail or window edge: masked scores become -inf
+#pragma unroll
+          for (int k = 0; k < 128; ++k) {
+            const int key = kbase + k;
+            if (key > q || key >= T || key < q - wl) sr[k] = __float_as_uint(-INFINITY);
+          }
+        }
+        // block max of the raw scores (the scale is positive), eight independent
+        // chains of three-input maxima (two new scores per instruction)
+        float mx8[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) mx8[t] = fmaxf(__uint_as_float(sr[2 * t]), __uint_as_float(sr[2 * t + 1]));
+#pragma unroll
+        for (int k = 16; k < 128; k += 16) {
+#pragma unroll
+          for (int t = 0; t < 8; ++t)
+            mx8[t] = fmax3(mx8[t], __uint_as_float(sr[k + 2 * t]), __uint_as_float(sr[k + 2 * t + 1]));
+        }
+        const float mraw = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
         const float mblk = mraw * scale_log2;
         const bool move = mblk > m_ref + TF_RESCALE;   // true on the first block with a visible key
         const float m_new = move ? mblk : m_ref;
@@ -716,7 +547,7 @@ __global__ void __launch_bounds__(384, 1)
         const float factor = none ? 1.f : ex2_approx(m_ref - m_new);
         // O holds the products of blocks < j (S of this block was issued after
         // the last of them completed), so it may be rescaled now
-        if (j > j_first && __any_sync(0xffffffffu, move)) {
+        if (j >= 1 && __any_sync(0xffffffffu, move)) {
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t ra[32];
@@ -732,90 +563,32 @@ __global__ void __launch_bounds__(384, 1)
         const float m_off = none ? 0.f : m_new;
         const uint64_t nb2 = f2_pack(-m_off, -m_off);
         uint64_t rs2 = f2_pack(0.f, 0.f);
-        if constexpr (kPacked) {
-          auto probabilities = [&](const uint32_t (&x)[32], int c) {
-            uint32_t pk[16];
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-              float p[8];
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[32];
 #pragma unroll
-              for (int e = 0; e < 8; e += 2) {
-                float x0, x1;
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(x[k + e]), __uint_as_float(x[k + e + 1])), sl2, nb2), x0, x1);
-                if (e < ((k & 8) ? GPT_FWD_MUFU_ODD : GPT_FWD_MUFU_EVEN)) {
-                  p[e] = ex2_approx(x0);
-                  p[e + 1] = ex2_approx(x1);
-                } else {
-                  f2_unpack(f2_exp2_poly(f2_pack(fmaxf(x0, -126.f), fmaxf(x1, -126.f))), p[e], p[e + 1]);
-                }
-              }
+          for (int k = 0; k < 64; k += 8) {
+            float p[8];
 #pragma unroll
-              for (int e = 0; e < 8; e += 2) {
-                rs2 = f2_add(rs2, f2_pack(p[e], p[e + 1]));
-                pk[(k + e) >> 1] = pack_bf16x2(p[e], p[e + 1]);
-              }
-            }
-            tmem_store16(t_s + 16 * c, pk);
-          };
-          if (!masked) {
-            uint32_t xa[32], xb[32];
-            tmem_load32_async(t_s, xa);
-            tmem_landed(xa);
-#pragma unroll 1
-            for (int c = 0; c < 4; c += 2) {
-              tmem_load32_async(t_s + 32 * c + 32, xb);
-              probabilities(xa, c);
-              tmem_landed(xb);
-              if (c == 0) tmem_load32_async(t_s + 64, xa);
-              probabilities(xb, c + 1);
-              tmem_landed(xa);
-            }
-          } else {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t seen = seen_of(c);
-              if (__any_sync(0xffffffffu, seen != 0)) {
-                uint32_t x[32];
-                tmem_load32_async(t_s + 32 * c, x);
-                tmem_wait_ld();
-                mask_scores(x, seen);
-                probabilities(x, c);
+            for (int e = 0; e < 8; e += 2) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c * 64 + k + e]), __uint_as_float(sr[c * 64 + k + e + 1])),
+                               sl2, nb2),
+                        x0, x1);
+              if (e < ((k & 8) ? GPT_FWD_MUFU_ODD : GPT_FWD_MUFU_EVEN)) {
+                p[e] = ex2_approx(x0);
+                p[e + 1] = ex2_approx(x1);
               } else {
-                uint32_t pk[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) pk[k] = 0u;
-                tmem_store16(t_s + 16 * c, pk);
+                f2_unpack(f2_exp2_poly(f2_pack(fmaxf(x0, -126.f), fmaxf(x1, -126.f))), p[e], p[e + 1]);
               }
             }
-          }
-        } else {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int k = 0; k < 64; k += 8) {
-              float p[8];
-#pragma unroll
-              for (int e = 0; e < 8; e += 2) {
-                float x0, x1;
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c * 64 + k + e]), __uint_as_float(sr[c * 64 + k + e + 1])),
-                                 sl2, nb2),
-                          x0, x1);
-                if (e < ((k & 8) ? GPT_FWD_MUFU_ODD : GPT_FWD_MUFU_EVEN)) {
-                  p[e] = ex2_approx(x0);
-                  p[e + 1] = ex2_approx(x1);
-                } else {
-                  f2_unpack(f2_exp2_poly(f2_pack(fmaxf(x0, -126.f), fmaxf(x1, -126.f))), p[e], p[e + 1]);
-                }
-              }
-#pragma unroll
-              for (int e = 0; e < 8; e += 2) {
-                rs2 = f2_add(rs2, f2_pack(p[e], p[e + 1]));
-                pk[(k + e) >> 1] = pack_bf16x2(p[e], p[e + 1]);
-              }
+            for (int e = 0; e < 8; e += 2) {
+              rs2 = f2_add(rs2, f2_pack(p[e], p[e + 1]));
+              pk[(k + e) >> 1] = pack_bf16x2(p[e], p[e + 1]);
             }
-            tmem_store32(t_s + c * 32, pk);
           }
+          tmem_store32(t_s + c * 32, pk);
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
@@ -832,12 +605,12 @@ __global__ void __launch_bounds__(384, 1)
         const int b = it.bh / H, h = it.bh - (it.bh / H) * H;
         const float inv = 1.f / l;
         const int w0 = q0 + quarter * 32;   // the warp's first row
-        const long long pitch = kPacked ? pk.o_tok : static_cast<long long>(H) * 128;
-        bf16* orow = o + (static_cast<long long>(b) * T + w0) * pitch + h * (kPacked ? pk.o_head : 128);
+        const long long pitch = static_cast<long long>(H) * 128;
+        bf16* orow = o + (static_cast<long long>(b) * T + w0) * pitch + h * 128;
 #pragma unroll 1
         for (int c = 0; c < 128; c += 32)
-          store_rows<32>(t_o + c, inv, sOut + (warp - 4) * 2048, orow + c, pitch, Tv - w0);
-        if (q < Tv) lse[static_cast<long long>(it.bh) * T + q] = (m_ref + log2f(l)) * 0.69314718055994531f;
+          store_rows<32>(t_o + c, inv, sOut + (warp - 4) * 2048, orow + c, pitch, T - w0);
+        if (q < T) lse[static_cast<long long>(it.bh) * T + q] = (m_ref + log2f(l)) * 0.69314718055994531f;
         // O of this tile has been read: the next item's first P V may overwrite it
         tc_fence_before();
       }
@@ -849,6 +622,419 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+}
+
+// bits 0 .. n - 1
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
+// Scores whose bit is clear become -inf.
+__device__ __forceinline__ void mask_scores(uint32_t (&x)[32], uint32_t seen) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    if (!(seen & (1u << k))) x[k] = __float_as_uint(-INFINITY);
+}
+
+// Maximum of 32 scores, four chains of three-input maxima.
+__device__ __forceinline__ float max32(const uint32_t (&x)[32], float m) {
+  float c[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) c[t] = fmaxf(__uint_as_float(x[2 * t]), __uint_as_float(x[2 * t + 1]));
+#pragma unroll
+  for (int k = 8; k < 32; k += 8) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) c[t] = fmax3(c[t], __uint_as_float(x[k + 2 * t]), __uint_as_float(x[k + 2 * t + 1]));
+  }
+  return fmax3(fmax3(c[0], c[1], c[2]), c[3], m);
+}
+
+// -------------------------------------- packed forward on tcgen05 / TMEM
+//
+// Persistent, two blocks an SM, each with its own 128-query tiles of one head,
+// taken in turn; the two hide each other's softmax and products, start and
+// end of a tile.  (Pairs of tiles that share their key blocks in one block, as
+// above, leave a fifth of the softmax time idle here: neighbours seldom see
+// equally many blocks.)
+// 192 threads:
+//   warps 0..3  softmax, one query row (TMEM lane) per thread, as above; then
+//               O / l and the log-sum-exp
+//   warp 4      TMA: takes the items and publishes them in a shared ring, loads
+//               Q, and K_j and V_j through one buffer each: K_j+1 comes while
+//               the softmax of block j runs, V_j+1 while that of j + 1 does
+//   warp 5      TMEM owner and MMA issuer: S = Q K_j^T into columns [0,128),
+//               O += P V_j into [128,256), P over the first 64 columns of S
+constexpr int PF_STAGE = 8192;   // output rows: 2 KB for each softmax warp
+constexpr int PF_SMEM = 3 * TF_BUF + PF_STAGE + 256;
+
+template <bool kFine>
+__global__ void __launch_bounds__(192, 2)
+    attn_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                           const __grid_constant__ CUtensorMap tv, bf16* __restrict__ o, float* __restrict__ lse,
+                           int H, int Hkv, int T, float scale_log2, int* err, long long wait_cycles,
+                           const PackedArgs pk) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // the 128-byte-swizzled tiles need a 1024-byte-aligned base, which the
+  // dynamic shared memory window provides; refuse to run otherwise
+  if (smem_u32(smem_raw) & 1023u) {
+    if (threadIdx.x == 0 && err) atomicOr(err, ERRF_SHAPE);
+    return;
+  }
+  uint8_t* sQ = smem_raw;
+  uint8_t* sK = smem_raw + TF_BUF;
+  uint8_t* sV = smem_raw + 2 * TF_BUF;
+  uint8_t* sOut = smem_raw + 3 * TF_BUF;
+  uint4* answer = reinterpret_cast<uint4*>(smem_raw + 3 * TF_BUF + PF_STAGE);   // next_block_ask's
+  uint64_t* bars = reinterpret_cast<uint64_t*>(answer + 1);
+  uint64_t* q_full = bars + 0;    // Q of item n landed (or the end marker)
+  uint64_t* q_empty = bars + 1;   // item n's S products done and every softmax warp has its fields
+  uint64_t* k_full = bars + 2;
+  uint64_t* k_empty = bars + 3;
+  uint64_t* v_full = bars + 4;
+  uint64_t* v_empty = bars + 5;
+  uint64_t* s_full = bars + 6;    // S of a block in TMEM
+  uint64_t* p_full = bars + 7;    // P of a block in TMEM
+  uint64_t* pv_done = bars + 8;   // P V of a block complete
+  uint64_t* drain = bars + 9;
+  uint64_t* answered = bars + 10;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 11);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  volatile int* item_ring = reinterpret_cast<volatile int*>(tmem_holder + 2);   // [4][4]: head (-1: end), tile, first key block
+
+  const int warp = warp_id(), lane = lane_id();
+  const long long wlim = wait_limit_or_default(wait_cycles);
+  // positions that hold sequences; a plan of another T is refused
+  const bool fits = pk.meta[kMetaMagic] == kPlanMagic && pk.meta[kMetaT] == T;
+  const int Tv = fits ? pk.meta[kMetaTotal] : 0;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1 + 4);   // the MMA commit and one arrival per softmax warp
+    mbar_init(k_full, 1); mbar_init(k_empty, 1);
+    mbar_init(v_full, 1); mbar_init(v_empty, 1);
+    mbar_init(s_full, 1); mbar_init(p_full, 128); mbar_init(pv_done, 1);
+    mbar_init(drain, 1);
+    mbar_init(answered, 1);
+    if (!fits && blockIdx.x == 0 && err) atomicOr(err, ERRF_SHAPE);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+  }
+  if (warp == 5) {
+    tmem_alloc(tmem_holder, 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      // -------------------------------------------------------------- TMA
+      // item number and fields are fetched one item ahead, so that the answer's
+      // and the plan's latency hides behind the current item's loads
+      const int entries = fits ? pk.meta[kMetaFwd] : 0, n_items = entries * H;
+      int nx_h = -1;
+      int2 nx = make_int2(0, 0);
+      bool asked = false;
+      uint32_t answers = 0;
+      auto fetch = [&](int idx) {   // false: a block without work (tiles past the sequences)
+        if (idx >= n_items) return false;
+        nx_h = idx / entries;
+        nx = __ldg(pk.fwd + (idx - nx_h * entries));
+        return true;
+      };
+      auto take = [&] {   // false: the wait expired
+        nx_h = -1;
+        while (asked) {
+          if (!mbar_wait_t<kFine>(answered, answers & 1, abort_flag, err, wlim)) return false;
+          ++answers;
+          asked = false;
+          const int idx = next_block_answer(answer);
+          if (idx < 0 || fetch(idx)) break;
+          next_block_ask(answer, answered);
+          asked = true;
+        }
+        return true;
+      };
+      fetch(blockIdx.x);
+      bool ok = true;
+      uint32_t g = 0;     // key blocks loaded so far
+      int last_q = -1;    // last item whose Q was loaded
+      for (int n = 0;; ++n) {
+        // the previous item's Q is no longer read and every warp has its fields
+        if (n > 0 && !mbar_wait_t<kFine>(q_empty, (n - 1) & 1, abort_flag, err, wlim)) { ok = false; break; }
+        volatile int* f = item_ring + 4 * (n & 3);
+        const int h = nx_h, qt = nx.x, j0 = nx.y;
+        f[0] = h; f[1] = qt; f[2] = j0;
+        if (h < 0) {
+          mbar_arrive(q_full);   // end marker: releases the ring entry
+          break;
+        }
+        next_block_ask(answer, answered);
+        asked = true;
+        const int hk = h / (H / Hkv);
+        mbar_arrive_expect_tx(q_full, TF_BUF);
+        tma_load_3d(sQ, &tq, q_full, 0, qt * 128, h);
+        tma_load_3d(sQ + TF_TILE, &tq, q_full, 64, qt * 128, h);
+        last_q = n;
+        for (int j = j0; j <= qt; ++j) {
+          if (!mbar_wait_t<kFine>(k_empty, (g & 1) ^ 1u, abort_flag, err, wlim)) { ok = false; break; }
+          mbar_arrive_expect_tx(k_full, TF_BUF);
+          tma_load_3d(sK, &tk, k_full, 0, j * 128, hk);
+          tma_load_3d(sK + TF_TILE, &tk, k_full, 64, j * 128, hk);
+          if (!mbar_wait_t<kFine>(v_empty, (g & 1) ^ 1u, abort_flag, err, wlim)) {
+            // K of this block is in flight, V is not
+            for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(k_full, g & 1); ++i) {}
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(v_full, TF_BUF);
+          tma_load_3d(sV, &tv, v_full, 0, j * 128, hk);
+          tma_load_3d(sV + TF_TILE, &tv, v_full, 64, j * 128, hk);
+          ++g;
+          if (j == j0 && !take()) { ok = false; break; }
+        }
+        if (!ok) break;
+      }
+      if (!ok) {
+        // let the copies already started land before the CTA exits
+        if (asked)
+          for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(answered, answers & 1); ++i) {}
+        if (last_q >= 0)
+          for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(q_full, last_q & 1); ++i) {}
+        if (g > 0) {
+          for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(k_full, (g - 1) & 1); ++i) {}
+          for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(v_full, (g - 1) & 1); ++i) {}
+        }
+      }
+    }
+  } else if (warp == 5) {
+    // -------------------------------------------------------------- MMA
+    // the whole warp, converged; one lane issues
+    const bool leader = elect_lane();
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    auto wait1 = [&](uint64_t* bar, uint32_t par) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait_t<kFine>(bar, par, abort_flag, err, wlim));
+    };
+    constexpr uint32_t IDESC_S = make_idesc(1, 128, false, false);
+    constexpr uint32_t IDESC_O = make_idesc(1, 128, false, true);
+    const uint64_t dq = smem_desc_sw128(smem_u32(sQ), 16, 1024), dk = smem_desc_sw128(smem_u32(sK), 16, 1024);
+    const uint64_t dv = smem_desc_sw128(smem_u32(sV), TF_TILE, 1024);
+    bool ok = true;
+    uint32_t g = 0;   // key blocks done so far
+    for (int n = 0; ok; ++n) {
+      if (!wait1(q_full, n & 1)) break;
+      const volatile int* f = item_ring + 4 * (n & 3);
+      const int h = __shfl_sync(0xffffffffu, f[0], 0), qt = __shfl_sync(0xffffffffu, f[1], 0);
+      const int j0 = __shfl_sync(0xffffffffu, f[2], 0);
+      if (h < 0) break;
+      for (int j = j0; j <= qt; ++j, ++g) {
+        // S over P of the block before, once its product has read it
+        if (!wait1(k_full, g & 1) || (g > 0 && !wait1(pv_done, (g - 1) & 1))) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off16 = ((kk >> 2) * TF_TILE + (kk & 3) * 32) >> 4;
+          umma_f16_by(leader, tm, dq + off16, dk + off16, IDESC_S, kk > 0 ? 1u : 0u);
+        }
+        umma_commit_by(leader, s_full);
+        umma_commit_by(leader, k_empty);
+        if (j == qt) umma_commit_by(leader, q_empty);   // the item's last S
+        if (!wait1(v_full, g & 1)) { ok = false; break; }
+        const int past = Tv - j * 128;   // rows of V from here on belong to no sequence
+        if (Tv < T && past < 128) {
+          for (int x = past * 16 + lane; x < 128 * 16; x += 32)
+            *reinterpret_cast<uint4*>(sV + ((x >> 3) & 1) * TF_TILE + (x >> 4) * 128 + (x & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (!wait1(p_full, g & 1)) { ok = false; break; }
+        tc_fence_after();
+        // P from TMEM, 16 keys = 8 packed columns per step
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_f16_tmem_a_by(leader, tm + 128, tm + kk * 8, dv + ((kk * 2048) >> 4), IDESC_O,
+                             (j > j0 || kk > 0) ? 1u : 0u);
+        umma_commit_by(leader, pv_done);
+        umma_commit_by(leader, v_empty);
+      }
+    }
+    umma_commit_by(leader, drain);
+    for (uint32_t i = 0; i < (1u << 22) && !mbar_try_wait(drain, 0); ++i) {}
+  } else {
+    // ---------------------------------------------------------- softmax
+    const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t t_s = tmem + lane_base, t_o = tmem + lane_base + 128;
+    const uint64_t sl2 = f2_pack(scale_log2, scale_log2);
+    bool ok = true;
+    uint32_t g = 0;   // S blocks consumed so far
+    auto wait_all = [&](uint64_t* bar, uint32_t par) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait_t<kFine>(bar, par, abort_flag, err, wlim));
+    };
+    for (int n = 0; ok; ++n) {
+      if (!wait_all(q_full, n & 1)) break;
+      const volatile int* f = item_ring + 4 * (n & 3);
+      const int h = f[0], qt = f[1], j0 = f[2];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_empty);   // this warp has the fields
+      if (h < 0) break;
+      const int w0 = qt * 128 + warp * 32, q = w0 + lane;   // the warp's first row, this thread's
+      const int lo = q < Tv ? __ldg(pk.lo + q) : 0;         // first key of the row
+      const int lo_max = __reduce_max_sync(0xffffffffu, lo);
+      float m_ref = -INFINITY, l = 0.f;   // reference max (log2 units) and row sum relative to it
+      for (int j = j0; j <= qt; ++j, ++g) {
+        if (!wait_all(s_full, g & 1)) { ok = false; break; }
+        tc_fence_after();
+        const int kbase = j * 128;
+        const bool diag = j == qt;
+        float mraw = -INFINITY;           // block max of the raw scores (the scale is positive)
+        // Packed rows meet masked blocks at every sequence boundary.  Straight-
+        // line code for a row and for each kind of mask, as below, left the
+        // softmax warps a fifth of their time without instructions, so here the
+        // row is read from TMEM 32 scores at a time, now and again for P, by
+        // loops that stay in the instruction cache, mask by bits and skip the
+        // chunks that no row of the warp sees (16,384 tokens of chats, 10 heads:
+        // 91 us instead of 103; whole rows of 2048: 229 instead of 217).
+        // Keys past the last sequence lie above every row of the diagonal block.
+        const bool masked = diag || kbase < lo_max;
+        // keys that this row sees, from kbase on: first .. end - 1
+        const int first = lo - kbase, end = q + 1 - kbase;
+        auto seen_of = [&](int c) { return low_bits(end - 32 * c) & ~low_bits(first - 32 * c); };
+        if (!masked) {
+          uint32_t xa[32], xb[32];
+#pragma unroll 1
+          for (int c = 0; c < 4; c += 2) {
+            tmem_load32_async(t_s + 32 * c, xa);
+            tmem_load32_async(t_s + 32 * c + 32, xb);
+            tmem_wait_ld();
+            mraw = max32(xb, max32(xa, mraw));
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t seen = seen_of(c);
+            if (__any_sync(0xffffffffu, seen != 0)) {
+              uint32_t x[32];
+              tmem_load32_async(t_s + 32 * c, x);
+              tmem_wait_ld();
+              mask_scores(x, seen);
+              mraw = max32(x, mraw);
+            }
+          }
+        }
+        const float mblk = mraw * scale_log2;
+        const bool move = mblk > m_ref + TF_RESCALE;   // true on the first block with a visible key
+        const float m_new = move ? mblk : m_ref;
+        // 1 when the reference stays, 0 when it leaves -inf; a row that has seen
+        // only masked scores (window edge) keeps -inf and offsets by 0 below
+        const bool none = m_new == -INFINITY;
+        const float factor = none ? 1.f : ex2_approx(m_ref - m_new);
+        // O holds the products of blocks < j (S of this block was issued after
+        // the last of them completed), so it may be rescaled now
+        if (j > j0 && __any_sync(0xffffffffu, move)) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t ra[32];
+            tmem_load32_async(t_o + c * 32, ra);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) ra[k] = __float_as_uint(__uint_as_float(ra[k]) * factor);
+            tmem_store32(t_o + c * 32, ra);
+          }
+        }
+        // probabilities relative to the reference (masked scores give 0), row sum,
+        // bf16 P over the first 64 columns of S
+        const float m_off = none ? 0.f : m_new;
+        const uint64_t nb2 = f2_pack(-m_off, -m_off);
+        uint64_t rs2 = f2_pack(0.f, 0.f);
+        auto probabilities = [&](const uint32_t (&x)[32], int c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            float p[8];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(x[k + e]), __uint_as_float(x[k + e + 1])), sl2, nb2), x0, x1);
+              if (e < ((k & 8) ? GPT_FWD_MUFU_ODD : GPT_FWD_MUFU_EVEN)) {
+                p[e] = ex2_approx(x0);
+                p[e + 1] = ex2_approx(x1);
+              } else {
+                f2_unpack(f2_exp2_poly(f2_pack(fmaxf(x0, -126.f), fmaxf(x1, -126.f))), p[e], p[e + 1]);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              rs2 = f2_add(rs2, f2_pack(p[e], p[e + 1]));
+              pk[(k + e) >> 1] = pack_bf16x2(p[e], p[e + 1]);
+            }
+          }
+          tmem_store16(t_s + 16 * c, pk);
+        };
+        if (!masked) {
+          uint32_t xa[32], xb[32];
+          tmem_load32_async(t_s, xa);
+          tmem_landed(xa);
+#pragma unroll 1
+          for (int c = 0; c < 4; c += 2) {
+            tmem_load32_async(t_s + 32 * c + 32, xb);
+            probabilities(xa, c);
+            tmem_landed(xb);
+            if (c == 0) tmem_load32_async(t_s + 64, xa);
+            probabilities(xb, c + 1);
+            tmem_landed(xa);
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t seen = seen_of(c);
+            if (__any_sync(0xffffffffu, seen != 0)) {
+              uint32_t x[32];
+              tmem_load32_async(t_s + 32 * c, x);
+              tmem_wait_ld();
+              mask_scores(x, seen);
+              probabilities(x, c);
+            } else {
+              uint32_t pk[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) pk[k] = 0u;
+              tmem_store16(t_s + 16 * c, pk);
+            }
+          }
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        mbar_arrive(p_full);
+        float rs0, rs1;
+        f2_unpack(rs2, rs0, rs1);
+        l = l * factor + (rs0 + rs1);
+        m_ref = m_new;
+      }
+      // epilogue: O / l once the last P V has landed
+      if (ok) ok = wait_all(pv_done, (g - 1) & 1);
+      if (ok) {
+        tc_fence_after();
+        const float inv = 1.f / l;
+        bf16* orow = o + w0 * pk.o_tok + h * pk.o_head;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32)
+          store_rows<32>(t_o + c, inv, sOut + warp * 2048, orow + c, pk.o_tok, Tv - w0);
+        if (q < Tv) lse[static_cast<long long>(h) * T + q] = (m_ref + log2f(l)) * 0.69314718055994531f;
+        // O has been read: the next item's first P V may overwrite it
+        tc_fence_before();
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
   }
 }
 
@@ -1731,26 +1917,26 @@ __global__ void attn_bwd_dot_kernel(const bf16* __restrict__ o, const bf16* __re
 
 // --------------------------------------------------- packed: plan and setup
 
-// A plan: kPlanMeta words, lo and hi [T], forward entries [pairs of tiles],
-// backward entries [key blocks].
+// A plan: kPlanMeta words, lo and hi [T], forward entries [tiles], backward
+// entries [key blocks].
 struct PlanView {
   int* meta;
   int* lo;
   int* hi;
-  int4* fwd;
+  int2* fwd;
   int2* bwd;
   size_t bytes;
 };
 __host__ __device__ inline PlanView plan_view(void* base, int T) {
-  const size_t n = (static_cast<size_t>(T) + 3) / 4 * 4, nq = (static_cast<size_t>(T) + 127) / 128;
+  const size_t n = (static_cast<size_t>(T) + 1) / 2 * 2, nq = (static_cast<size_t>(T) + 127) / 128;
   int* p = static_cast<int*>(base);
   PlanView v;
   v.meta = p;
   v.lo = p + kPlanMeta;
   v.hi = v.lo + n;
-  v.fwd = reinterpret_cast<int4*>(v.hi + n);
-  v.bwd = reinterpret_cast<int2*>(v.fwd + (nq + 1) / 2);
-  v.bytes = (kPlanMeta + 2 * n) * sizeof(int) + (nq + 1) / 2 * sizeof(int4) + nq * sizeof(int2);
+  v.fwd = reinterpret_cast<int2*>(v.hi + n);
+  v.bwd = v.fwd + nq;
+  v.bytes = (kPlanMeta + 2 * n) * sizeof(int) + 2 * nq * sizeof(int2);
   return v;
 }
 
@@ -1813,19 +1999,29 @@ __global__ void __launch_bounds__(1024)
     P.meta[kMetaT] = T;
     P.meta[kMetaMagic] = kPlanMagic;
   }
-  const int nb = (valid + 127) / 128, count = dir ? nb : (nb + 1) / 2;
-  // entry e; w: its steps
-  auto entry = [&](int e) -> int4 {
-    if (dir) {
-      const int n = (hi_of(min(e * 128 + 127, valid - 1)) >> 7) - e + 1;   // hi grows with the key
-      return make_int4(e, n, 0, n);
+  const int count = (valid + 127) / 128;
+  // entry e, and its steps
+  auto entry = [&](int e, int* steps) -> int2 {
+    if (dir) {   // hi grows with the key
+      *steps = (hi_of(min(e * 128 + 127, valid - 1)) >> 7) - e + 1;
+      return make_int2(e, *steps);
     }
-    const int qt = 2 * e, a = lo_of(qt * 128) >> 7, b = qt + 1 < nb ? lo_of(qt * 128 + 128) >> 7 : -1;
-    return make_int4(qt, a, b, (b >= 0 ? qt + 2 : qt + 1) - a);
+    const int a = lo_of(e * 128) >> 7;
+    *steps = e + 1 - a;
+    return make_int2(e, a);
   };
-  const int4 mine = tid < count ? entry(tid) : make_int4(0, 0, 0, 0);
-  for (int e = tid; e < count; e += 1024)
-    atomicAdd(&hist[kBuckets - min((e == tid ? mine : entry(e)).w, kBuckets)], 1);
+  auto bucket = [](int steps) { return kBuckets - min(steps, kBuckets); };
+  int steps = 0;
+  int2 mine = make_int2(0, 0);   // each thread's first entry is searched once
+  if (tid < count) {
+    mine = entry(tid, &steps);
+    atomicAdd(&hist[bucket(steps)], 1);
+  }
+  for (int e = tid + 1024; e < count; e += 1024) {
+    int n;
+    entry(e, &n);
+    atomicAdd(&hist[bucket(n)], 1);
+  }
   __syncthreads();
   // exclusive sums of the 1024 buckets, one per thread
   const int in_bucket = hist[tid];
@@ -1842,11 +2038,12 @@ __global__ void __launch_bounds__(1024)
   if (tid == 0) P.meta[dir ? kMetaBwd : kMetaFwd] = count;
   hist[tid] = before;
   __syncthreads();
-  for (int e = tid; e < count; e += 1024) {
-    const int4 v = e == tid ? mine : entry(e);
-    const int at = atomicAdd(&hist[kBuckets - min(v.w, kBuckets)], 1);
-    if (dir) P.bwd[at] = make_int2(v.x, v.y);
-    else P.fwd[at] = make_int4(v.x, v.y, v.z, 0);
+  int2* order = dir ? P.bwd : P.fwd;
+  if (tid < count) order[atomicAdd(&hist[bucket(steps)], 1)] = mine;
+  for (int e = tid + 1024; e < count; e += 1024) {
+    int n;
+    const int2 v = entry(e, &n);
+    order[atomicAdd(&hist[bucket(n)], 1)] = v;
   }
 }
 
@@ -1976,7 +2173,7 @@ void launch_attn_fwd(const bf16* q, const bf16* k, const bf16* v, bf16* o, float
                      long long wait_cycles) {
   // a limit shorter than one blocking probe needs the finely polling build
   const bool fine = wait_limit_or_default(wait_cycles) < kShortWaitCycles;
-  auto kern = fine ? attn_fwd_tc_kernel<true, false> : attn_fwd_tc_kernel<false, false>;
+  auto kern = fine ? attn_fwd_tc_kernel<true> : attn_fwd_tc_kernel<false>;
   static std::atomic<unsigned long long> configured[2] = {};
   if (set_smem_limit_once(kern, TF_SMEM, configured[fine ? 1 : 0]) != cudaSuccess) {
     if (err) cudaMemsetAsync(err, 0xff, sizeof(int), s);   // latched as a device error
@@ -1998,7 +2195,7 @@ void launch_attn_fwd(const bf16* q, const bf16* k, const bf16* v, bf16* o, float
   const float scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(HD));
   kern<<<grid, 384, TF_SMEM, s>>>(mq, mk, mv, o, lse, H, Hkv, kv_stride, T, window_bound(window, T),
                                                 scale_log2,
-                                                static_cast<int>(n_items), sched_word(sched, s), err, wait_cycles, PackedArgs{});
+                                                static_cast<int>(n_items), sched_word(sched, s), err, wait_cycles);
 }
 
 void launch_attn_bwd(const bf16* q, const bf16* k, const bf16* v, const bf16* o, const bf16* dout,
@@ -2076,9 +2273,9 @@ cudaError_t launch_attn_packed_fwd(const PackedTensor& q, const PackedTensor& k,
                                    const PackedTensor& o, float* lse, int H, int Hkv, int T, float scale,
                                    const void* plan, cudaStream_t s, int* err, long long wait_cycles) {
   const bool fine = wait_limit_or_default(wait_cycles) < kShortWaitCycles;
-  auto kern = fine ? attn_fwd_tc_kernel<true, true> : attn_fwd_tc_kernel<false, true>;
+  auto kern = fine ? attn_packed_fwd_kernel<true> : attn_packed_fwd_kernel<false>;
   static std::atomic<unsigned long long> configured[2] = {};
-  cudaError_t e = set_smem_limit_once(kern, TF_SMEM, configured[fine ? 1 : 0]);
+  cudaError_t e = set_smem_limit_once(kern, PF_SMEM, configured[fine ? 1 : 0]);
   if (e != cudaSuccess) return e;
   CUtensorMap mq, mk, mv;
   if (!map_heads(&mq, q, T, H) || !map_heads(&mk, k, T, Hkv) || !map_heads(&mv, v, T, Hkv))
@@ -2090,9 +2287,9 @@ cudaError_t launch_attn_packed_fwd(const PackedTensor& q, const PackedTensor& k,
   pa.fwd = P.fwd;
   pa.o_tok = o.tok;
   pa.o_head = o.head;
-  const int items = ((T + 127) / 128 + 1) / 2 * H;   // a block each; most are taken over before they start
-  kern<<<items, 384, TF_SMEM, s>>>(mq, mk, mv, static_cast<bf16*>(const_cast<void*>(o.ptr)), lse, H, Hkv, Hkv, T,
-                                   1 << 30, scale * 1.4426950408889634f, 0, nullptr, err, wait_cycles, pa);
+  const int items = (T + 127) / 128 * H;   // a block each; most are taken over before they start
+  kern<<<items, 192, PF_SMEM, s>>>(mq, mk, mv, static_cast<bf16*>(const_cast<void*>(o.ptr)), lse, H, Hkv, T,
+                                   scale * 1.4426950408889634f, err, wait_cycles, pa);
   return cudaGetLastError();
 }
 
