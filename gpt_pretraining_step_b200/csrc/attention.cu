@@ -1102,6 +1102,14 @@ __device__ __forceinline__ void store_row_units(uint8_t* tile, const uint32_t (&
 constexpr int TB_STAGE = 32768;   // dQ staging: 4 warps x two [32 queries][32 dims] fp32 boxes
 constexpr int TB_SMEM = 6 * TF_BUF + TB_STAGE + 2048 + 256;
 
+// Copies `bytes` (a multiple of 16; both addresses too) to shared memory, counted on bar.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 // Query-block loop of key block j: nb query blocks j .. (window end) for each
 // of the G query heads of the group.
 struct BwdBlock {
@@ -1267,12 +1275,17 @@ __global__ void __launch_bounds__(512, 1)
         const int i = kb.q_block(it), h = kb.q_head(it), bh = kb.b * H + h;
         const int s = g & 1;
         if (!mbar_wait_t<kFine>(&q_empty[s], ((g >> 1) & 1) ^ 1u, abort_flag, err, wlim)) return false;
-        mbar_arrive_expect_tx(&q_full[s], TF_BUF);
+        // packed: the rows' -lse and -D come with Q and dO, from [H][128 nq] arrays
+        constexpr uint32_t kRows = kPacked ? 512 : 0;
+        const long long rows = kPacked ? static_cast<long long>(h) * nq * 128 + i * 128 : 0;
+        mbar_arrive_expect_tx(&q_full[s], TF_BUF + kRows);
+        if constexpr (kPacked) bulk_load(lse_s + s * 128, lse + rows, kRows, &q_full[s]);
         tma_load_3d(sQ + s * TF_BUF, mq, &q_full[s], 0, i * 128, bh);
         tma_load_3d(sQ + s * TF_BUF + TF_TILE, mq, &q_full[s], 64, i * 128, bh);
         ++issued_q;
         if (!mbar_wait_t<kFine>(do_empty, (g & 1) ^ 1u, abort_flag, err, wlim)) return false;
-        mbar_arrive_expect_tx(do_full, TF_BUF);
+        mbar_arrive_expect_tx(do_full, TF_BUF + kRows);
+        if constexpr (kPacked) bulk_load(dd_s + s * 128, Dv + rows, kRows, do_full);
         tma_load_4d(sdO, mdo, do_full, 0, h, i * 128, kb.b);
         tma_load_4d(sdO + TF_TILE, mdo, do_full, 64, h, i * 128, kb.b);
         ++issued_do;
@@ -1551,12 +1564,17 @@ __global__ void __launch_bounds__(512, 1)
     };
     // Every decision to leave a loop is taken by this vote, so the eight
     // warps always meet at the same named barriers: a warp that left on its
-    // own would leave the others waiting at the next vote.
+    // own would leave the others waiting at the next vote.  The packed build has
+    // no such barrier (its lse and D come by TMA), so there a warp decides alone.
+    auto passed = [&](bool got) -> bool {
+      if constexpr (kPacked) return __all_sync(0xffffffffu, got);
+      else return !any_fail(got);
+    };
     int g0 = 0;
     for (int n = 0; ok; ++n) {
       {
         const bool got = mbar_wait_t<kFine>(kv_full, n & 1, abort_flag, err, wlim);
-        if (any_fail(got)) { ok = false; break; }
+        if (!passed(got)) { ok = false; break; }
       }
       const int idx = item_ring[n & 3];
       __syncwarp();
@@ -1699,18 +1717,24 @@ __global__ void __launch_bounds__(512, 1)
           do_chunk(std::integral_constant<int, 1>{});
         };
 
-        publish(0, fetch(0));
-        float staged = n_it > 1 ? fetch(1) : 0.f;
+        float staged = 0.f;
+        if constexpr (!kPacked) {
+          publish(0, fetch(0));
+          if (n_it > 1) staged = fetch(1);
+        }
         // it = -1 only computes P of the first block
         for (int it = -1; it < n_it && ok; ++it) {
           const int gi = g0 + it;
           if (it >= 0) {
             // dS'_i = P_i (dP_i - D) once dP^T_i is in TMEM
-            const bool got = mbar_wait_t<kFine>(dp_full, gi & 1, abort_flag, err, wlim);
-            if (any_fail(got)) { ok = false; break; }
-            // every thread is past block i-1's use of buffer (i+1) & 1
-            if (it + 1 < n_it) publish(it + 1, staged);
-            if (it + 2 < n_it) staged = fetch(it + 2);
+            const bool got = mbar_wait_t<kFine>(dp_full, gi & 1, abort_flag, err, wlim) &&
+                             (!kPacked || mbar_wait_t<kFine>(do_full, gi & 1, abort_flag, err, wlim));   // D is here
+            if (!passed(got)) { ok = false; break; }
+            if constexpr (!kPacked) {
+              // every thread is past block i-1's use of buffer (i+1) & 1
+              if (it + 1 < n_it) publish(it + 1, staged);
+              if (it + 2 < n_it) staged = fetch(it + 2);
+            }
             tc_fence_after();
             uint32_t da[32], db[32];
             tmem_load32_async(tmem + lane_base + 128 + (2 * half) * 32, da);
@@ -1750,8 +1774,10 @@ __global__ void __launch_bounds__(512, 1)
           }
           // P_{i+1} while the tensor cores run this block's dV, dK, dQ
           if (it + 1 < n_it) {
-            const bool got1 = mbar_wait_t<kFine>(s_full, (gi + 1) & 1, abort_flag, err, wlim);
-            if (any_fail(got1)) { ok = false; break; }   // also publishes lse/D of block i+1
+            const bool got1 = mbar_wait_t<kFine>(s_full, (gi + 1) & 1, abort_flag, err, wlim) &&
+                              (!kPacked || mbar_wait_t<kFine>(&q_full[(gi + 1) & 1], ((gi + 1) >> 1) & 1, abort_flag,
+                                                              err, wlim));   // lse is here
+            if (!passed(got1)) { ok = false; break; }   // not packed: also publishes lse/D of block i+1
             tc_fence_after();
             compute_p(it + 1);
           }
@@ -1759,7 +1785,7 @@ __global__ void __launch_bounds__(512, 1)
         // dK and dV of this key block, complete with the last block's products
         if (ok) {
           const bool got = mbar_wait_t<kFine>(mm_done, (g0 + n_it - 1) & 1, abort_flag, err, wlim);
-          ok = !any_fail(got);
+          ok = passed(got);
         }
         if (ok && dqkv) {
           // straight into the token-major q|k|v gradient rows: dV as it is, dK
@@ -2085,40 +2111,55 @@ __device__ __forceinline__ void packed_setup(const SetupMaps& in, CUtensorMap* o
         : "memory");
 }
 
-// Backward: D[h, t] = sum_i dO * O of the rows that hold sequences and
-// zeros in the fp32 dq accumulator, some (t, h) rows a warp, whose loads are
-// issued together; the first block does the setup.
+// Before the backward, for the rows that hold sequences: nd = -D, D[h, t] =
+// sum_i dO * O, nl = -lse in log2 units, both [H][T rounded up to 128] and
+// filled up to the end of the last row's tile (nl -inf: P = 0), and zeros in
+// the fp32 dq accumulator.  A warp takes kRowsPerWarp tokens of a head, whose
+// loads are issued together; the first block does the setup and the fill.
 constexpr int kRowsPerWarp = 4;
 __global__ void __launch_bounds__(256)
     attention_packed_pre_kernel(const __grid_constant__ SetupMaps in, CUtensorMap* out, int* ctl, const int* meta,
                                 const bf16* __restrict__ o, long long o_tok, long long o_head,
                                 const bf16* __restrict__ dout, long long do_tok, long long do_head,
-                                float* __restrict__ Dv, float* __restrict__ dq, int H, int T, int* err) {
+                                const float* __restrict__ lse, float* __restrict__ nl, float* __restrict__ nd,
+                                float* __restrict__ dq, int H, int T, int* err) {
   __shared__ __align__(128) CUtensorMap stage[4];
+  const bool fits = meta[kMetaMagic] == kPlanMagic && meta[kMetaT] == T;
+  const int valid = fits ? meta[kMetaTotal] : 0, pitch = (T + 127) / 128 * 128, lane = lane_id();
   if (blockIdx.x == 0) {
     if (warp_id() == 0) packed_setup(in, out, ctl, meta, T, err, stage);
+    const int fill = (valid + 127) / 128 * 128 - valid;
+    for (int i = threadIdx.x; i < H * fill; i += 256) {
+      const long long at = static_cast<long long>(i / fill) * pitch + valid + i % fill;
+      nl[at] = -INFINITY;
+      nd[at] = 0.f;
+    }
     return;
   }
-  if (meta[kMetaMagic] != kPlanMagic || meta[kMetaT] != T) return;
-  // T * H fits in an int
-  const int rows = meta[kMetaTotal] * H, w = ((blockIdx.x - 1) * 8 + warp_id()) * kRowsPerWarp;
+  const int groups = (valid + kRowsPerWarp - 1) / kRowsPerWarp, w = (blockIdx.x - 1) * 8 + warp_id();
+  if (w >= groups * H) return;
+  const int h = w / groups, t0 = (w - h * groups) * kRowsPerWarp, n = min(kRowsPerWarp, valid - t0);
   uint2 x[kRowsPerWarp], y[kRowsPerWarp];
 #pragma unroll
   for (int i = 0; i < kRowsPerWarp; ++i) {
-    if (w >= rows - i) break;
-    const int t = (w + i) / H, h = w + i - t * H;
-    x[i] = *reinterpret_cast<const uint2*>(o + t * o_tok + h * o_head + lane_id() * 4);
-    y[i] = *reinterpret_cast<const uint2*>(dout + t * do_tok + h * do_head + lane_id() * 4);
+    if (i >= n) break;
+    x[i] = *reinterpret_cast<const uint2*>(o + (t0 + i) * o_tok + h * o_head + lane * 4);
+    y[i] = *reinterpret_cast<const uint2*>(dout + (t0 + i) * do_tok + h * do_head + lane * 4);
   }
+  const float l = lane < n ? lse[static_cast<long long>(h) * T + t0 + lane] : 0.f;
+  float d = 0.f;
 #pragma unroll
   for (int i = 0; i < kRowsPerWarp; ++i) {
-    if (w >= rows - i) break;
-    const int t = (w + i) / H, h = w + i - t * H, row = h * T + t;
-    reinterpret_cast<float4*>(dq + static_cast<long long>(row) * HD)[lane_id()] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float s = bf16_lo(x[i].x) * bf16_lo(y[i].x) + bf16_hi(x[i].x) * bf16_hi(y[i].x) + bf16_lo(x[i].y) * bf16_lo(y[i].y) +
-              bf16_hi(x[i].y) * bf16_hi(y[i].y);
-    s = warp_sum(s);
-    if (lane_id() == 0) Dv[row] = s;
+    if (i >= n) break;
+    reinterpret_cast<float4*>(dq + (static_cast<long long>(h) * T + t0 + i) * HD)[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float s = warp_sum(bf16_lo(x[i].x) * bf16_lo(y[i].x) + bf16_hi(x[i].x) * bf16_hi(y[i].x) +
+                             bf16_lo(x[i].y) * bf16_lo(y[i].y) + bf16_hi(x[i].y) * bf16_hi(y[i].y));
+    if (lane == i) d = s;
+  }
+  if (lane < n) {
+    const long long at = static_cast<long long>(h) * pitch + t0 + lane;
+    nl[at] = l * -1.4426950408889634f;
+    nd[at] = -d;
   }
 }
 
@@ -2246,7 +2287,7 @@ namespace {
 
 constexpr size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 
-// control words, then the four tensor maps, then (backward) D and the fp32 dq
+// scratch of a backward: control words, then the four tensor maps
 constexpr size_t kPackedHead = 256 + 4 * sizeof(CUtensorMap);
 
 // Strides of an extent-1 dimension are never used: any legal value stands in.
@@ -2260,9 +2301,10 @@ bool map_heads(CUtensorMap* m, const PackedTensor& t, long long tokens, long lon
 
 size_t attention_plan_bytes(int T) { return al256(plan_view(nullptr, T).bytes); }
 
+// then -lse and -D, [H][T rounded up to 128] each, and the fp32 dq [H][T][128]
 size_t attention_packed_bwd_scratch(int T, int H) {
-  const size_t rows = static_cast<size_t>(T) * H;
-  return al256(kPackedHead) + al256(rows * sizeof(float)) + al256(rows * HD * sizeof(float));
+  const size_t padded = (static_cast<size_t>(T) + 127) / 128 * 128 * H, rows = static_cast<size_t>(T) * H;
+  return al256(kPackedHead) + 2 * al256(padded * sizeof(float)) + al256(rows * HD * sizeof(float));
 }
 
 void launch_attention_plan(const int* cu, int n_seq, int T, int window, void* plan, int* err, cudaStream_t s) {
@@ -2307,8 +2349,10 @@ cudaError_t launch_attn_packed_bwd(const PackedTensor& q, const PackedTensor& k,
   uint8_t* base = static_cast<uint8_t*>(scratch);
   int* ctl = reinterpret_cast<int*>(base);
   CUtensorMap* dmaps = reinterpret_cast<CUtensorMap*>(base + 256);
-  float* Dv = reinterpret_cast<float*>(base + al256(kPackedHead));
-  float* acc = reinterpret_cast<float*>(base + al256(kPackedHead) + al256(rows * sizeof(float)));
+  const size_t padded = al256((static_cast<size_t>(T) + 127) / 128 * 128 * H * sizeof(float));
+  float* nl = reinterpret_cast<float*>(base + al256(kPackedHead));
+  float* nd = reinterpret_cast<float*>(base + al256(kPackedHead) + padded);
+  float* acc = reinterpret_cast<float*>(base + al256(kPackedHead) + 2 * padded);
   SetupMaps maps = {};
   CUtensorMap mdq;
   const long long dims[4] = {HD, H, T, 1};
@@ -2320,9 +2364,10 @@ cudaError_t launch_attn_packed_bwd(const PackedTensor& q, const PackedTensor& k,
     return cudaErrorInvalidValue;
   const PlanView P = plan_view(const_cast<void*>(plan), T);
   const int row_blocks = static_cast<int>((rows + 8 * kRowsPerWarp - 1) / (8 * kRowsPerWarp));
-  attention_packed_pre_kernel<<<1 + row_blocks, 256, 0, s>>>(
+  const int pre_blocks = static_cast<int>((((T + kRowsPerWarp - 1ll) / kRowsPerWarp) * H + 7) / 8);
+  attention_packed_pre_kernel<<<1 + pre_blocks, 256, 0, s>>>(
       maps, dmaps, ctl, P.meta, static_cast<const bf16*>(o.ptr), o.tok, o.head, static_cast<const bf16*>(dout.ptr),
-      dout.tok, dout.head, Dv, acc, H, T, err);
+      dout.tok, dout.head, lse, nl, nd, acc, H, T, err);
   PackedArgs pa = {};
   pa.hi = P.hi;
   pa.bwd = P.bwd;
@@ -2334,7 +2379,7 @@ cudaError_t launch_attn_packed_bwd(const PackedTensor& q, const PackedTensor& k,
   pa.dv_head = dv.head;
   const long long units = 1ll * ((T + 127) / 128) * Hkv;
   const int grid = static_cast<int>(std::min<long long>(units, device_sm_count()));
-  kern<<<grid, 512, TB_SMEM, s>>>(maps.m[0], maps.m[1], maps.m[2], maps.m[3], mdq, lse, Dv,
+  kern<<<grid, 512, TB_SMEM, s>>>(maps.m[0], maps.m[1], maps.m[2], maps.m[3], mdq, nl, nd,
                                   static_cast<bf16*>(const_cast<void*>(dk.ptr)),
                                   static_cast<bf16*>(const_cast<void*>(dv.ptr)), H, Hkv, Hkv, T, 1 << 30, scale, 0,
                                   ctl + kCtlSched, err, wait_cycles, nullptr, nullptr, nullptr, pa);
