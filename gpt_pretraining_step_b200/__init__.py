@@ -471,19 +471,19 @@ def attention_bwd(q, k, v, o, lse, dout, window=-1, stream=None):
 #
 # A tensor of another type, shape or device than the call takes would be read
 # out of range, so these calls check theirs.  They are made once per layer, on
-# batches that may be small: the checks compare plain integers and the stream
-# comes as a raw handle, which keeps a call to some ten microseconds of host time.
+# batches that may be small, where the host's time is the call's: the checks
+# compare plain integers, outputs come from an argument's new_empty (a third
+# less than torch.empty with its type and device) and the stream as a raw handle.
 
 def _refuse(name, t, want):
     raise GptError(GPT_EINVAL, f"{name} must be {want}; got {t.dtype} {tuple(t.shape)} with strides {t.stride()} "
                                f"on {t.device}")
 
 
-def _current(name, t):
+def _current(torch, name, t):
     """Index of t's device, which has to be the current one (its streams run the call)."""
-    import torch
     dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise GptError(GPT_EINVAL, f"{name} is on {t.device}, not on the current CUDA device")
     return dev
 
@@ -495,30 +495,33 @@ def _flat(name, t, dtype, shape, dev):
     return t.data_ptr()
 
 
-def _heads(name, t, n, heads, dev, bf16):
+def _heads(name, t, shape, dev, bf16):
     """gpt_heads of a [n, heads, 128] tensor argument."""
-    if t.dtype != bf16 or t.shape != (n, heads, 128) or t.get_device() != dev or t.stride(2) != 1:
-        _refuse(name, t, f"a bf16 tensor {(n, heads, 128)} with contiguous rows of 128 on cuda:{dev}")
-    return Heads(t.data_ptr(), t.stride(0), t.stride(1))
+    if t.dtype != bf16 or t.shape != shape or t.get_device() != dev:
+        _refuse(name, t, f"a bf16 tensor {shape} on cuda:{dev}")
+    token, head, one = t.stride()
+    if one != 1:
+        _refuse(name, t, "a tensor with contiguous rows of 128")
+    return Heads(t.data_ptr(), token, head)
 
 
-def _raw_stream(stream, dev, made=()):
+def _raw_stream(torch, stream, dev, *made):
     """Handle of `stream` or of the current one.  Memory of the tensors made
     for the call must not be given out again on the current stream before
     another stream's work on it has run."""
-    import torch
     current = torch._C._cuda_getCurrentRawStream(dev)
     if stream is None or stream.cuda_stream == current:
         return current
     for t in made:
-        t.record_stream(stream)
+        if t is not None:
+            t.record_stream(stream)
     return stream.cuda_stream
 
 
 @functools.lru_cache(maxsize=256)
-def _bytes(query, *sizes):
-    """Size of a plan or scratch buffer (a pure function of its arguments)."""
-    return max(getattr(lib(), query)(*sizes), 256)
+def _words(query, *sizes):
+    """Size of a plan or scratch buffer in 4-byte words (a pure function of its arguments)."""
+    return (max(getattr(lib(), query)(*sizes), 256) + 3) // 4
 
 
 class AttentionPlan:
@@ -526,9 +529,9 @@ class AttentionPlan:
 
     def __init__(self, cu_seqlens, n_tokens, window=-1, stream=None):
         import torch
-        self.n_tokens, self.window, self.device = int(n_tokens), int(window), _current("cu_seqlens", cu_seqlens)
-        self.buf = torch.empty(_bytes("gpt_op_attention_plan_bytes", self.n_tokens), dtype=torch.uint8,
-                               device=cu_seqlens.device)
+        self.n_tokens, self.window = int(n_tokens), int(window)
+        self.device = _current(torch, "cu_seqlens", cu_seqlens)
+        self.buf = cu_seqlens.new_empty(_words("gpt_op_attention_plan_bytes", self.n_tokens), dtype=torch.int32)
         self.update(cu_seqlens, stream)
 
     def update(self, cu_seqlens, stream=None):
@@ -539,7 +542,7 @@ class AttentionPlan:
             _refuse("cu_seqlens", cu_seqlens, "[sequences + 1]")
         cu = _flat("cu_seqlens", cu_seqlens, torch.int32, (n,), self.device)
         _check(lib().gpt_op_attention_plan(cu, n - 1, self.n_tokens, self.window, self.buf.data_ptr(),
-                                           _raw_stream(stream, self.device, (self.buf,))))
+                                           _raw_stream(torch, stream, self.device, self.buf)))
 
 
 def attention_plan(cu_seqlens, n_tokens, window=-1, stream=None):
@@ -555,16 +558,18 @@ def attention_packed_fwd(q, k, v, plan, scale=0.0, o=None, lse=None, stream=None
     [H, n_tokens], new unless given; rows past the last sequence keep what
     they held (new tensors: anything)."""
     import torch
-    n, dev, bf16 = plan.n_tokens, _current("q", q), torch.bfloat16
+    n, dev, bf16, f32 = plan.n_tokens, _current(torch, "q", q), torch.bfloat16, torch.float32
     H, Hkv = q.shape[1], k.shape[1]
+    rows, kv_rows = (n, H, 128), (n, Hkv, 128)
+    hq, hk, hv = (_heads("q", q, rows, dev, bf16), _heads("k", k, kv_rows, dev, bf16),
+                  _heads("v", v, kv_rows, dev, bf16))
     if o is None:
-        o = torch.empty((n, H, 128), dtype=bf16, device=q.device)
+        o = q.new_empty(rows)
     if lse is None:
-        lse = torch.empty((H, n), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((H, n), dtype=f32)
     _check(lib().gpt_op_attention_packed_fwd(
-        _heads("q", q, n, H, dev, bf16), _heads("k", k, n, Hkv, dev, bf16), _heads("v", v, n, Hkv, dev, bf16),
-        _heads("o", o, n, H, dev, bf16), _flat("lse", lse, torch.float32, (H, n), dev), n, H, Hkv, scale,
-        plan.buf.data_ptr(), _raw_stream(stream, dev, (o, lse))))
+        hq, hk, hv, _heads("o", o, rows, dev, bf16), _flat("lse", lse, f32, (H, n), dev), n, H, Hkv, scale,
+        plan.buf.data_ptr(), _raw_stream(torch, stream, dev, o, lse)))
     return o, lse
 
 
@@ -572,51 +577,56 @@ def attention_packed_bwd(q, k, v, o, lse, dout, plan, scale=0.0, dq=None, dk=Non
     """Gradients (bf16, shaped as q, k and v; new unless given) of
     attention_packed_fwd, from its o and lse and the gradient dout of o."""
     import torch
-    n, dev, bf16 = plan.n_tokens, _current("q", q), torch.bfloat16
+    n, dev, bf16, f32 = plan.n_tokens, _current(torch, "q", q), torch.bfloat16, torch.float32
     H, Hkv = q.shape[1], k.shape[1]
+    rows, kv_rows = (n, H, 128), (n, Hkv, 128)
+    hq, hk, hv = (_heads("q", q, rows, dev, bf16), _heads("k", k, kv_rows, dev, bf16),
+                  _heads("v", v, kv_rows, dev, bf16))
     if dq is None:
-        dq = torch.empty((n, H, 128), dtype=bf16, device=q.device)
+        dq = q.new_empty(rows)
     if dk is None:
-        dk = torch.empty((n, Hkv, 128), dtype=bf16, device=q.device)
+        dk = q.new_empty(kv_rows)
     if dv is None:
-        dv = torch.empty((n, Hkv, 128), dtype=bf16, device=q.device)
-    scratch = torch.empty(_bytes("gpt_op_attention_packed_bwd_scratch", n, H), dtype=torch.uint8, device=q.device)
+        dv = q.new_empty(kv_rows)
+    scratch = q.new_empty(_words("gpt_op_attention_packed_bwd_scratch", n, H), dtype=f32)
     _check(lib().gpt_op_attention_packed_bwd(
-        _heads("q", q, n, H, dev, bf16), _heads("k", k, n, Hkv, dev, bf16), _heads("v", v, n, Hkv, dev, bf16),
-        _heads("o", o, n, H, dev, bf16), _flat("lse", lse, torch.float32, (H, n), dev),
-        _heads("dout", dout, n, H, dev, bf16), _heads("dq", dq, n, H, dev, bf16), _heads("dk", dk, n, Hkv, dev, bf16),
-        _heads("dv", dv, n, Hkv, dev, bf16), n, H, Hkv, scale, plan.buf.data_ptr(), scratch.data_ptr(),
-        _raw_stream(stream, dev, (dq, dk, dv, scratch))))
+        hq, hk, hv, _heads("o", o, rows, dev, bf16), _flat("lse", lse, f32, (H, n), dev),
+        _heads("dout", dout, rows, dev, bf16), _heads("dq", dq, rows, dev, bf16),
+        _heads("dk", dk, kv_rows, dev, bf16), _heads("dv", dv, kv_rows, dev, bf16), n, H, Hkv, scale,
+        plan.buf.data_ptr(), scratch.data_ptr(), _raw_stream(torch, stream, dev, dq, dk, dv, scratch)))
     return dq, dk, dv
 
 
 def _rows(name, t, dev):
     """Row stride of a [M, V] tensor argument with contiguous rows."""
-    if t.dim() != 2 or t.get_device() != dev or (t.stride(1) != 1 and t.shape[1] > 1):
-        _refuse(name, t, f"[M, V] with contiguous rows on cuda:{dev}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    if t.dim() != 2 or t.get_device() != dev:
+        _refuse(name, t, f"[M, V] on cuda:{dev}")
+    (M, V), (row, one) = t.shape, t.stride()
+    if one != 1 and V > 1:
+        _refuse(name, t, "[M, V] with contiguous rows")
+    return row if M > 1 else max(row, V)
 
 
-def _loss_rows(logits, grad, dlogits):
+def _loss_rows(torch, logits, grad, dlogits):
     """(M, V, dtype code, row stride, gradient or None, its address and row
     stride, device) of both losses."""
-    import torch
-    dev = _current("logits", logits)
+    dev = _current(torch, "logits", logits)
     ld = _rows("logits", logits, dev)
     M, V = logits.shape
-    code = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}.get(logits.dtype)
-    if code is None:
+    dtype = logits.dtype
+    code = DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_FP32
+    if code == DTYPE_FP32 and dtype != torch.float32:
         _refuse("logits", logits, "bf16 or fp32")
     if not grad:
         return M, V, code, ld, None, None, ld, dev
     ld_d = ld
     if dlogits is None:
         # the rows' alignment follows the logits'
-        dlogits = torch.empty_strided((M, V), (ld, 1), dtype=logits.dtype, device=logits.device)
+        dlogits = logits.new_empty((M, V)) if ld == V else logits.new_empty_strided((M, V), (ld, 1))
     else:
         ld_d = _rows("dlogits", dlogits, dev)
-        if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype:
-            _refuse("dlogits", dlogits, f"{logits.dtype} {(M, V)}")
+        if dlogits.shape != logits.shape or dlogits.dtype != dtype:
+            _refuse("dlogits", dlogits, f"{dtype} {(M, V)}")
     return M, V, code, ld, dlogits, dlogits.data_ptr(), ld_d, dev
 
 
@@ -631,18 +641,17 @@ def policy_loss(logits, targets, old_logp, advantage, weight, ref_logp=None, kl_
     and of the clipped positions; dlogits (None with grad=False) is new unless
     given, and may be logits itself."""
     import torch
-    M, V, code, ld, dlogits, d, ld_d, dev = _loss_rows(logits, grad, dlogits)
-    f32 = torch.float32
-    stats = torch.empty(4, dtype=f32, device=logits.device)
-    logp = torch.empty(M, dtype=f32, device=logits.device)
-    scratch = torch.empty(_bytes("gpt_op_policy_loss_scratch", M), dtype=torch.uint8, device=logits.device)
+    M, V, code, ld, dlogits, d, ld_d, dev = _loss_rows(torch, logits, grad, dlogits)
+    f32, shape = torch.float32, (M,)
+    args = (_flat("targets", targets, torch.int32, shape, dev),
+            None if old_logp is None else _flat("old_logp", old_logp, f32, shape, dev),
+            None if ref_logp is None else _flat("ref_logp", ref_logp, f32, shape, dev),
+            _flat("advantage", advantage, f32, shape, dev), _flat("weight", weight, f32, shape, dev))
+    stats, logp = weight.new_empty(4), weight.new_empty(M)
+    scratch = weight.new_empty(_words("gpt_op_policy_loss_scratch", M))
     _check(lib().gpt_op_policy_loss(
-        logits.data_ptr(), code, ld, _flat("targets", targets, torch.int32, (M,), dev),
-        None if old_logp is None else _flat("old_logp", old_logp, f32, (M,), dev),
-        None if ref_logp is None else _flat("ref_logp", ref_logp, f32, (M,), dev),
-        _flat("advantage", advantage, f32, (M,), dev), _flat("weight", weight, f32, (M,), dev), M, V, clip_low,
-        clip_high, kl_coef, stats.data_ptr(), logp.data_ptr(), d, ld_d, scratch.data_ptr(),
-        _raw_stream(stream, dev, (stats, logp, scratch) + ((dlogits,) if grad else ()))))
+        logits.data_ptr(), code, ld, *args, M, V, clip_low, clip_high, kl_coef, stats.data_ptr(), logp.data_ptr(), d,
+        ld_d, scratch.data_ptr(), _raw_stream(torch, stream, dev, stats, logp, scratch, dlogits)))
     return stats, logp, dlogits
 
 
@@ -655,22 +664,19 @@ def preference_loss(logits, targets, cu_seqlens, ref_logp=None, beta=0.1, label_
     Returns (loss [], margin [pairs], seq_logp [2 pairs], logp [M], dlogits);
     rows past the last sequence keep what they held (new tensors: anything)."""
     import torch
-    M, V, code, ld, dlogits, d, ld_d, dev = _loss_rows(logits, grad, dlogits)
-    n, f32 = cu_seqlens.numel() - 1, torch.float32
+    M, V, code, ld, dlogits, d, ld_d, dev = _loss_rows(torch, logits, grad, dlogits)
+    n, f32, i32 = cu_seqlens.numel() - 1, torch.float32, torch.int32
     if n < 2 or n % 2:
         _refuse("cu_seqlens", cu_seqlens, "[2 * pairs + 1]")
-    loss = torch.empty((), dtype=f32, device=logits.device)
-    margin = torch.empty(n // 2, dtype=f32, device=logits.device)
-    seq_logp = torch.empty(n, dtype=f32, device=logits.device)
-    logp = torch.empty(M, dtype=f32, device=logits.device)
-    scratch = torch.empty(_bytes("gpt_op_preference_loss_scratch", M, n // 2), dtype=torch.uint8,
-                          device=logits.device)
+    y, cu = _flat("targets", targets, i32, (M,), dev), _flat("cu_seqlens", cu_seqlens, i32, (n + 1,), dev)
+    ref = None if ref_logp is None else _flat("ref_logp", ref_logp, f32, (n,), dev)
+    loss, margin = logits.new_empty((), dtype=f32), logits.new_empty(n // 2, dtype=f32)
+    seq_logp, logp = logits.new_empty(n, dtype=f32), logits.new_empty(M, dtype=f32)
+    scratch = targets.new_empty(_words("gpt_op_preference_loss_scratch", M, n // 2))
     _check(lib().gpt_op_preference_loss(
-        logits.data_ptr(), code, ld, _flat("targets", targets, torch.int32, (M,), dev),
-        _flat("cu_seqlens", cu_seqlens, torch.int32, (n + 1,), dev), n // 2,
-        None if ref_logp is None else _flat("ref_logp", ref_logp, f32, (n,), dev), M, V, beta, label_smoothing,
-        loss.data_ptr(), margin.data_ptr(), seq_logp.data_ptr(), logp.data_ptr(), d, ld_d, scratch.data_ptr(),
-        _raw_stream(stream, dev, (loss, margin, seq_logp, logp, scratch) + ((dlogits,) if grad else ()))))
+        logits.data_ptr(), code, ld, y, cu, n // 2, ref, M, V, beta, label_smoothing, loss.data_ptr(),
+        margin.data_ptr(), seq_logp.data_ptr(), logp.data_ptr(), d, ld_d, scratch.data_ptr(),
+        _raw_stream(torch, stream, dev, loss, margin, seq_logp, logp, scratch, dlogits)))
     return loss, margin, seq_logp, logp, dlogits
 
 
