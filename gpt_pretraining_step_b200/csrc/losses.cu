@@ -132,14 +132,9 @@ struct Softmax {
     for (int k = 0; k < N; ++k) {
 #pragma unroll
       for (int e = 0; e < n; e += 2) {
-#ifdef SCALAR
-        const float d0 = v[k][e] - b, d1 = v[k][e + 1] - b;
-        const float x0 = fmaf(d0, kLog2e, d0 * kLog2eLow), x1 = fmaf(d1, kLog2e, d1 * kLog2eLow);
-#else
         const uint64_t d = f2_add(f2_pack(v[k][e], v[k][e + 1]), nb);
         float x0, x1;
         f2_unpack(f2_fma(d, hi, f2_mul(d, lo)), x0, x1);
-#endif
         sum[e & 2] += ex2(x0);
         sum[(e & 2) + 1] += ex2(x1);
       }
