@@ -702,9 +702,6 @@ __global__ void __launch_bounds__(192, 2)
 
   const int warp = warp_id(), lane = lane_id();
   const long long wlim = wait_limit_or_default(wait_cycles);
-  // positions that hold sequences; a plan of another T is refused
-  const bool fits = pk.meta[kMetaMagic] == kPlanMagic && pk.meta[kMetaT] == T;
-  const int Tv = fits ? pk.meta[kMetaTotal] : 0;
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -714,7 +711,6 @@ __global__ void __launch_bounds__(192, 2)
     mbar_init(s_full, 1); mbar_init(p_full, 128); mbar_init(pv_done, 1);
     mbar_init(drain, 1);
     mbar_init(answered, 1);
-    if (!fits && blockIdx.x == 0 && err) atomicOr(err, ERRF_SHAPE);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tq);
@@ -729,6 +725,11 @@ __global__ void __launch_bounds__(192, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  chain_wait();
+  // positions that hold sequences; a plan of another T is refused
+  const bool fits = pk.meta[kMetaMagic] == kPlanMagic && pk.meta[kMetaT] == T;
+  const int Tv = fits ? pk.meta[kMetaTotal] : 0;
+  if (!fits && blockIdx.x == 0 && threadIdx.x == 0 && err) atomicOr(err, ERRF_SHAPE);
 
   if (warp == 4) {
     if (lane == 0) {
@@ -1199,7 +1200,6 @@ __global__ void __launch_bounds__(512, 1)
   const int warp = warp_id(), lane = lane_id();
   const int nq = (T + 127) / 128;
   const long long wlim = wait_limit_or_default(wait_cycles);
-  const int Tv = kPacked ? pa.ctl[kCtlValid] : T;   // positions of a row that hold sequences
   auto block_of = [&](int n, int idx) -> BwdBlock {
     if constexpr (kPacked) return bwd_block_packed(item_info + 4 * (n & 3), H, Hkv);
     else return bwd_block(idx, H, Hkv, kvs, nq, wl);
@@ -1237,6 +1237,8 @@ __global__ void __launch_bounds__(512, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  if constexpr (kPacked) chain_wait();
+  const int Tv = kPacked ? pa.ctl[kCtlValid] : T;   // positions of a row that hold sequences
 
   // registers: 72 for the TMA / MMA warp group, 96 for the dQ group, 168 for
   // the two softmax groups (4*72 + 4*96 + 8*168 = 2016 per lane of a warp,
@@ -1989,6 +1991,7 @@ __device__ __forceinline__ SeqRange seq_range(const int* cu, int n_seq, int T, i
 constexpr int kPlanSeqs = 4095;
 __global__ void __launch_bounds__(1024)
     attention_plan_kernel(const int* __restrict__ cu_arg, int n_seq, int T, int window, void* plan, int* err) {
+  chain_go();
   constexpr int kBuckets = 1024;
   __shared__ int cu_s[kPlanSeqs + 1];
   __shared__ int hist[kBuckets];
@@ -2124,6 +2127,8 @@ __global__ void __launch_bounds__(256)
                                 const float* __restrict__ lse, float* __restrict__ nl, float* __restrict__ nd,
                                 float* __restrict__ dq, int H, int T, int* err) {
   __shared__ __align__(128) CUtensorMap stage[4];
+  chain_go();
+  chain_wait();
   const bool fits = meta[kMetaMagic] == kPlanMagic && meta[kMetaT] == T;
   const int valid = fits ? meta[kMetaTotal] : 0, pitch = (T + 127) / 128 * 128, lane = lane_id();
   if (blockIdx.x == 0) {
@@ -2167,6 +2172,7 @@ __global__ void __launch_bounds__(256)
 __global__ void __launch_bounds__(256)
     attention_packed_dq_kernel(const float* __restrict__ acc, bf16* __restrict__ dq, long long dq_tok,
                                long long dq_head, const int* ctl, int H, int T) {
+  chain_wait();
   const int rows = ctl[kCtlValid] * H, w = (blockIdx.x * 8 + warp_id()) * kRowsPerWarp;
   float4 v[kRowsPerWarp];
 #pragma unroll
@@ -2330,9 +2336,8 @@ cudaError_t launch_attn_packed_fwd(const PackedTensor& q, const PackedTensor& k,
   pa.o_tok = o.tok;
   pa.o_head = o.head;
   const int items = (T + 127) / 128 * H;   // a block each; most are taken over before they start
-  kern<<<items, 192, PF_SMEM, s>>>(mq, mk, mv, static_cast<bf16*>(const_cast<void*>(o.ptr)), lse, H, Hkv, T,
-                                   scale * 1.4426950408889634f, err, wait_cycles, pa);
-  return cudaGetLastError();
+  return launch_chained(kern, items, 192, PF_SMEM, s, mq, mk, mv, static_cast<bf16*>(const_cast<void*>(o.ptr)), lse, H,
+                        Hkv, T, scale * 1.4426950408889634f, err, wait_cycles, pa);
 }
 
 cudaError_t launch_attn_packed_bwd(const PackedTensor& q, const PackedTensor& k, const PackedTensor& v,
@@ -2365,9 +2370,10 @@ cudaError_t launch_attn_packed_bwd(const PackedTensor& q, const PackedTensor& k,
   const PlanView P = plan_view(const_cast<void*>(plan), T);
   const int row_blocks = static_cast<int>((rows + 8 * kRowsPerWarp - 1) / (8 * kRowsPerWarp));
   const int pre_blocks = static_cast<int>((((T + kRowsPerWarp - 1ll) / kRowsPerWarp) * H + 7) / 8);
-  attention_packed_pre_kernel<<<1 + pre_blocks, 256, 0, s>>>(
-      maps, dmaps, ctl, P.meta, static_cast<const bf16*>(o.ptr), o.tok, o.head, static_cast<const bf16*>(dout.ptr),
+  e = launch_chained(
+      attention_packed_pre_kernel, 1ll + pre_blocks, 256, 0, s, maps, dmaps, ctl, P.meta, static_cast<const bf16*>(o.ptr), o.tok, o.head, static_cast<const bf16*>(dout.ptr),
       dout.tok, dout.head, lse, nl, nd, acc, H, T, err);
+  if (e != cudaSuccess) return e;
   PackedArgs pa = {};
   pa.hi = P.hi;
   pa.bwd = P.bwd;
@@ -2379,12 +2385,12 @@ cudaError_t launch_attn_packed_bwd(const PackedTensor& q, const PackedTensor& k,
   pa.dv_head = dv.head;
   const long long units = 1ll * ((T + 127) / 128) * Hkv;
   const int grid = static_cast<int>(std::min<long long>(units, device_sm_count()));
-  kern<<<grid, 512, TB_SMEM, s>>>(maps.m[0], maps.m[1], maps.m[2], maps.m[3], mdq, nl, nd,
-                                  static_cast<bf16*>(const_cast<void*>(dk.ptr)),
-                                  static_cast<bf16*>(const_cast<void*>(dv.ptr)), H, Hkv, Hkv, T, 1 << 30, scale, 0,
-                                  ctl + kCtlSched, err, wait_cycles, nullptr, nullptr, nullptr, pa);
-  attention_packed_dq_kernel<<<row_blocks, 256, 0, s>>>(acc, static_cast<bf16*>(const_cast<void*>(dq.ptr)), dq.tok, dq.head, ctl, H, T);
-  return cudaGetLastError();
+  e = launch_chained(kern, grid, 512, TB_SMEM, s, maps.m[0], maps.m[1], maps.m[2], maps.m[3], mdq, nl, nd,
+                     static_cast<bf16*>(const_cast<void*>(dk.ptr)), static_cast<bf16*>(const_cast<void*>(dv.ptr)), H,
+                     Hkv, Hkv, T, 1 << 30, scale, 0, ctl + kCtlSched, err, wait_cycles, nullptr, nullptr, nullptr, pa);
+  if (e != cudaSuccess) return e;
+  return launch_chained(attention_packed_dq_kernel, row_blocks, 256, 0, s, acc,
+                        static_cast<bf16*>(const_cast<void*>(dq.ptr)), dq.tok, dq.head, ctl, H, T);
 }
 
 }  // namespace gpt

@@ -532,6 +532,30 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// A kernel launched by launch_chained may start while the stream's kernel
+// before it finishes: it calls chain_wait in every thread before it touches
+// memory, which returns once that kernel and its writes are complete.  A
+// kernel that calls chain_go lets the one after it start as soon as all its
+// own blocks have, instead of when they have ended.
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void chain_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... Params, typename... Args>
+inline cudaError_t launch_chained(void (*kern)(Params...), long long grid, int block, int smem, cudaStream_t s,
+                                  Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(block, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
+}
+
 // Raises a kernel's dynamic shared memory limit once per device (the
 // attribute belongs to the device's context, and one process may drive
 // several GPUs or call from several threads).

@@ -313,7 +313,7 @@ __device__ __forceinline__ double target_logp(float x, const Softmax& a) {
 
 // Launches pick(G, S) over the rows.  G follows the row's bytes: 8 vectors of
 // a thread at 64 KB, fewer threads where a row would leave most of them idle.
-template <typename T, int S, typename Pick, typename... Args>
+template <typename T, int S, bool kChained, typename Pick, typename... Args>
 cudaError_t launch_rows(const LossRows& r, cudaStream_t s, Pick pick, Args... args) {
   const long long bytes = 1ll * r.V * sizeof(T);
   auto launch = [&](auto kG) -> cudaError_t {
@@ -325,6 +325,7 @@ cudaError_t launch_rows(const LossRows& r, cudaStream_t s, Pick pick, Args... ar
       const cudaError_t e = set_smem_limit_once(kern, S * kPieceBytes, configured);
       if (e != cudaSuccess) return e;
     }
+    if constexpr (kChained) return launch_chained(kern, std::max(r.M, 1), G, slots * kPieceBytes, s, args...);
     kern<<<std::max(r.M, 1), G, slots * kPieceBytes, s>>>(args...);
     return cudaGetLastError();
   };
@@ -368,6 +369,7 @@ template <typename T, int G, int S>
 __global__ void __launch_bounds__(G)
     policy_row_kernel(const LossRows R, const PolicyArgs a, float4* __restrict__ terms, int* err) {
   extern __shared__ uint4 ring[];
+  chain_go();
   __shared__ float2 red[G / 32];
   __shared__ float gs;
   const int r = blockIdx.x;
@@ -401,6 +403,7 @@ __global__ void __launch_bounds__(G)
 // stats = sums of the rows' terms, in 64 bits and a fixed order
 __global__ void __launch_bounds__(1024) policy_sum_kernel(const float4* __restrict__ terms, int M, float* stats) {
   __shared__ double red[4][32];
+  chain_wait();
   double s[4] = {0.0, 0.0, 0.0, 0.0};
   for (int i = threadIdx.x; i < M; i += 1024) {
     const float4 t = terms[i];
@@ -449,6 +452,7 @@ __global__ void __launch_bounds__(G)
     preference_logp_kernel(const LossRows R, const PreferenceArgs a, float2* __restrict__ ms, double* __restrict__ lps,
                            PairWords* words) {
   extern __shared__ uint4 ring[];
+  chain_go();
   __shared__ float2 red[G / 32];
   const int r = blockIdx.x;
   if (r == 0 && threadIdx.x == 0) words->done = 0;
@@ -486,6 +490,8 @@ __global__ void __launch_bounds__(kSumThreads)
                           float* __restrict__ g, PairWords* words, int* err) {
   __shared__ double red[kSumThreads / 32];
   __shared__ bool last;
+  chain_go();
+  chain_wait();
   const int n = 2 * a.n_pairs, tid = threadIdx.x;
   int bad = a.cu[0] != 0 || a.cu[n] > R.M;
   for (int i = tid; i < n; i += kSumThreads) bad |= a.cu[i + 1] < a.cu[i];
@@ -549,6 +555,7 @@ __global__ void __launch_bounds__(G)
     preference_grad_kernel(const LossRows R, const PreferenceArgs a, const float2* __restrict__ ms,
                            const float* __restrict__ g, const PairWords* __restrict__ words) {
   extern __shared__ uint4 ring[];
+  chain_wait();
   const int r = blockIdx.x;
   if (r >= words->rows) return;
   T* d = static_cast<T*>(R.dlogits) + r * R.ld_d;
@@ -579,8 +586,8 @@ size_t preference_loss_scratch(int M, int n_pairs) {
 template <typename T>
 static cudaError_t policy_rows(const LossRows& r, const PolicyArgs& a, float4* terms, int* err, cudaStream_t s) {
   auto pick = [](auto g, auto slots) { return policy_row_kernel<T, decltype(g)::value, decltype(slots)::value>; };
-  if (1ll * r.V * sizeof(T) <= 65536) return launch_rows<T, 4>(r, s, pick, r, a, terms, err);
-  return launch_rows<T, 6>(r, s, pick, r, a, terms, err);
+  if (1ll * r.V * sizeof(T) <= 65536) return launch_rows<T, 4, false>(r, s, pick, r, a, terms, err);
+  return launch_rows<T, 6, false>(r, s, pick, r, a, terms, err);
 }
 
 cudaError_t launch_policy_loss(const LossRows& r, const PolicyArgs& a, void* scratch, int* err, cudaStream_t s) {
@@ -589,8 +596,7 @@ cudaError_t launch_policy_loss(const LossRows& r, const PolicyArgs& a, void* scr
     const cudaError_t e = r.fp32 ? policy_rows<float>(r, a, terms, err, s) : policy_rows<bf16>(r, a, terms, err, s);
     if (e != cudaSuccess) return e;
   }
-  policy_sum_kernel<<<1, 1024, 0, s>>>(terms, r.M, a.stats);
-  return cudaGetLastError();
+  return launch_chained(policy_sum_kernel, 1, 1024, 0, s, terms, r.M, a.stats);
 }
 
 template <typename T>
@@ -607,14 +613,15 @@ static cudaError_t preference_rows(const LossRows& r, const PreferenceArgs& a, v
   double* lps = reinterpret_cast<double*>(take(static_cast<size_t>(r.M) * sizeof(double)));
   double* sums = reinterpret_cast<double*>(take(2 * static_cast<size_t>(a.n_pairs) * sizeof(double)));
   float* g = reinterpret_cast<float*>(take(2 * static_cast<size_t>(a.n_pairs) * sizeof(float)));
-  cudaError_t e = launch_rows<T, 2>(
+  cudaError_t e = launch_rows<T, 2, false>(
       r, s, [](auto g, auto slots) { return preference_logp_kernel<T, decltype(g)::value, decltype(slots)::value>; },
       r, a, ms, lps, words);
   if (e != cudaSuccess) return e;
   const int blocks = std::min(2 * a.n_pairs, 2 * device_sm_count());
-  preference_sum_kernel<<<blocks, kSumThreads, 0, s>>>(r, a, lps, sums, g, words, err);
+  e = launch_chained(preference_sum_kernel, blocks, kSumThreads, 0, s, r, a, lps, sums, g, words, err);
+  if (e != cudaSuccess) return e;
   if (r.dlogits && r.M > 0)
-    e = launch_rows<T, 4>(
+    e = launch_rows<T, 4, true>(
         r, s,
         [](auto g, auto slots) { return preference_grad_kernel<T, decltype(g)::value, decltype(slots)::value>; }, r, a,
         ms, g, words);
