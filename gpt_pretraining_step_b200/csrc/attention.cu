@@ -28,9 +28,9 @@ constexpr int HD = 128;
 
 // ------------------------------------------------------- packed sequences
 //
-// The packed forward and the packed build of the backward (kPacked): one row of T positions holds
-// sequences of different lengths end to end, and query t sees the keys
-// lo[t] .. t, lo[t] = max(start of t's sequence, t - window).  lo does not
+// For the packed forward and the packed build of the backward (kPacked), T
+// positions hold sequences of different lengths end to end, and query t sees
+// the keys lo[t] .. t, lo[t] = max(start of t's sequence, t - window).  lo does not
 // decrease with t, so a tile of 128 queries sees the key blocks from that of
 // lo[first query] to its own: tiles and key blocks stay on the 128-position
 // grid whatever the sequence boundaries (a tile may hold many short
@@ -654,7 +654,13 @@ __device__ __forceinline__ float max32(const uint32_t (&x)[32], float m) {
 // taken in turn; the two hide each other's softmax and products, start and
 // end of a tile.  (Pairs of tiles that share their key blocks in one block, as
 // above, leave a fifth of the softmax time idle here: neighbours seldom see
-// equally many blocks.)
+// equally many blocks.  16,384 tokens of chats of 24 to 1024, 10 heads over 2:
+// 79 us against 90; 32,768 of documents of 128 to 2048, 10 heads: 186 against
+// 205, 500 TFLOP/s of visible pairs, 670 of the blocks it runs.)  A tile takes
+// about 4.4 us and 2.35 us a key block, of which S = Q K^T alone fills half
+// the shared-memory bandwidth (both operands of a 128 x 128 product): bound by
+// the chain S, softmax, P V of the two tiles, with the tensor pipe 37% busy
+// and 31% of the issue slots used.  Two threads a row measured the same.
 // 192 threads:
 //   warps 0..3  softmax, one query row (TMEM lane) per thread, as above; then
 //               O / l and the log-sum-exp
@@ -893,13 +899,12 @@ __global__ void __launch_bounds__(192, 2)
         const int kbase = j * 128;
         const bool diag = j == qt;
         float mraw = -INFINITY;           // block max of the raw scores (the scale is positive)
-        // Packed rows meet masked blocks at every sequence boundary.  Straight-
-        // line code for a row and for each kind of mask, as below, left the
-        // softmax warps a fifth of their time without instructions, so here the
-        // row is read from TMEM 32 scores at a time, now and again for P, by
-        // loops that stay in the instruction cache, mask by bits and skip the
-        // chunks that no row of the warp sees (16,384 tokens of chats, 10 heads:
-        // 91 us instead of 103; whole rows of 2048: 229 instead of 217).
+        // Masked blocks come at every sequence boundary.  Straight-line code for a
+        // row and for each kind of mask, as in the kernel above, left the softmax
+        // warps a fifth of their time without instructions, so the row is read
+        // from TMEM 32 scores at a time, now and again for P, by loops that stay
+        // in the instruction cache, mask by bits and skip the chunks that no row
+        // of the warp sees (chats: 90 us instead of 103 when this came in).
         // Keys past the last sequence lie above every row of the diagonal block.
         const bool masked = diag || kbase < lo_max;
         // keys that this row sees, from kbase on: first .. end - 1
@@ -1089,6 +1094,15 @@ __global__ void __launch_bounds__(192, 2)
 //               other warps' work.  (Adding each row with 16-byte vector
 //               reductions from registers measured 0.925 ms against 0.68 ms
 //               at B 16, H 10, T 2048.)
+
+// The packed build takes single key blocks in the plan's order.  The rows' -lse
+// and -D come with Q and dO by bulk copies (from attention_packed_pre_kernel's
+// arrays of whole tiles), so that its softmax warps meet at no barrier; the
+// masks of a 32-query chunk are bits; dK and dV rows go out through the dS
+// tile.  32,768 tokens of documents, 10 heads: 350 us, 606 TFLOP/s of visible
+// pairs, 830 of the blocks it runs (466 us with staged lse and D, a form for
+// each kind of mask and a lane for each stored row); bound by the softmax
+// warps, about 1,800 cycles for P and as many for dS of the 4,400 a block takes.
 
 // Row r, query columns 64*half .. 64*half+63 of a [128][128] bf16 tile kept as
 // two 64-column halves of [128 rows][128 B] with the 128-byte swizzle (16-byte

@@ -3,15 +3,20 @@
     python -m gpt_pretraining_step_b200.opbench gemm --M 32768 --N 1280 --K 5120 --b-trans
     python -m gpt_pretraining_step_b200.opbench attention --B 4 --H 10 --T 2048
     python -m gpt_pretraining_step_b200.opbench newton-schulz --batch 20 --rows 1280 --cols 5120
+    python -m gpt_pretraining_step_b200.opbench packed-attention --tokens 32768 --shortest 128 --longest 2048
+    python -m gpt_pretraining_step_b200.opbench policy-loss --rows 8192 --vocab 32768
+    python -m gpt_pretraining_step_b200.opbench preference-loss --rows 8192 --vocab 32768
 
 Inputs are seeded standard normals on the device; every op runs through the
 library's C ABI.  Prints one line per op with the mean time per call and the
-achieved TFLOP/s of its algorithmic FLOPs.
+achieved TFLOP/s of its algorithmic FLOPs (of the losses, the GB/s of the
+logits that they read and write).
 """
 from __future__ import annotations
 
 import argparse
 import json
+import random
 
 
 def _time(fn, reps, warmup):
@@ -31,7 +36,8 @@ def _time(fn, reps, warmup):
 def main(argv=None):
     import torch
 
-    from . import attention_bwd, attention_fwd, matmul_bf16, newton_schulz
+    from . import (attention_bwd, attention_fwd, attention_packed_bwd, attention_packed_fwd, attention_plan,
+                   matmul_bf16, newton_schulz, policy_loss, preference_loss)
 
     ap = argparse.ArgumentParser()
     sub = ap.add_subparsers(dest="op", required=True)
@@ -52,7 +58,20 @@ def main(argv=None):
     n.add_argument("--rows", type=int, default=1280)
     n.add_argument("--cols", type=int, default=5120)
     n.add_argument("--tf32-steps", type=int, default=-1)
-    for p in (g, a, n):
+    pa = sub.add_parser("packed-attention", help="causal attention over packed sequences, plan, forward and backward")
+    pa.add_argument("--tokens", type=int, default=32768)
+    pa.add_argument("--shortest", type=int, default=128, help="lengths are spread over their logarithm")
+    pa.add_argument("--longest", type=int, default=2048)
+    pa.add_argument("--H", type=int, default=10)
+    pa.add_argument("--kv-heads", type=int, default=0, help="grouped kv heads (0 = H)")
+    pa.add_argument("--window", type=int, default=-1, help="sliding window, tokens of left context (-1 = full)")
+    po = sub.add_parser("policy-loss", help="clipped policy loss with a KL term and its gradient")
+    pr = sub.add_parser("preference-loss", help="preference loss over 16 pairs of equal answers and its gradient")
+    for p in (po, pr):
+        p.add_argument("--rows", type=int, default=8192)
+        p.add_argument("--vocab", type=int, default=32768)
+        p.add_argument("--dtype", choices=["bfloat16", "float32"], default="bfloat16")
+    for p in (g, a, n, pa, po, pr):
         p.add_argument("--reps", type=int, default=4)
         p.add_argument("--warmup", type=int, default=2)
     args = ap.parse_args(argv)
@@ -83,6 +102,41 @@ def main(argv=None):
         print(json.dumps({"op": "attention_fwd", **common, "ms": ms_f, "tflops": flops / (ms_f / 1e3) / 1e12}))
         print(json.dumps({"op": "attention_bwd", **common, "ms": ms_b,
                           "tflops": 2.5 * flops / (ms_b / 1e3) / 1e12}))
+    elif args.op == "packed-attention":
+        rng, lens = random.Random(0), []
+        while sum(lens) < args.tokens:
+            length = round(args.shortest * (args.longest / args.shortest) ** rng.random())
+            lens.append(min(args.tokens - sum(lens), length))
+        N, hkv, w = args.tokens, args.kv_heads or args.H, args.window
+        cu = torch.tensor([0] + lens, dtype=torch.int32, device=dev).cumsum(0, dtype=torch.int32)
+        q, do = (torch.randn((N, args.H, 128), device=dev).bfloat16() for _ in range(2))
+        k, v = (torch.randn((N, hkv, 128), device=dev).bfloat16() for _ in range(2))
+        plan = attention_plan(cu, N, w)
+        o, lse = attention_packed_fwd(q, k, v, plan)
+        pairs = sum(sum(min(t, w) + 1 if w >= 0 else t + 1 for t in range(x)) for x in lens)
+        flops = 4.0 * args.H * 128 * pairs
+        common = {"tokens": N, "sequences": len(lens), "H": args.H, "kv_heads": hkv, "window": w}
+        print(json.dumps({"op": "attention_plan", **common,
+                          "ms": _time(lambda: plan.update(cu), args.reps, args.warmup)}))
+        ms_f = _time(lambda: attention_packed_fwd(q, k, v, plan), args.reps, args.warmup)
+        ms_b = _time(lambda: attention_packed_bwd(q, k, v, o, lse, do, plan), args.reps, args.warmup)
+        print(json.dumps({"op": "attention_packed_fwd", **common, "ms": ms_f, "tflops": flops / (ms_f / 1e3) / 1e12}))
+        print(json.dumps({"op": "attention_packed_bwd", **common, "ms": ms_b,
+                          "tflops": 2.5 * flops / (ms_b / 1e3) / 1e12}))
+    elif args.op in ("policy-loss", "preference-loss"):
+        M, V, dtype = args.rows, args.vocab, getattr(torch, args.dtype)
+        x = torch.randn((M, V), device=dev, dtype=dtype)
+        y = torch.randint(0, V, (M,), device=dev).to(torch.int32)
+        if args.op == "policy-loss":
+            adv, weight = torch.randn(M, device=dev), torch.full((M,), 1.0 / M, device=dev)
+            ms = _time(lambda: policy_loss(x, y, None, adv, weight), args.reps, args.warmup)
+            moved = 2 * x.numel() * x.element_size()        # one read, one write
+        else:
+            cu = torch.linspace(0, M, 33, device=dev).to(torch.int32)
+            ms = _time(lambda: preference_loss(x, y, cu), args.reps, args.warmup)
+            moved = 3 * x.numel() * x.element_size()        # a read for the sums, one and a write for the gradient
+        print(json.dumps({"op": args.op, "rows": M, "vocab": V, "dtype": args.dtype, "ms": ms,
+                          "gbs": moved / (ms / 1e3) / 1e9}))
     else:
         G = torch.randn((args.batch, args.rows, args.cols), device=dev)
         ms = _time(lambda: newton_schulz(G, tf32_steps=args.tf32_steps), args.reps, args.warmup)
