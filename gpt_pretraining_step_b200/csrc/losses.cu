@@ -141,7 +141,7 @@ struct Softmax {
     const float b = base(m);
     const uint64_t nb = f2_pack(-b, -b), hi = f2_pack(kLog2e, kLog2e), lo = f2_pack(kLog2eLow, kLog2eLow),
                    mean = f2_pack(kEx2Mean, kEx2Mean);
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    uint64_t sum[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
     for (int k = 0; k < N; ++k) {
 #pragma unroll
@@ -149,11 +149,12 @@ struct Softmax {
         const uint64_t d = f2_add(f2_pack(v[k][e], v[k][e + 1]), nb);
         float x0, x1;
         f2_unpack(f2_fma(d, hi, f2_fma(d, lo, mean)), x0, x1);
-        sum[e & 2] += ex2(x0);
-        sum[(e & 2) + 1] += ex2(x1);
+        sum[(e >> 1) & 1] = f2_add(sum[(e >> 1) & 1], f2_pack(ex2(x0), ex2(x1)));
       }
     }
-    s += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    float s0, s1;
+    f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
+    s += s0 + s1;
   }
 };
 

@@ -107,7 +107,7 @@ def exact(torch, w, x, y, cu, extra, H, Hkv, window, loss):
         L = sums[cu[1:].long()] - sums[cu[:-1].long()]
         value = -torch.nn.functional.logsigmoid(BETA * (L[0::2] - L[1::2])).mean()
     value.backward()
-    return value, dict(head=p["head"].grad, out=p["out"].grad, qkv=p["qkv"].grad, x=xd.grad), lp.detach()
+    return value.detach(), dict(head=p["head"].grad, out=p["out"].grad, qkv=p["qkv"].grad, x=xd.grad), lp.detach()
 
 
 @pytest.mark.parametrize("loss", ["policy", "preference"])
