@@ -704,7 +704,8 @@ __global__ void __launch_bounds__(192, 2)
   uint64_t* answered = bars + 10;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 11);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  volatile int* item_ring = reinterpret_cast<volatile int*>(tmem_holder + 2);   // [4][4]: head (-1: end), tile, first key block
+  // [4][4]: head (-1: end), tile, first key block
+  volatile int* item_ring = reinterpret_cast<volatile int*>(tmem_holder + 2);
 
   const int warp = warp_id(), lane = lane_id();
   const long long wlim = wait_limit_or_default(wait_cycles);
@@ -1363,133 +1364,130 @@ __global__ void __launch_bounds__(512, 1)
       }
     }
   } else if (warp == 1) {
-    {
-      // -------------------------------------------------------------- MMA
-      // the whole warp, converged; one lane issues
-      const bool leader = elect_lane();
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      auto wait1 = [&](uint64_t* bar, uint32_t par) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait_t<kFine>(bar, par, abort_flag, err, wlim));
-      };
-      auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
-      constexpr uint32_t IDESC_KK = make_idesc(1, 128, false, false);   // S^T, dP^T
-      constexpr uint32_t IDESC_KM = make_idesc(1, 128, false, true);    // dV (A in TMEM), dK
-      constexpr uint32_t IDESC_MM = make_idesc(1, 128, true, true);     // dQ
-      const uint32_t k_addr = smem_u32(sK), v_addr = smem_u32(sV), do_addr = smem_u32(sdO);
-      const uint32_t dst_addr = smem_u32(sdSt);
-      // X^T = A B^T over the 128 head dims, both operands K-major; the empty
-      // asm keeps the descriptors from being hoisted into registers
-      auto qk_product = [&](uint32_t d_tmem, uint32_t a_addr, uint32_t b_addr) {
-        uint64_t da = smem_desc_sw128(a_addr, 16, 1024), db = smem_desc_sw128(b_addr, 16, 1024);
+    // -------------------------------------------------------------- MMA
+    // the whole warp, converged; one lane issues
+    const bool leader = elect_lane();
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    auto wait1 = [&](uint64_t* bar, uint32_t par) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait_t<kFine>(bar, par, abort_flag, err, wlim));
+    };
+    auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    constexpr uint32_t IDESC_KK = make_idesc(1, 128, false, false);   // S^T, dP^T
+    constexpr uint32_t IDESC_KM = make_idesc(1, 128, false, true);    // dV (A in TMEM), dK
+    constexpr uint32_t IDESC_MM = make_idesc(1, 128, true, true);     // dQ
+    const uint32_t k_addr = smem_u32(sK), v_addr = smem_u32(sV), do_addr = smem_u32(sdO);
+    const uint32_t dst_addr = smem_u32(sdSt);
+    // X^T = A B^T over the 128 head dims, both operands K-major
+    auto qk_product = [&](uint32_t d_tmem, uint32_t a_addr, uint32_t b_addr) {
+      uint64_t da = smem_desc_sw128(a_addr, 16, 1024), db = smem_desc_sw128(b_addr, 16, 1024);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off16 = ((kk >> 2) * TF_TILE + (kk & 3) * 32) >> 4;
-          umma_f16_by(leader, d_tmem, da + off16, db + off16, IDESC_KK, kk > 0 ? 1u : 0u);
-        }
-      };
-      bool ok = true;
-      int g0 = 0;   // query blocks done so far
-      for (int n = 0; ok; ++n) {
-        if (!wait1(kv_full, n & 1)) { ok = false; break; }
-        const int idx = uniform(item_ring[n & 3]);
-        if (idx < 0) break;
-        {
-          const BwdBlock kb = block_of(n, idx);
-          const int n_it = uniform(kb.n_it);
-          // S^T of the first query block goes where the previous key block's
-          // last dQ was (wait until the dQ warps have read it), dP^T where
-          // its last P was (wait until that dV is done)
-          ok = wait1(&q_full[g0 & 1], (g0 >> 1) & 1) &&
-               (g0 == 0 || wait1(dq_free, (g0 - 1) & 1));
+      for (int kk = 0; kk < 8; ++kk) {
+        const uint32_t off16 = ((kk >> 2) * TF_TILE + (kk & 3) * 32) >> 4;
+        umma_f16_by(leader, d_tmem, da + off16, db + off16, IDESC_KK, kk > 0 ? 1u : 0u);
+      }
+    };
+    bool ok = true;
+    int g0 = 0;   // query blocks done so far
+    for (int n = 0; ok; ++n) {
+      if (!wait1(kv_full, n & 1)) { ok = false; break; }
+      const int idx = uniform(item_ring[n & 3]);
+      if (idx < 0) break;
+      {
+        const BwdBlock kb = block_of(n, idx);
+        const int n_it = uniform(kb.n_it);
+        // S^T of the first query block goes where the previous key block's
+        // last dQ was (wait until the dQ warps have read it), dP^T where
+        // its last P was (wait until that dV is done)
+        ok = wait1(&q_full[g0 & 1], (g0 >> 1) & 1) &&
+             (g0 == 0 || wait1(dq_free, (g0 - 1) & 1));
+        if (!ok) break;
+        tc_fence_after();
+        qk_product(tm, k_addr, smem_u32(sQ + (g0 & 1) * TF_BUF));   // S^T of the first block
+        umma_commit_by(leader, s_full);
+        ok = wait1(do_full, g0 & 1) &&
+             (g0 == 0 || wait1(do_empty, (g0 - 1) & 1));
+        if (!ok) break;
+        tc_fence_after();
+        qk_product(tm + 128, v_addr, do_addr);   // dP^T of the first block
+        umma_commit_by(leader, dp_full);
+        if (n_it > 1) {
+          ok = wait1(s_free, g0 & 1) &&
+               wait1(&q_full[(g0 + 1) & 1], ((g0 + 1) >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
-          qk_product(tm, k_addr, smem_u32(sQ + (g0 & 1) * TF_BUF));   // S^T of the first block
+          qk_product(tm, k_addr, smem_u32(sQ + ((g0 + 1) & 1) * TF_BUF));   // S^T of the second block
           umma_commit_by(leader, s_full);
-          ok = wait1(do_full, g0 & 1) &&
-               (g0 == 0 || wait1(do_empty, (g0 - 1) & 1));
-          if (!ok) break;
+        }
+        for (int it = 0; it < n_it && ok; ++it) {
+          const int gi = g0 + it;
+          const int s = gi & 1;
+          if (!wait1(p_ready, gi & 1)) { ok = false; break; }
           tc_fence_after();
-          qk_product(tm + 128, v_addr, do_addr);   // dP^T of the first block
-          umma_commit_by(leader, dp_full);
-          if (n_it > 1) {
-            ok = wait1(s_free, g0 & 1) &&
-                 wait1(&q_full[(g0 + 1) & 1], ((g0 + 1) >> 1) & 1);
-            if (!ok) break;
+          const uint32_t q_addr = smem_u32(sQ + s * TF_BUF);
+          // dV += P^T dO: A = P^T from TMEM, 16 queries = 8 packed columns per
+          // step; queries 0..63 at columns 128.., 64..127 at columns 192..
+          {
+            uint64_t ddo = smem_desc_sw128(do_addr, TF_TILE, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              umma_f16_tmem_a_by(leader, tm + 256, tm + 128 + (kk >> 2) * 64 + (kk & 3) * 8, ddo + ((kk * 2048) >> 4),
+                              IDESC_KM, (it > 0 || kk > 0) ? 1u : 0u);
+          }
+          umma_commit_by(leader, do_empty);
+          // dK and dQ once dS_i is in shared memory (the softmax warps compute it
+          // while dV runs)
+          if (!wait1(ds_ready, gi & 1)) { ok = false; break; }
+          tc_fence_after();
+          {
+            uint64_t dsa = smem_desc_sw128(dst_addr, 16, 1024), dqb = smem_desc_sw128(q_addr, TF_TILE, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t aoff16 = ((kk >> 2) * TF_TILE + (kk & 3) * 32) >> 4;   // K-major A: 16 queries per step
+              const uint32_t boff16 = (kk * 2048) >> 4;                            // MN-major B: 16 query rows per step
+              umma_f16_by(leader, tm + 384, dsa + aoff16, dqb + boff16, IDESC_KM, (it > 0 || kk > 0) ? 1u : 0u);
+            }
+          }
+          umma_commit_by(leader, &q_empty[s]);
+          // dQ_i goes to [0,128), which holds S^T_{i+1} (wait until the softmax
+          // warps have read it) or, for the last block, dQ_{i-1} (wait until
+          // the dQ warps have read it)
+          if (it + 1 < n_it) {
+            if (!wait1(s_free, (gi + 1) & 1)) { ok = false; break; }
+          } else if (it > 0) {
+            if (!wait1(dq_free, (gi - 1) & 1)) { ok = false; break; }
+          }
+          tc_fence_after();
+          {
+            uint64_t dka = smem_desc_sw128(k_addr, TF_TILE, 1024), dsb = smem_desc_sw128(dst_addr, TF_TILE, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t off16 = (kk * 2048) >> 4;   // 16 keys per step, both operands MN-major
+              umma_f16_by(leader, tm, dsb + off16, dka + off16, IDESC_MM, kk > 0 ? 1u : 0u);   // dQ = dS K
+            }
+          }
+          umma_commit_by(leader, mm_done);
+          if (it + 1 == n_it) umma_commit_by(leader, kv_empty);   // K and V of this key block are free
+          if (it + 1 < n_it) {
+            // dP^T_{i+1} overwrites P^T_i: dV_i must have completed
+            if (!wait1(do_empty, gi & 1) ||
+                !wait1(do_full, (gi + 1) & 1)) { ok = false; break; }
             tc_fence_after();
-            qk_product(tm, k_addr, smem_u32(sQ + ((g0 + 1) & 1) * TF_BUF));   // S^T of the second block
+            qk_product(tm + 128, v_addr, do_addr);
+            umma_commit_by(leader, dp_full);
+          }
+          if (it + 2 < n_it) {
+            if (!wait1(dq_free, gi & 1) ||
+                !wait1(&q_full[s], ((gi + 2) >> 1) & 1)) { ok = false; break; }
+            tc_fence_after();
+            qk_product(tm, k_addr, q_addr);   // S^T_{i+2} (same Q slot as block i)
             umma_commit_by(leader, s_full);
           }
-          for (int it = 0; it < n_it && ok; ++it) {
-            const int gi = g0 + it;
-            const int s = gi & 1;
-            if (!wait1(p_ready, gi & 1)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t q_addr = smem_u32(sQ + s * TF_BUF);
-            // dV += P^T dO: A = P^T from TMEM, 16 queries = 8 packed columns per
-            // step; queries 0..63 at columns 128.., 64..127 at columns 192..
-            {
-              uint64_t ddo = smem_desc_sw128(do_addr, TF_TILE, 1024);
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                umma_f16_tmem_a_by(leader, tm + 256, tm + 128 + (kk >> 2) * 64 + (kk & 3) * 8, ddo + ((kk * 2048) >> 4),
-                                IDESC_KM, (it > 0 || kk > 0) ? 1u : 0u);
-            }
-            umma_commit_by(leader, do_empty);
-            // dK and dQ once dS_i is in shared memory (the softmax warps compute it
-            // while dV runs)
-            if (!wait1(ds_ready, gi & 1)) { ok = false; break; }
-            tc_fence_after();
-            {
-              uint64_t dsa = smem_desc_sw128(dst_addr, 16, 1024), dqb = smem_desc_sw128(q_addr, TF_TILE, 1024);
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk) {
-                const uint32_t aoff16 = ((kk >> 2) * TF_TILE + (kk & 3) * 32) >> 4;   // K-major A: 16 queries per step
-                const uint32_t boff16 = (kk * 2048) >> 4;                            // MN-major B: 16 query rows per step
-                umma_f16_by(leader, tm + 384, dsa + aoff16, dqb + boff16, IDESC_KM, (it > 0 || kk > 0) ? 1u : 0u);
-              }
-            }
-            umma_commit_by(leader, &q_empty[s]);
-            // dQ_i goes to [0,128), which holds S^T_{i+1} (wait until the softmax
-            // warps have read it) or, for the last block, dQ_{i-1} (wait until
-            // the dQ warps have read it)
-            if (it + 1 < n_it) {
-              if (!wait1(s_free, (gi + 1) & 1)) { ok = false; break; }
-            } else if (it > 0) {
-              if (!wait1(dq_free, (gi - 1) & 1)) { ok = false; break; }
-            }
-            tc_fence_after();
-            {
-              uint64_t dka = smem_desc_sw128(k_addr, TF_TILE, 1024), dsb = smem_desc_sw128(dst_addr, TF_TILE, 1024);
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk) {
-                const uint32_t off16 = (kk * 2048) >> 4;   // 16 keys per step, both operands MN-major
-                umma_f16_by(leader, tm, dsb + off16, dka + off16, IDESC_MM, kk > 0 ? 1u : 0u);   // dQ = dS K
-              }
-            }
-            umma_commit_by(leader, mm_done);
-            if (it + 1 == n_it) umma_commit_by(leader, kv_empty);   // K and V of this key block are free
-            if (it + 1 < n_it) {
-              // dP^T_{i+1} overwrites P^T_i: dV_i must have completed
-              if (!wait1(do_empty, gi & 1) ||
-                  !wait1(do_full, (gi + 1) & 1)) { ok = false; break; }
-              tc_fence_after();
-              qk_product(tm + 128, v_addr, do_addr);
-              umma_commit_by(leader, dp_full);
-            }
-            if (it + 2 < n_it) {
-              if (!wait1(dq_free, gi & 1) ||
-                  !wait1(&q_full[s], ((gi + 2) >> 1) & 1)) { ok = false; break; }
-              tc_fence_after();
-              qk_product(tm, k_addr, q_addr);   // S^T_{i+2} (same Q slot as block i)
-              umma_commit_by(leader, s_full);
-            }
-          }
-          g0 += n_it;
         }
+        g0 += n_it;
       }
-      umma_commit_by(leader, drain);
-      for (uint32_t x = 0; x < (1u << 22) && !mbar_try_wait(drain, 0); ++x) {}
     }
+    umma_commit_by(leader, drain);
+    for (uint32_t x = 0; x < (1u << 22) && !mbar_try_wait(drain, 0); ++x) {}
   } else if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n" ::: "memory");
     // ------------------------------------------------------------------ dQ
@@ -1650,8 +1648,8 @@ __global__ void __launch_bounds__(512, 1)
           mbar_arrive(s_free);   // S^T of this block has been read
           // One 32-query chunk of the row in one of four forms, chosen per
           // chunk by a warp-uniform test: no mask, the causal diagonal's lane
-          // mask (queries below the key row), all masked (P = 0), or the general
-          // mask (ragged keys, window edge).  A per-element mask inside one loop
+          // mask (queries below the key row; packed: a mask of bits), all masked
+          // (P = 0), or the general mask (ragged keys, window edge; not packed).  A per-element mask inside one loop
           // was if-converted into every block's path and cost more than the
           // exponentials.
           auto run_chunk = [&](auto kCC, auto kMode, uint32_t seen = 0u) {
@@ -2170,7 +2168,8 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int i = 0; i < kRowsPerWarp; ++i) {
     if (i >= n) break;
-    reinterpret_cast<float4*>(dq + (static_cast<long long>(h) * T + t0 + i) * HD)[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const long long row = static_cast<long long>(h) * T + t0 + i;
+    reinterpret_cast<float4*>(dq + row * HD)[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
     const float s = warp_sum(bf16_lo(x[i].x) * bf16_lo(y[i].x) + bf16_hi(x[i].x) * bf16_hi(y[i].x) +
                              bf16_lo(x[i].y) * bf16_lo(y[i].y) + bf16_hi(x[i].y) * bf16_hi(y[i].y));
     if (lane == i) d = s;
@@ -2385,8 +2384,9 @@ cudaError_t launch_attn_packed_bwd(const PackedTensor& q, const PackedTensor& k,
   const int row_blocks = static_cast<int>((rows + 8 * kRowsPerWarp - 1) / (8 * kRowsPerWarp));
   const int pre_blocks = static_cast<int>((((T + kRowsPerWarp - 1ll) / kRowsPerWarp) * H + 7) / 8);
   e = launch_chained(
-      attention_packed_pre_kernel, 1ll + pre_blocks, 256, 0, s, maps, dmaps, ctl, P.meta, static_cast<const bf16*>(o.ptr), o.tok, o.head, static_cast<const bf16*>(dout.ptr),
-      dout.tok, dout.head, lse, nl, nd, acc, H, T, err);
+      attention_packed_pre_kernel, 1ll + pre_blocks, 256, 0, s, maps, dmaps, ctl, P.meta,
+      static_cast<const bf16*>(o.ptr), o.tok, o.head, static_cast<const bf16*>(dout.ptr), dout.tok, dout.head, lse, nl,
+      nd, acc, H, T, err);
   if (e != cudaSuccess) return e;
   PackedArgs pa = {};
   pa.hi = P.hi;

@@ -471,8 +471,9 @@ int gpt_op_attention_plan(const int32_t* cu_seqlens, int n_seq, int n_tokens, in
  * (kv head h / (H / Hkv)) o_t = sum_j softmax_j(scale q_t . k_j) v_j over the
  * keys that t sees, and lse fp32 [H, n_tokens], the natural log of the
  * softmax denominator.  Rows past the last sequence are neither read nor
- * written.  Within a 128-position tile a NaN or infinity in an input of one
- * sequence may reach the others of the tile, here and in the backward.
+ * written.  o must not overlap k or v.  Within a 128-position tile a NaN or
+ * infinity in an input of one sequence may reach the others of the tile, here
+ * and in the backward.
  *   scale    > 0, or 0 for 1 / sqrt(128)
  *   plan     made for the same n_tokens (another plan: nothing is written and
  *            gpt_op_check reports it) */
