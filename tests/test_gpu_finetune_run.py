@@ -259,3 +259,16 @@ def test_expired_waits_are_reported_and_calls_recover(torch):
     got = [o2, lse2, *g.attention_packed_bwd(q, k, v, o2, lse2, do, plan)[1:]]
     g.op_check()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_nothing_to_do(torch):
+    """No tokens, no rows: empty results and no error."""
+    import gpt_pretraining_step_b200 as g
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = torch.empty((0, 4, 128), dtype=torch.bfloat16, device="cuda")
+    k = torch.empty((0, 2, 128), dtype=torch.bfloat16, device="cuda")
+    plan = g.attention_plan(cu, 0)
+    o, lse = g.attention_packed_fwd(q, k, k, plan)
+    dq, dk, dv = g.attention_packed_bwd(q, k, k, o, lse, o, plan)
+    g.op_check()
+    assert o.shape == q.shape and lse.shape == (4, 0) and dq.shape == q.shape and dk.shape == dv.shape == k.shape

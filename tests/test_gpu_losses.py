@@ -299,3 +299,23 @@ def test_refusals(torch):
             call()
         assert e.value.code == gpt.GPT_EINVAL, i
     gpt.op_check()
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_errors_of_log_probabilities_do_not_add_up(torch, dtype):
+    """Their mean over many rows, which a sequence's sum multiplies by its
+    length: the exponentials' mean error is made up for to 2.8e-8 at worst
+    (where the argument is above -1), and 8192 errors of 2.5e-7 root mean square
+    average to within 3 * 2.8e-9."""
+    import gpt_pretraining_step_b200 as gpt
+    off = []
+    for seed in range(4):
+        logits, y, _ = make_rows(torch, 2048, 20000, getattr(torch, dtype), 20000, 0.0, seed)
+        cu = torch.tensor([0, 2048, 2048], dtype=torch.int32, device="cuda")
+        _, _, seq, logp, _ = gpt.preference_loss(logits, y, cu, grad=False)
+        _, lp, _, _ = exact_rows(torch, logits, y)
+        off.append(logp.double() - lp)
+        # the sum is rounded once more
+        most = 2048 * (2.8e-8 + 3 * 2.5e-7 / 2048 ** 0.5) + 2.0 ** -24 * lp.sum().abs()
+        assert abs(seq[0].double() - lp.sum()) <= most
+    assert abs(torch.cat(off).mean()) <= 2.8e-8 + 3 * 2.8e-9
