@@ -518,6 +518,9 @@ def _raw_stream(torch, stream, dev, *made):
     return stream.cuda_stream
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
 @functools.lru_cache(maxsize=256)
 def _words(query, *sizes):
     """Size of a plan or scratch buffer in 4-byte words (a pure function of its arguments)."""
@@ -529,7 +532,10 @@ class AttentionPlan:
 
     def __init__(self, cu_seqlens, n_tokens, window=-1, stream=None):
         import torch
-        self.n_tokens, self.window = int(n_tokens), int(window)
+        # the C ABI takes 32-bit integers, and binding a larger one drops its upper bits
+        self.n_tokens, self.window = int(n_tokens), max(-1, min(int(window), _INT_MAX))
+        if not 0 <= self.n_tokens <= _INT_MAX:
+            raise GptError(GPT_EINVAL, f"n_tokens must be in [0, 2^30]; got {n_tokens}")
         self.device = _current(torch, "cu_seqlens", cu_seqlens)
         self.buf = cu_seqlens.new_empty(_words("gpt_op_attention_plan_bytes", self.n_tokens), dtype=torch.int32)
         self.update(cu_seqlens, stream)
@@ -537,12 +543,21 @@ class AttentionPlan:
     def update(self, cu_seqlens, stream=None):
         """Plan another batch of the same n_tokens and window into the same buffer."""
         import torch
+        _current(torch, "cu_seqlens", cu_seqlens)
         n = cu_seqlens.numel()
-        if n < 1:
-            _refuse("cu_seqlens", cu_seqlens, "[sequences + 1]")
+        if not 1 <= n <= _INT_MAX:
+            _refuse("cu_seqlens", cu_seqlens, "[sequences + 1], up to 2^30 sequences")
         cu = _flat("cu_seqlens", cu_seqlens, torch.int32, (n,), self.device)
         _check(lib().gpt_op_attention_plan(cu, n - 1, self.n_tokens, self.window, self.buf.data_ptr(),
                                            _raw_stream(torch, stream, self.device, self.buf)))
+
+
+def _planned(torch, q, plan):
+    """Index of the device of q and its plan."""
+    dev = _current(torch, "q", q)
+    if plan.device != dev:
+        raise GptError(GPT_EINVAL, f"the plan is on cuda:{plan.device}, q on cuda:{dev}")
+    return dev
 
 
 def attention_plan(cu_seqlens, n_tokens, window=-1, stream=None):
@@ -558,7 +573,7 @@ def attention_packed_fwd(q, k, v, plan, scale=0.0, o=None, lse=None, stream=None
     [H, n_tokens], new unless given; rows past the last sequence keep what
     they held (new tensors: anything)."""
     import torch
-    n, dev, bf16, f32 = plan.n_tokens, _current(torch, "q", q), torch.bfloat16, torch.float32
+    n, dev, bf16, f32 = plan.n_tokens, _planned(torch, q, plan), torch.bfloat16, torch.float32
     H, Hkv = q.shape[1], k.shape[1]
     rows, kv_rows = (n, H, 128), (n, Hkv, 128)
     hq, hk, hv = (_heads("q", q, rows, dev, bf16), _heads("k", k, kv_rows, dev, bf16),
@@ -577,7 +592,7 @@ def attention_packed_bwd(q, k, v, o, lse, dout, plan, scale=0.0, dq=None, dk=Non
     """Gradients (bf16, shaped as q, k and v; new unless given) of
     attention_packed_fwd, from its o and lse and the gradient dout of o."""
     import torch
-    n, dev, bf16, f32 = plan.n_tokens, _current(torch, "q", q), torch.bfloat16, torch.float32
+    n, dev, bf16, f32 = plan.n_tokens, _planned(torch, q, plan), torch.bfloat16, torch.float32
     H, Hkv = q.shape[1], k.shape[1]
     rows, kv_rows = (n, H, 128), (n, Hkv, 128)
     hq, hk, hv = (_heads("q", q, rows, dev, bf16), _heads("k", k, kv_rows, dev, bf16),
@@ -613,6 +628,8 @@ def _loss_rows(torch, logits, grad, dlogits):
     dev = _current(torch, "logits", logits)
     ld = _rows("logits", logits, dev)
     M, V = logits.shape
+    if M > _INT_MAX or V > _INT_MAX:
+        _refuse("logits", logits, "[M, V] with M below 2^31 and V up to 2^24")
     dtype = logits.dtype
     code = DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_FP32
     if code == DTYPE_FP32 and dtype != torch.float32:
@@ -621,8 +638,9 @@ def _loss_rows(torch, logits, grad, dlogits):
         return M, V, code, ld, None, None, ld, dev
     ld_d = ld
     if dlogits is None:
-        # the rows' alignment follows the logits'
-        dlogits = logits.new_empty((M, V)) if ld == V else logits.new_empty_strided((M, V), (ld, 1))
+        # rows aligned to 16 bytes as the logits' are, without their gaps
+        ld_d = V + (ld - V) % (8 if code == DTYPE_BF16 else 4) if M > 1 else V
+        dlogits = logits.new_empty((M, V)) if ld_d == V else logits.new_empty_strided((M, V), (ld_d, 1))
     else:
         ld_d = _rows("dlogits", dlogits, dev)
         if dlogits.shape != logits.shape or dlogits.dtype != dtype:
@@ -666,7 +684,7 @@ def preference_loss(logits, targets, cu_seqlens, ref_logp=None, beta=0.1, label_
     import torch
     M, V, code, ld, dlogits, d, ld_d, dev = _loss_rows(torch, logits, grad, dlogits)
     n, f32, i32 = cu_seqlens.numel() - 1, torch.float32, torch.int32
-    if n < 2 or n % 2:
+    if n < 2 or n % 2 or n > _INT_MAX:
         _refuse("cu_seqlens", cu_seqlens, "[2 * pairs + 1]")
     y, cu = _flat("targets", targets, i32, (M,), dev), _flat("cu_seqlens", cu_seqlens, i32, (n + 1,), dev)
     ref = None if ref_logp is None else _flat("ref_logp", ref_logp, f32, (n,), dev)

@@ -1790,7 +1790,7 @@ size_t gpt_op_attention_plan_bytes(int n_tokens) { return n_tokens < 0 ? 0 : att
 
 int gpt_op_attention_plan(const int32_t* cu_seqlens, int n_seq, int n_tokens, int window, void* plan, void* stream) {
   if (!cu_seqlens || !plan) return fail(GPT_EINVAL, "null pointer");
-  if (n_seq < 0 || n_tokens < 0 || n_tokens > (1 << 30)) return fail(GPT_EINVAL, "bad plan shape");
+  if (n_seq < 0 || n_seq > (1 << 30) || n_tokens < 0 || n_tokens > (1 << 30)) return fail(GPT_EINVAL, "bad plan shape");
   if (!aligned_scratch(plan)) return fail(GPT_EINVAL, "plan must be 256-byte aligned");
   int* err = nullptr;
   int rc = op_err(&err);

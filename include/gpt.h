@@ -458,7 +458,7 @@ typedef struct gpt_heads {
  * layer, head count and direction of the batch, on any number of streams at
  * once after this call has run; a new batch of the same n_tokens may be
  * planned into the same buffer, also by replaying a captured graph.
- *   cu_seqlens  device int32 [n_seq + 1]; it has to start at 0, not decrease
+ *   cu_seqlens  device int32 [n_seq + 1], n_seq up to 2^30; it has to start at 0, not decrease
  *               and end within n_tokens: otherwise the plan holds no
  *               sequence, so the calls that use it write nothing, and
  *               gpt_op_check reports GPT_ERANGE

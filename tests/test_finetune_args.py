@@ -112,3 +112,13 @@ def test_binding_refuses_host_tensors(g):
             call()
         assert e.value.code == g.GPT_EINVAL
     assert ctypes.sizeof(g.Heads) == 24 and q.stride() == (256, 128, 1)
+
+
+def test_binding_refuses_what_32_bits_do_not_hold(g):
+    """ctypes drops the upper bits of an int argument, so the binding looks first."""
+    import torch
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    for n in (2 ** 32 + 4, 2 ** 31, -1):
+        with pytest.raises(g.GptError, match="n_tokens"):
+            g.attention_plan(cu, n)
+    assert g.lib().gpt_op_attention_plan(A, (1 << 30) + 1, 64, -1, A, None) == g.GPT_EINVAL

@@ -296,3 +296,27 @@ def test_refusals(torch):
             call()
         assert e.value.code == g.GPT_EINVAL, i
     g.op_check()
+
+
+def test_plan_of_another_device(torch):
+    """Memory of one device is not read by another's kernels."""
+    import gpt_pretraining_step_b200 as g
+    q, k, v, do, cu, n = make(torch, [64], 0, 4, 2, "heads", 3)
+    plan = g.attention_plan(cu, n)
+    o, lse = g.attention_packed_fwd(q, k, v, plan)
+    plan.device = 1   # as if it had been made there
+    for call in (lambda: g.attention_packed_fwd(q, k, v, plan), lambda: plan.update(cu),
+                 lambda: g.attention_packed_bwd(q, k, v, o, lse, do, plan)):
+        with pytest.raises(g.GptError, match="cuda:1"):
+            call()
+    g.op_check()
+
+
+def test_windows_past_32_bits_are_no_window(torch):
+    import gpt_pretraining_step_b200 as g
+    q, k, v, do, cu, n = make(torch, [200, 57], 0, 2, 2, "heads", 4)
+    want = g.attention_packed_fwd(q, k, v, g.attention_plan(cu, n))
+    for window in (2 ** 40, 2 ** 32, 2 ** 31 - 1, -2 ** 40):
+        got = g.attention_packed_fwd(q, k, v, g.attention_plan(cu, n, window))
+        assert all(torch.equal(a, b) for a, b in zip(want, got)), window
+    g.op_check()
