@@ -357,6 +357,9 @@ cudaError_t launch_rows(const LossRows& r, cudaStream_t s, Pick pick, Args... ar
 // one (at a border both are) and 0 elsewhere, plus c (1 - exp(d)), the row
 // factor is g = w dlp.  The scalars of a row are computed in 64 bits: k loses
 // half its digits for small d in 32, and it is one thread's work.
+// A term of weight 0 is left out, infinite (the target masked to -inf) or not.
+__device__ __forceinline__ double times(double weight, double x) { return weight == 0.0 ? 0.0 : weight * x; }
+
 struct PolicyRow {
   float g;
   float4 term;   // w times: loss, surrogate, k, clipped
@@ -370,12 +373,13 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& a, int r, doub
   double dlp = cut ? 0.0 : -adv * ratio, k = 0.0;
   if (a.ref_logp) {
     const double d = a.ref_logp[r] - lp, e = expm1(d);
-    k = e - d;
-    dlp -= a.kl_coef * e;
+    k = isinf(e) ? e : e - d;
+    dlp -= times(a.kl_coef, e);
   }
   PolicyRow p;
+  const double surrogate = -adv * used;
   p.g = static_cast<float>(w * dlp);
-  p.term = make_float4(static_cast<float>(w * (a.kl_coef * k - adv * used)), static_cast<float>(w * (-adv * used)),
+  p.term = make_float4(static_cast<float>(w * (times(a.kl_coef, k) + surrogate)), static_cast<float>(w * surrogate),
                        static_cast<float>(w * k), cut ? w32 : 0.f);
   return p;
 }
@@ -544,7 +548,7 @@ __global__ void __launch_bounds__(kSumThreads)
     // sigmoid(-|z|), and log sigmoid(+-z) = min(+-z, 0) - log(1 + exp(-|z|))
     const double t = exp(-fabs(z)), soft = log1p(t), less = t / (1.0 + t);
     const double sig_pos = z >= 0.0 ? 1.0 - less : less, sig_neg = z >= 0.0 ? less : 1.0 - less;
-    loss += (1.0 - a.smoothing) * (soft + fmax(-z, 0.0)) + a.smoothing * (soft + fmax(z, 0.0));
+    loss += soft + times(1.0 - a.smoothing, fmax(-z, 0.0)) + times(a.smoothing, fmax(z, 0.0));
     const double dz = a.beta / a.n_pairs * (a.smoothing * sig_pos - (1.0 - a.smoothing) * sig_neg);
     a.margin[i] = static_cast<float>(z);
     g[2 * i] = static_cast<float>(dz);

@@ -319,3 +319,45 @@ def test_errors_of_log_probabilities_do_not_add_up(torch, dtype):
         most = 2048 * (2.8e-8 + 3 * 2.5e-7 / 2048 ** 0.5) + 2.0 ** -24 * lp.sum().abs()
         assert abs(seq[0].double() - lp.sum()) <= most
     assert abs(torch.cat(off).mean()) <= 2.8e-8 + 3 * 2.8e-9
+
+
+def test_infinite_terms_of_weight_zero(torch):
+    """A counted target masked to -inf: lp = -inf, so the KL estimate is infinite
+    and an answer's sum, too; where their weights are 0 they are no part of the
+    loss, and the gradients stay finite."""
+    import gpt_pretraining_step_b200 as gpt
+    M, V = 4, 300
+    logits, y, _ = make_rows(torch, M, V, torch.float32, V, 0.0, 3)
+    logits[3, y[3].long()] = -math.inf
+    one, old = torch.ones(M, device="cuda"), torch.zeros(M, device="cuda")
+    ref = torch.full((M,), -2.0, device="cuda")
+    stats, logp, d = gpt.policy_loss(logits, y, old, one, one, ref_logp=ref, kl_coef=0.0)
+    want, _, want_d = gpt.policy_loss(logits, y, old, one, one)
+    assert logp[3] == -math.inf and stats[2] == math.inf
+    assert torch.equal(stats[:2], want[:2]) and stats[0].isfinite()
+    assert torch.equal(d, want_d) and (d[3] == 0).all() and d.isfinite().all()
+    # the rejected answer is impossible: the margin is infinite and nothing is left to learn
+    cu = torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda")
+    loss, margin, seq, _, d = gpt.preference_loss(logits, y, cu)
+    assert loss == 0 and margin[0] == math.inf and seq[1] == -math.inf and (d == 0).all()
+    # the chosen one is
+    cu = torch.tensor([0, 2, 2], dtype=torch.int32, device="cuda")
+    loss, margin, _, _, d = gpt.preference_loss(logits[2:], y[2:], cu, beta=0.5)
+    assert loss == math.inf and margin[0] == -math.inf and d.isfinite().all()
+    gpt.op_check()
+
+
+def test_new_gradient_leaves_out_the_gaps(torch):
+    """Of logits that are every tenth row of a buffer: rows as aligned, memory
+    of the rows alone."""
+    import gpt_pretraining_step_b200 as gpt
+    for dt, n in ((torch.bfloat16, 8), (torch.float32, 4)):
+        for V, ld in ((1000, 10000), (1001, 10008), (1001, 10010)):
+            logits, y, _ = make_rows(torch, 6, V, dt, ld, 0.0, 3)
+            one = torch.ones(6, device="cuda")
+            _, _, d = gpt.policy_loss(logits, y, None, one, one)
+            _, _, flat = gpt.policy_loss(logits.contiguous(), y, None, one, one)
+            assert V <= d.stride(0) < V + n and (d.stride(0) - ld) % n == 0
+            assert d.untyped_storage().nbytes() <= 6 * d.stride(0) * d.element_size()
+            assert torch.allclose(d, flat, rtol=2.0 ** -7, atol=1e-6)
+    gpt.op_check()
