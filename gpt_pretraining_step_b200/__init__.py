@@ -590,7 +590,8 @@ def attention_packed_fwd(q, k, v, plan, scale=0.0, o=None, lse=None, stream=None
 
 def attention_packed_bwd(q, k, v, o, lse, dout, plan, scale=0.0, dq=None, dk=None, dv=None, stream=None):
     """Gradients (bf16, shaped as q, k and v; new unless given) of
-    attention_packed_fwd, from its o and lse and the gradient dout of o."""
+    attention_packed_fwd, from its lse and the gradient dout of o (o itself is
+    checked but not read: gpt_op_attention_packed_bwd)."""
     import torch
     n, dev, bf16, f32 = plan.n_tokens, _planned(torch, q, plan), torch.bfloat16, torch.float32
     H, Hkv = q.shape[1], k.shape[1]

@@ -1838,7 +1838,7 @@ int gpt_op_attention_packed_bwd(const gpt_heads* q, const gpt_heads* k, const gp
     return rc;
   int* err = nullptr;
   if ((rc = op_err(&err))) return rc;
-  GPT_CK(launch_attn_packed_bwd(tq, tk, tv, to, tdo, lse, tdq, tdk, tdv, H, Hkv, n_tokens,
+  GPT_CK(launch_attn_packed_bwd(tq, tk, tv, tdo, lse, tdq, tdk, tdv, H, Hkv, n_tokens,
                                 scale > 0.f ? scale : 1.f / sqrtf(128.f), plan, scratch,
                                 static_cast<cudaStream_t>(stream), err, g_op_wait_cycles.load()));
   return GPT_OK;

@@ -49,10 +49,8 @@ constexpr int HD = 128;
 // sequences' end, so that TMA fills the rows of all four operands with zeros.
 // Scores, maxima, row sums, lse, D and every sum over keys or queries are fp32.
 // P and dS are rounded to bf16, as the tensor cores take both operands of a
-// product in one type and q, k, v and dO are bf16: against 64 bits o, dq, dk
-// and dv are off by 0.002 to 0.003 of their norm, 0.0017 of it from their own
-// rounding to bf16.  (A product with dS in two bf16 parts would cost a second
-// one of dQ and dK each, 40% more of the backward's.)
+// product in one type and q, k, v and dO are bf16, and dS is formed from the
+// rounded P.
 struct PackedArgs {
   const int* meta;          // forward: the plan's kMeta* words
   const int* lo;            // [T]
@@ -1103,7 +1101,7 @@ __global__ void __launch_bounds__(192, 2)
 //               at B 16, H 10, T 2048.)
 
 // The packed build takes single key blocks in the plan's order.  The rows' -lse
-// and -D come with Q and dO by bulk copies (from attention_packed_pre_kernel's
+// and -D come with Q and dO by bulk copies (from attention_packed_dot_kernel's
 // arrays of whole tiles), so that its softmax warps meet at no barrier; the
 // masks of a 32-query chunk are bits; dK and dV rows go out through the dS
 // tile.  32,768 tokens of documents, 10 heads: 350 us, 606 TFLOP/s of visible
@@ -2132,62 +2130,321 @@ __device__ __forceinline__ void packed_setup(const SetupMaps& in, CUtensorMap* o
         : "memory");
 }
 
-// Before the backward, for the rows that hold sequences: nd = -D, D[h, t] =
-// sum_i dO * O, nl = -lse in log2 units, both [H][T rounded up to 128] and
-// filled up to the end of the last row's tile (nl -inf: P = 0), and zeros in
-// the fp32 dq accumulator.  A warp takes kRowsPerWarp tokens of a head, whose
-// loads are issued together; the first block does the setup and the fill.
-constexpr int kRowsPerWarp = 4;
-__global__ void __launch_bounds__(256)
-    attention_packed_pre_kernel(const __grid_constant__ SetupMaps in, CUtensorMap* out, int* ctl, const int* meta,
-                                const bf16* __restrict__ o, long long o_tok, long long o_head,
-                                const bf16* __restrict__ dout, long long do_tok, long long do_head,
+// Before the backward, for the rows that hold sequences: nd = -D, D[h, t] = sum_j
+// P_tj dP_tj over the keys that t sees, dP_tj = dO_t . v_j; nl = -lse in log2
+// units; both [H][T rounded up to 128] and filled up to the end of the last
+// row's tile (nl -inf: P = 0); zeros in the fp32 dq accumulator; and the
+// backward's setup.
+//
+// D could be had as dO_t . o_t from the forward's o, in 50 us instead of 137 (32,768
+// tokens of documents, 10 heads), but o is rounded to bf16, and dS = P (dP - D)
+// would carry the whole error of D in rows whose probability sits on one key,
+// where dP - D of that key is small: dq and dk were then off by 0.004 to 0.008 of
+// their norm on sequences of 2 to 40 tokens, against 0.0024 for a rounding of dS
+// and one of the result.  So the kernel takes P and dP as the backward will, S =
+// Q K^T and dP = dO V^T into TMEM and P = exp(S - lse), and divides by sum_j P_tj,
+// which makes the row sums of dS vanish to fp32.
+//
+// Persistent, a block an SM, items by cluster launch control as in the
+// forward.  608 threads:
+//   warps 0..15 two groups of eight, group b for every other key block, in TMEM
+//               columns 256 b (S) and 256 b + 128 (dP); two threads for a query
+//               row (TMEM lane), each 64 of the block's keys; the four sums of a
+//               row meet in shared memory.  (One thread a row and group: 184 us.)
+//   warp 16     TMA: takes the items and publishes them in a shared ring; loads
+//               Q and dO, and K_j and V_j through two-slot rings
+//   warp 17     TMEM owner and MMA issuer
+//   warp 18     the backward's setup (every block writes the same words)
+// DRAM alone takes 75 us (q, k, v, dO read, the zeros written); the rest is the
+// latency of TMEM loads and barriers (tensor pipe 41% busy, issue slots 33%).  Two
+// tiles that share their key blocks load half as much, but leave no second
+// buffer of S and dP: 180 us.
+constexpr int PD_SUMS = 2 * 3 * 128 * 8;
+constexpr int PD_SMEM = 6 * TF_BUF + PD_SUMS + 4 * static_cast<int>(sizeof(CUtensorMap)) + 256;
+
+template <bool kFine>
+__global__ void __launch_bounds__(608, 1)
+    attention_packed_dot_kernel(const __grid_constant__ SetupMaps in, CUtensorMap* maps, int* ctl,
                                 const float* __restrict__ lse, float* __restrict__ nl, float* __restrict__ nd,
-                                float* __restrict__ dq, int H, int T, int* err) {
-  __shared__ __align__(128) CUtensorMap stage[4];
-  chain_go();
-  chain_wait();
-  const bool fits = meta[kMetaMagic] == kPlanMagic && meta[kMetaT] == T;
-  const int valid = fits ? meta[kMetaTotal] : 0, pitch = (T + 127) / 128 * 128, lane = lane_id();
-  if (blockIdx.x == 0) {
-    if (warp_id() == 0) packed_setup(in, out, ctl, meta, T, err, stage);
-    const int fill = (valid + 127) / 128 * 128 - valid;
-    for (int i = threadIdx.x; i < H * fill; i += 256) {
-      const long long at = static_cast<long long>(i / fill) * pitch + valid + i % fill;
-      nl[at] = -INFINITY;
-      nd[at] = 0.f;
+                                float* __restrict__ dq, int H, int Hkv, int T, float scale_log2, int* err,
+                                long long wait_cycles, const PackedArgs pk) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // the 128-byte-swizzled tiles need a 1024-byte-aligned base, which the
+  // dynamic shared memory window provides; refuse to run otherwise
+  if (smem_u32(smem_raw) & 1023u) {
+    chain_wait();
+    if (threadIdx.x == 0) {
+      if (err) atomicOr(err, ERRF_SHAPE);
+      ctl[kCtlSched] = ctl[kCtlEntries] = ctl[kCtlValid] = 0;   // no backward either
     }
     return;
   }
-  const int groups = (valid + kRowsPerWarp - 1) / kRowsPerWarp, w = (blockIdx.x - 1) * 8 + warp_id();
-  if (w >= groups * H) return;
-  const int h = w / groups, t0 = (w - h * groups) * kRowsPerWarp, n = min(kRowsPerWarp, valid - t0);
-  uint2 x[kRowsPerWarp], y[kRowsPerWarp];
-#pragma unroll
-  for (int i = 0; i < kRowsPerWarp; ++i) {
-    if (i >= n) break;
-    x[i] = *reinterpret_cast<const uint2*>(o + (t0 + i) * o_tok + h * o_head + lane * 4);
-    y[i] = *reinterpret_cast<const uint2*>(dout + (t0 + i) * do_tok + h * do_head + lane * 4);
+  uint8_t* sQ = smem_raw;
+  uint8_t* sdO = smem_raw + TF_BUF;
+  uint8_t* sK = smem_raw + 2 * TF_BUF;   // two slots
+  uint8_t* sV = smem_raw + 4 * TF_BUF;   // two slots
+  float2* sums = reinterpret_cast<float2*>(smem_raw + 6 * TF_BUF);   // [2][3][128]: sums of P and P dP, item n & 1
+  CUtensorMap* stage = reinterpret_cast<CUtensorMap*>(smem_raw + 6 * TF_BUF + PD_SUMS);
+  uint4* answer = reinterpret_cast<uint4*>(stage + 4);   // next_block_ask's
+  uint64_t* bars = reinterpret_cast<uint64_t*>(answer + 1);
+  uint64_t* q_full = bars + 0;     // Q and dO of item n landed (or the end marker)
+  uint64_t* q_empty = bars + 1;    // item n's products done and every row warp has its fields
+  uint64_t* kv_full = bars + 2;    // [2]
+  uint64_t* kv_empty = bars + 4;   // [2]
+  uint64_t* sd_full = bars + 6;    // [2] per group: S and dP of a block in TMEM
+  uint64_t* sd_empty = bars + 8;   // [2] per group: they have been read
+  uint64_t* part = bars + 10;      // [2]: the sums of item n, n & 1, are in shared memory
+  uint64_t* drain = bars + 12;
+  uint64_t* answered = bars + 13;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 14);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  // [4][4]: head (-1: end), tile, first key block
+  volatile int* item_ring = reinterpret_cast<volatile int*>(tmem_holder + 2);
+
+  const int warp = warp_id(), lane = lane_id();
+  const long long wlim = wait_limit_or_default(wait_cycles);
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1 + 16);   // the MMA commit and one arrival per row warp
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&kv_full[i], 1); mbar_init(&kv_empty[i], 1);
+      mbar_init(&sd_full[i], 1); mbar_init(&sd_empty[i], 256); mbar_init(&part[i], 384);
+    }
+    mbar_init(drain, 1);
+    mbar_init(answered, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    for (int i = 0; i < 4; ++i) tma_prefetch_desc(&in.m[i]);
   }
-  const float l = lane < n ? lse[static_cast<long long>(h) * T + t0 + lane] : 0.f;
-  float d = 0.f;
-#pragma unroll
-  for (int i = 0; i < kRowsPerWarp; ++i) {
-    if (i >= n) break;
-    const long long row = static_cast<long long>(h) * T + t0 + i;
-    reinterpret_cast<float4*>(dq + row * HD)[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float s = warp_sum(bf16_lo(x[i].x) * bf16_lo(y[i].x) + bf16_hi(x[i].x) * bf16_hi(y[i].x) +
-                             bf16_lo(x[i].y) * bf16_lo(y[i].y) + bf16_hi(x[i].y) * bf16_hi(y[i].y));
-    if (lane == i) d = s;
+  if (warp == 17) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
   }
-  if (lane < n) {
-    const long long at = static_cast<long long>(h) * pitch + t0 + lane;
-    nl[at] = l * -1.4426950408889634f;
-    nd[at] = -d;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  chain_wait();
+  // positions that hold sequences; a plan of another T is refused (by the setup)
+  const bool fits = pk.meta[kMetaMagic] == kPlanMagic && pk.meta[kMetaT] == T;
+  const int Tv = fits ? pk.meta[kMetaTotal] : 0;
+
+  if (warp == 18) {
+    packed_setup(in, maps, ctl, pk.meta, T, err, stage);
+  } else if (warp == 16) {
+    if (lane == 0) {
+      // -------------------------------------------------------------- TMA
+      // item number and fields are fetched one item ahead, as in the forward
+      const int entries = fits ? pk.meta[kMetaFwd] : 0, n_items = entries * H;
+      int nx_h = -1;
+      int2 nx = make_int2(0, 0);
+      bool asked = false;
+      uint32_t answers = 0;
+      auto fetch = [&](int idx) {   // false: a block without work (tiles past the sequences)
+        if (idx >= n_items) return false;
+        nx_h = idx / entries;
+        nx = __ldg(pk.fwd + (idx - nx_h * entries));
+        return true;
+      };
+      auto take = [&] {   // false: the wait expired
+        nx_h = -1;
+        while (asked) {
+          if (!mbar_wait_t<kFine>(answered, answers & 1, abort_flag, err, wlim)) return false;
+          ++answers;
+          asked = false;
+          const int idx = next_block_answer(answer);
+          if (idx < 0 || fetch(idx)) break;
+          next_block_ask(answer, answered);
+          asked = true;
+        }
+        return true;
+      };
+      fetch(blockIdx.x);
+      bool ok = true;
+      uint32_t g = 0;     // key blocks loaded so far
+      int last_q = -1;    // last item whose Q was loaded
+      for (int n = 0;; ++n) {
+        // the previous item's Q and dO are no longer read and every warp has its fields
+        if (n > 0 && !mbar_wait_t<kFine>(q_empty, (n - 1) & 1, abort_flag, err, wlim)) { ok = false; break; }
+        volatile int* f = item_ring + 4 * (n & 3);
+        const int h = nx_h, qt = nx.x, j0 = nx.y;
+        f[0] = h; f[1] = qt; f[2] = j0;
+        if (h < 0) {
+          mbar_arrive(q_full);   // end marker: releases the ring entry
+          break;
+        }
+        next_block_ask(answer, answered);
+        asked = true;
+        const int hk = h / (H / Hkv);
+        mbar_arrive_expect_tx(q_full, 2 * TF_BUF);
+        for (int c = 0; c < 2; ++c) {
+          tma_load_3d(sQ + c * TF_TILE, &in.m[0], q_full, 64 * c, qt * 128, h);
+          tma_load_4d(sdO + c * TF_TILE, &in.m[3], q_full, 64 * c, h, qt * 128, 0);
+        }
+        last_q = n;
+        for (int j = j0; j <= qt; ++j, ++g) {
+          const uint32_t s = g & 1;
+          if (!mbar_wait_t<kFine>(&kv_empty[s], ((g >> 1) & 1) ^ 1u, abort_flag, err, wlim)) { ok = false; break; }
+          mbar_arrive_expect_tx(&kv_full[s], 2 * TF_BUF);
+          for (int c = 0; c < 2; ++c) {
+            tma_load_3d(sK + s * TF_BUF + c * TF_TILE, &in.m[1], &kv_full[s], 64 * c, j * 128, hk);
+            tma_load_3d(sV + s * TF_BUF + c * TF_TILE, &in.m[2], &kv_full[s], 64 * c, j * 128, hk);
+          }
+          if (j == j0 && !take()) { ++g; ok = false; break; }
+        }
+        if (!ok) break;
+      }
+      if (!ok) {
+        // let the copies already started land before the CTA exits
+        if (asked)
+          for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(answered, answers & 1); ++i) {}
+        if (last_q >= 0)
+          for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(q_full, last_q & 1); ++i) {}
+        for (uint32_t x = g > 2 ? g - 2 : 0; x < g; ++x)
+          for (uint32_t i = 0; i < (1u << 20) && !mbar_try_wait(&kv_full[x & 1], (x >> 1) & 1); ++i) {}
+      }
+    }
+  } else if (warp == 17) {
+    // -------------------------------------------------------------- MMA
+    // the whole warp, converged; one lane issues
+    const bool leader = elect_lane();
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    auto wait1 = [&](uint64_t* bar, uint32_t par) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait_t<kFine>(bar, par, abort_flag, err, wlim));
+    };
+    constexpr uint32_t IDESC = make_idesc(1, 128, false, false);
+    // X = A B^T over the 128 head dims, both operands K-major
+    auto product = [&](uint32_t d_tmem, const uint8_t* a, const uint8_t* b) {
+      const uint64_t da = smem_desc_sw128(smem_u32(a), 16, 1024), db = smem_desc_sw128(smem_u32(b), 16, 1024);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        const uint32_t off16 = ((kk >> 2) * TF_TILE + (kk & 3) * 32) >> 4;
+        umma_f16_by(leader, d_tmem, da + off16, db + off16, IDESC, kk > 0 ? 1u : 0u);
+      }
+    };
+    bool ok = true;
+    uint32_t g = 0;   // key blocks done so far
+    for (int n = 0; ok; ++n) {
+      if (!wait1(q_full, n & 1)) break;
+      const volatile int* f = item_ring + 4 * (n & 3);
+      const int h = __shfl_sync(0xffffffffu, f[0], 0), qt = __shfl_sync(0xffffffffu, f[1], 0);
+      const int j0 = __shfl_sync(0xffffffffu, f[2], 0);
+      if (h < 0) break;
+      for (int j = j0; j <= qt; ++j, ++g) {
+        const uint32_t s = g & 1, use = (g >> 1) & 1;
+        if (!wait1(&kv_full[s], use) || !wait1(&sd_empty[s], use ^ 1u)) { ok = false; break; }
+        tc_fence_after();
+        product(tm + 256 * s, sQ, sK + s * TF_BUF);
+        product(tm + 256 * s + 128, sdO, sV + s * TF_BUF);
+        umma_commit_by(leader, &sd_full[s]);
+        umma_commit_by(leader, &kv_empty[s]);
+        if (j == qt) umma_commit_by(leader, q_empty);   // the item's last products
+      }
+    }
+    umma_commit_by(leader, drain);
+    for (uint32_t i = 0; i < (1u << 22) && !mbar_try_wait(drain, 0); ++i) {}
+  } else {
+    // ------------------------------------------------------------- rows
+    const int grp = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
+    const uint32_t t_s = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 256 * grp, t_d = t_s + 128;
+    const uint64_t sl2 = f2_pack(scale_log2, scale_log2);
+    const int pitch = (T + 127) / 128 * 128;
+    bool ok = true;
+    uint32_t g = 0;   // key blocks so far, both groups'
+    auto wait_all = [&](uint64_t* bar, uint32_t par) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait_t<kFine>(bar, par, abort_flag, err, wlim));
+    };
+    for (int n = 0; ok; ++n) {
+      if (!wait_all(q_full, n & 1)) break;
+      const volatile int* f = item_ring + 4 * (n & 3);
+      const int h = f[0], qt = f[1], j0 = f[2];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_empty);   // this warp has the fields
+      if (h < 0) break;
+      const int r = quarter * 32 + lane, q = qt * 128 + r;
+      const bool row = q < Tv;
+      const int lo = row ? __ldg(pk.lo + q) : 0;   // first key of the row
+      const int lo_max = __reduce_max_sync(0xffffffffu, lo);
+      const float m = row ? lse[static_cast<long long>(h) * T + q] * -1.4426950408889634f : -INFINITY;
+      const uint64_t m2 = f2_pack(m, m);
+      // zeros for the sums of dq, each warp every eighth row
+      for (int x = qt * 128 + warp; x < min(qt * 128 + 128, Tv); x += 16)
+        reinterpret_cast<float4*>(dq + (static_cast<long long>(h) * T + x) * HD)[lane] =
+            make_float4(0.f, 0.f, 0.f, 0.f);
+      uint64_t l2 = f2_pack(0.f, 0.f), d2 = l2;   // sums of P and of P dP
+      for (int j = j0; j <= qt; ++j, ++g) {
+        if (static_cast<int>(g & 1) != grp) continue;
+        if (!wait_all(&sd_full[grp], (g >> 1) & 1)) { ok = false; break; }
+        tc_fence_after();
+        const int kbase = j * 128;
+        const bool masked = j == qt || kbase < lo_max;
+        const int first = lo - kbase, end = q + 1 - kbase;   // keys that this row sees: first .. end - 1
+        auto add = [&](const uint32_t (&x)[32], const uint32_t (&y)[32]) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), sl2, m2), x0, x1);
+            const uint64_t p = f2_pack(ex2_approx(x0), ex2_approx(x1));
+            l2 = f2_add(l2, p);
+            d2 = f2_fma(p, f2_pack(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), d2);
+          }
+        };
+#pragma unroll 1
+        for (int c = 2 * half; c < 2 * half + 2; ++c) {
+          const uint32_t seen = masked ? low_bits(end - 32 * c) & ~low_bits(first - 32 * c) : ~0u;
+          if (!__any_sync(0xffffffffu, seen != 0)) continue;
+          uint32_t x[32], y[32];
+          tmem_load32_async(t_s + 32 * c, x);
+          tmem_load32_async(t_d + 32 * c, y);
+          tmem_wait_ld();
+          if (masked) {
+            mask_scores(x, seen);
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (!(seen & (1u << k))) y[k] = 0u;   // P = 0 would not remove a NaN
+          }
+          add(x, y);
+        }
+        tc_fence_before();
+        mbar_arrive(&sd_empty[grp]);
+      }
+      if (!ok) break;
+      float l0, l1, d0, d1;
+      f2_unpack(l2, l0, l1);
+      f2_unpack(d2, d0, d1);
+      float2 mine = make_float2(l0 + l1, d0 + d1);
+      const int who = warp >> 2;   // group and half
+      float2* row_sums = sums + (n & 1) * 3 * 128 + r;
+      if (who > 0) {
+        // item n - 2's sums have been read: this item was published after every warp had taken the one before
+        row_sums[(who - 1) * 128] = mine;
+        mbar_arrive(&part[n & 1]);
+      } else {
+        if (!wait_all(&part[n & 1], (n >> 1) & 1)) break;
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+          mine.x += row_sums[x * 128].x;
+          mine.y += row_sums[x * 128].y;
+        }
+        const long long at = static_cast<long long>(h) * pitch + q;
+        nl[at] = m;
+        nd[at] = row ? -mine.y / mine.x : 0.f;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 17) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 
-// dq in bf16 from the fp32 sums, rows that hold sequences.
+// dq in bf16 from the fp32 sums, rows that hold sequences.  A warp takes
+// kRowsPerWarp of them, whose loads are issued together.
+constexpr int kRowsPerWarp = 4;
 __global__ void __launch_bounds__(256)
     attention_packed_dq_kernel(const float* __restrict__ acc, bf16* __restrict__ dq, long long dq_tok,
                                long long dq_head, const int* ctl, int H, int T) {
@@ -2360,14 +2617,15 @@ cudaError_t launch_attn_packed_fwd(const PackedTensor& q, const PackedTensor& k,
 }
 
 cudaError_t launch_attn_packed_bwd(const PackedTensor& q, const PackedTensor& k, const PackedTensor& v,
-                                   const PackedTensor& o, const PackedTensor& dout, const float* lse,
-                                   const PackedTensor& dq, const PackedTensor& dk, const PackedTensor& dv, int H,
-                                   int Hkv, int T, float scale, const void* plan, void* scratch, cudaStream_t s,
-                                   int* err, long long wait_cycles) {
+                                   const PackedTensor& dout, const float* lse, const PackedTensor& dq,
+                                   const PackedTensor& dk, const PackedTensor& dv, int H, int Hkv, int T, float scale,
+                                   const void* plan, void* scratch, cudaStream_t s, int* err, long long wait_cycles) {
   const bool fine = wait_limit_or_default(wait_cycles) < kShortWaitCycles;
   auto kern = fine ? attn_bwd_tc_kernel<true, true> : attn_bwd_tc_kernel<false, true>;
-  static std::atomic<unsigned long long> configured[2] = {};
+  auto dot = fine ? attention_packed_dot_kernel<true> : attention_packed_dot_kernel<false>;
+  static std::atomic<unsigned long long> configured[4] = {};
   cudaError_t e = set_smem_limit_once(kern, TB_SMEM, configured[fine ? 1 : 0]);
+  if (e == cudaSuccess) e = set_smem_limit_once(dot, PD_SMEM, configured[fine ? 3 : 2]);
   if (e != cudaSuccess) return e;
   const size_t rows = static_cast<size_t>(T) * H;
   uint8_t* base = static_cast<uint8_t*>(scratch);
@@ -2388,13 +2646,14 @@ cudaError_t launch_attn_packed_bwd(const PackedTensor& q, const PackedTensor& k,
     return cudaErrorInvalidValue;
   const PlanView P = plan_view(const_cast<void*>(plan), T);
   const int row_blocks = static_cast<int>((rows + 8 * kRowsPerWarp - 1) / (8 * kRowsPerWarp));
-  const int pre_blocks = static_cast<int>((((T + kRowsPerWarp - 1ll) / kRowsPerWarp) * H + 7) / 8);
-  e = launch_chained(
-      attention_packed_pre_kernel, 1ll + pre_blocks, 256, 0, s, maps, dmaps, ctl, P.meta,
-      static_cast<const bf16*>(o.ptr), o.tok, o.head, static_cast<const bf16*>(dout.ptr), dout.tok, dout.head, lse, nl,
-      nd, acc, H, T, err);
-  if (e != cudaSuccess) return e;
   PackedArgs pa = {};
+  pa.meta = P.meta;
+  pa.lo = P.lo;
+  pa.fwd = P.fwd;
+  const int items = (T + 127) / 128 * H;   // a block each, as in the forward
+  e = launch_chained(dot, items, 608, PD_SMEM, s, maps, dmaps, ctl, lse, nl, nd, acc, H, Hkv, T,
+                     scale * 1.4426950408889634f, err, wait_cycles, pa);
+  if (e != cudaSuccess) return e;
   pa.hi = P.hi;
   pa.bwd = P.bwd;
   pa.ctl = ctl;

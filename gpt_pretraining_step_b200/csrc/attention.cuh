@@ -61,9 +61,8 @@ cudaError_t launch_attn_packed_fwd(const PackedTensor& q, const PackedTensor& k,
                                    const void* plan, cudaStream_t s, int* err, long long wait_cycles);
 size_t attention_packed_bwd_scratch(int T, int H);
 cudaError_t launch_attn_packed_bwd(const PackedTensor& q, const PackedTensor& k, const PackedTensor& v,
-                                   const PackedTensor& o, const PackedTensor& dout, const float* lse,
-                                   const PackedTensor& dq, const PackedTensor& dk, const PackedTensor& dv, int H,
-                                   int Hkv, int T, float scale, const void* plan, void* scratch, cudaStream_t s,
-                                   int* err, long long wait_cycles);
+                                   const PackedTensor& dout, const float* lse, const PackedTensor& dq,
+                                   const PackedTensor& dk, const PackedTensor& dv, int H, int Hkv, int T, float scale,
+                                   const void* plan, void* scratch, cudaStream_t s, int* err, long long wait_cycles);
 
 }  // namespace gpt

@@ -482,9 +482,13 @@ int gpt_op_attention_packed_fwd(const gpt_heads* q, const gpt_heads* k, const gp
                                 void* stream);
 
 /* Its backward: gradients of q, k and v (bf16; dk and dv summed over the
- * query heads of a kv head) from dout, with o and lse of the forward.  Sums
+ * query heads of a kv head) from dout, with lse of the forward.  Sums
  * are held in fp32; those of dq add up in no fixed order, so two runs may
  * differ in its last bit.  Outputs must not overlap each other or the inputs.
+ *   o        of the forward: checked like the others, but not read, since the
+ *            rows' D = sum_j P_tj (dout_t . v_j) is computed from its terms (o,
+ *            rounded to bf16, would lose what is left of dP - D in rows whose
+ *            probability sits on one key)
  *   scratch  device buffer of gpt_op_attention_packed_bwd_scratch(n_tokens, H)
  *            bytes, 256-byte aligned, of this call alone while it runs */
 size_t gpt_op_attention_packed_bwd_scratch(int n_tokens, int H);
