@@ -48,9 +48,12 @@ constexpr int HD = 128;
 // the tensor maps to device memory with their token extent cut to the
 // sequences' end, so that TMA fills the rows of all four operands with zeros.
 // Scores, maxima, row sums, lse, D and every sum over keys or queries are fp32.
-// P and dS are rounded to bf16, as the tensor cores take both operands of a
-// product in one type and q, k, v and dO are bf16, and dS is formed from the
-// rounded P.
+// Rounded to bf16 are only P, as the operand of P V and P^T dO, and dS, formed
+// from P in fp32, as that of dS K and dS^T Q: the tensor cores take both operands
+// of a product in one type, and q, k, v and dO are bf16.  Measured in the 2-norm
+// against 64 bits on sequences of 2 to 300 tokens, scores of the usual size and
+// eight times as large: dq and dk 0.0023 to 0.0025, dv 0.0015 to 0.0023, o 0.0018
+// to 0.0021, of which 0.0017 is the rounding of the result.
 struct PackedArgs {
   const int* meta;          // forward: the plan's kMeta* words
   const int* lo;            // [T]
@@ -1261,7 +1264,8 @@ __global__ void __launch_bounds__(512, 1)
 
   // registers: 72 for the TMA / MMA warp group, 96 for the dQ group, 168 for
   // the two softmax groups (4*72 + 4*96 + 8*168 = 2016 per lane of a warp,
-  // within the 16 warps x 128 the block is launched with)
+  // within the 16 warps x 128 the block is launched with); packed, whose softmax
+  // holds P in fp32: 72, 88 and 176 (4*72 + 4*88 + 8*176 = 2048)
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n" ::: "memory");
   if (warp == 0) {
     if (lane == 0) {
@@ -1493,7 +1497,8 @@ __global__ void __launch_bounds__(512, 1)
     umma_commit_by(leader, drain);
     for (uint32_t x = 0; x < (1u << 22) && !mbar_try_wait(drain, 0); ++x) {}
   } else if (warp >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n" ::: "memory");
+    if constexpr (kPacked) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n" ::: "memory");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n" ::: "memory");
     // ------------------------------------------------------------------ dQ
     const int quarter = warp & 3;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
@@ -1557,7 +1562,8 @@ __global__ void __launch_bounds__(512, 1)
     }
     if (lane == 0) bulk_wait_all();
   } else if (warp >= 4) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;\n" ::: "memory");
+    if constexpr (kPacked) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n" ::: "memory");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 168;\n" ::: "memory");
     // ------------------------------------------------------- P, dS, dK, dV
     const int quarter = warp & 3;
     const int half = (warp - 4) >> 2;        // which 64 query columns of the row
@@ -1634,8 +1640,9 @@ __global__ void __launch_bounds__(512, 1)
           float* base = (t256 < 128 ? lse_s : dd_s) + ((g0 + it2) & 1) * 128;
           base[t256 & 127] = v;
         };
-        // P of block it2 for this thread's key row and 64 query columns, packed bf16
-        uint32_t pk[32];
+        // P of block it2 for this thread's key row and 64 query columns: packed bf16,
+        // from which dS is formed too; packed build: fp32 for dS, rounded for dV alone
+        uint32_t pk[kPacked ? 64 : 32];
         auto compute_p = [&](int it2) {
           const bool diag = it2 % kb.nb == 0;
           const int q0 = kb.q_block(it2) * 128;
@@ -1662,7 +1669,7 @@ __global__ void __launch_bounds__(512, 1)
             const uint32_t (&sr)[32] = cc == 0 ? sa : sb;
             if constexpr (mode == 3) {
 #pragma unroll
-              for (int x = 0; x < 16; ++x) pk[16 * cc + x] = 0u;
+              for (int x = 0; x < (kPacked ? 32 : 16); ++x) pk[(kPacked ? 32 : 16) * cc + x] = 0u;
             } else {
 #pragma unroll
               for (int kq = 0; kq < 32; kq += 8) {
@@ -1698,8 +1705,13 @@ __global__ void __launch_bounds__(512, 1)
                   for (int e = 0; e < 8; ++e)
                     if (!key_ok || (diag && key > q0 + c * 32 + kq + e) || key < q0 + c * 32 + kq + e - wl) p[e] = 0.f;
                 }
+                if constexpr (kPacked) {
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) pk[16 * cc + ((kq + e) >> 1)] = pack_bf16x2(p[e], p[e + 1]);
+                  for (int e = 0; e < 8; ++e) pk[32 * cc + kq + e] = __float_as_uint(p[e]);
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 8; e += 2) pk[16 * cc + ((kq + e) >> 1)] = pack_bf16x2(p[e], p[e + 1]);
+                }
               }
             }
           };
@@ -1756,29 +1768,49 @@ __global__ void __launch_bounds__(512, 1)
             tc_fence_after();
             uint32_t da[32], db[32];
             tmem_load32_async(tmem + lane_base + 128 + (2 * half) * 32, da);
-            tmem_load32_async(tmem + lane_base + 128 + (2 * half + 1) * 32, db);
-            tmem_wait_ld();
-            // P^T_i over the first 32 of the 64 dP^T columns this warp has just read
-            tmem_store32(tmem + lane_base + 128 + 64 * half, pk);
+            // P^T_i over the first 32 of this warp's 64 dP^T columns, once they are read
+            if constexpr (kPacked) {
+              uint32_t pb[32];
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                pb[x] = pack_bf16x2(__uint_as_float(pk[2 * x]), __uint_as_float(pk[2 * x + 1]));
+              tmem_landed(da);
+              tmem_store32(tmem + lane_base + 128 + 64 * half, pb);
+            } else {
+              tmem_load32_async(tmem + lane_base + 128 + (2 * half + 1) * 32, db);
+              tmem_wait_ld();
+              tmem_store32(tmem + lane_base + 128 + 64 * half, pk);
+            }
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_fence_before();
             mbar_arrive(p_ready);
+            // the other 32, which dV leaves alone, while the first become dS (with P in
+            // fp32 there are no registers for all 64 before)
+            if constexpr (kPacked) tmem_load32_async(tmem + lane_base + 128 + (2 * half + 1) * 32, db);
             const float* nds = dd_s + (gi & 1) * 128;
             uint32_t dk2[32];
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc) {
               const int c = 2 * half + cc;
               const uint32_t (&dr)[32] = cc == 0 ? da : db;
+              if (kPacked && cc == 1) tmem_landed(db);
 #pragma unroll
               for (int kq = 0; kq < 32; kq += 4) {
                 const float4 d4 = *reinterpret_cast<const float4*>(nds + c * 32 + kq);
-                const uint32_t w0 = pk[16 * cc + (kq >> 1)], w1 = pk[16 * cc + (kq >> 1) + 1];
+                float pr[4];
+                if constexpr (kPacked) {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) pr[e] = __uint_as_float(pk[32 * cc + kq + e]);
+                } else {
+                  const uint32_t w0 = pk[16 * cc + (kq >> 1)], w1 = pk[16 * cc + (kq >> 1) + 1];
+                  pr[0] = bf16_lo(w0); pr[1] = bf16_hi(w0); pr[2] = bf16_lo(w1); pr[3] = bf16_hi(w1);
+                }
                 float a0, a1, a2, a3;
-                f2_unpack(f2_mul(f2_pack(bf16_lo(w0), bf16_hi(w0)),
+                f2_unpack(f2_mul(f2_pack(pr[0], pr[1]),
                                  f2_add(f2_pack(__uint_as_float(dr[kq]), __uint_as_float(dr[kq + 1])),
                                         f2_pack(d4.x, d4.y))),
                           a0, a1);
-                f2_unpack(f2_mul(f2_pack(bf16_lo(w1), bf16_hi(w1)),
+                f2_unpack(f2_mul(f2_pack(pr[2], pr[3]),
                                  f2_add(f2_pack(__uint_as_float(dr[kq + 2]), __uint_as_float(dr[kq + 3])),
                                         f2_pack(d4.z, d4.w))),
                           a2, a3);
@@ -1788,6 +1820,7 @@ __global__ void __launch_bounds__(512, 1)
             }
             store_row_units(sdSt, dk2, half, r);
             fence_proxy_async_smem();
+            if constexpr (kPacked) tc_fence_before();   // the next dP^T goes where db was read
             mbar_arrive(ds_ready);
           }
           // P_{i+1} while the tensor cores run this block's dV, dK, dQ
@@ -2136,12 +2169,11 @@ __device__ __forceinline__ void packed_setup(const SetupMaps& in, CUtensorMap* o
 // row's tile (nl -inf: P = 0); zeros in the fp32 dq accumulator; and the
 // backward's setup.
 //
-// D could be had as dO_t . o_t from the forward's o, in 50 us instead of 137 (32,768
+// D could be had as dO_t . o_t from the forward's o, in 50 us instead of 155 (32,768
 // tokens of documents, 10 heads), but o is rounded to bf16, and dS = P (dP - D)
 // would carry the whole error of D in rows whose probability sits on one key,
 // where dP - D of that key is small: dq and dk were then off by 0.004 to 0.008 of
-// their norm on sequences of 2 to 40 tokens, against 0.0024 for a rounding of dS
-// and one of the result.  So the kernel takes P and dP as the backward will, S =
+// their norm on sequences of 2 to 40 tokens, against 0.0024 now.  So the kernel takes P and dP as the backward will, S =
 // Q K^T and dP = dO V^T into TMEM and P = exp(S - lse), and divides by sum_j P_tj,
 // which makes the row sums of dS vanish to fp32.
 //
@@ -2158,7 +2190,7 @@ __device__ __forceinline__ void packed_setup(const SetupMaps& in, CUtensorMap* o
 // DRAM alone takes 75 us (q, k, v, dO read, the zeros written); the rest is the
 // latency of TMEM loads and barriers (tensor pipe 41% busy, issue slots 33%).  Two
 // tiles that share their key blocks load half as much, but leave no second
-// buffer of S and dP: 180 us.
+// buffer of S and dP: 193 us.
 constexpr int PD_SUMS = 2 * 3 * 128 * 8;
 constexpr int PD_SMEM = 6 * TF_BUF + PD_SUMS + 4 * static_cast<int>(sizeof(CUtensorMap)) + 256;
 
@@ -2397,7 +2429,8 @@ __global__ void __launch_bounds__(608, 1)
           uint32_t x[32], y[32];
           tmem_load32_async(t_s + 32 * c, x);
           tmem_load32_async(t_d + 32 * c, y);
-          tmem_wait_ld();
+          tmem_landed(x);
+          tmem_landed(y);
           if (masked) {
             mask_scores(x, seen);
 #pragma unroll
