@@ -36,6 +36,7 @@ ABI_FUNCTIONS = [
     "gpt_op_attention_plan_bytes", "gpt_op_attention_plan", "gpt_op_attention_packed_fwd",
     "gpt_op_attention_packed_bwd_scratch", "gpt_op_attention_packed_bwd", "gpt_op_policy_loss_scratch",
     "gpt_op_policy_loss", "gpt_op_preference_loss_scratch", "gpt_op_preference_loss",
+    "gpt_op_preference_loss_ex",
 ]
 DTYPE_BF16, DTYPE_FP32 = 0, 1
 GRAD_BUCKETS = 6
@@ -138,6 +139,8 @@ def lib():
             "gpt_op_preference_loss_scratch": (sz, [i32, i32]),
             "gpt_op_preference_loss": (i32, [vp, i32, i64, vp, vp, i32, vp, i32, i32, f32, f32, vp, vp, vp, vp, vp,
                                              i64, vp, vp]),
+            "gpt_op_preference_loss_ex": (i32, [vp, i32, i64, vp, vp, i32, vp, i32, i32, f32, f32, vp, vp, vp, vp, vp,
+                                                i64, i32, vp, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -675,14 +678,18 @@ def policy_loss(logits, targets, old_logp, advantage, weight, ref_logp=None, kl_
 
 
 def preference_loss(logits, targets, cu_seqlens, ref_logp=None, beta=0.1, label_smoothing=0.0, grad=True,
-                    dlogits=None, stream=None):
+                    dlogits=None, stream=None, clear_past=None):
     """Preference loss over pairs of packed answers and its gradient
     (gpt_op_preference_loss): sequences 2 i (chosen) and 2 i + 1 (rejected) of
     cu_seqlens int32 [2 pairs + 1].  logits, targets, grad and dlogits as for
     policy_loss; ref_logp fp32 [2 pairs], the reference model's seq_logp.
-    Returns (loss [], margin [pairs], seq_logp [2 pairs], logp [M], dlogits);
-    rows past the last sequence keep what they held (new tensors: anything)."""
+    Returns (loss [], margin [pairs], seq_logp [2 pairs], logp [M], dlogits).
+    Rows past the last sequence: logp and a new dlogits hold zeros there; a
+    given dlogits keeps what it held (in place: the logits), or zeros with
+    clear_past=True."""
     import torch
+    if clear_past is None:
+        clear_past = dlogits is None
     M, V, code, ld, dlogits, d, ld_d, dev = _loss_rows(torch, logits, grad, dlogits)
     n, f32, i32 = cu_seqlens.numel() - 1, torch.float32, torch.int32
     if n < 2 or n % 2 or n > _INT_MAX:
@@ -692,9 +699,9 @@ def preference_loss(logits, targets, cu_seqlens, ref_logp=None, beta=0.1, label_
     loss, margin = logits.new_empty((), dtype=f32), logits.new_empty(n // 2, dtype=f32)
     seq_logp, logp = logits.new_empty(n, dtype=f32), logits.new_empty(M, dtype=f32)
     scratch = targets.new_empty(_words("gpt_op_preference_loss_scratch", M, n // 2))
-    _check(lib().gpt_op_preference_loss(
+    _check(lib().gpt_op_preference_loss_ex(
         logits.data_ptr(), code, ld, y, cu, n // 2, ref, M, V, beta, label_smoothing, loss.data_ptr(),
-        margin.data_ptr(), seq_logp.data_ptr(), logp.data_ptr(), d, ld_d, scratch.data_ptr(),
+        margin.data_ptr(), seq_logp.data_ptr(), logp.data_ptr(), d, ld_d, bool(clear_past), scratch.data_ptr(),
         _raw_stream(torch, stream, dev, loss, margin, seq_logp, logp, scratch, dlogits)))
     return loss, margin, seq_logp, logp, dlogits
 

@@ -1886,10 +1886,10 @@ size_t gpt_op_preference_loss_scratch(int M, int n_pairs) {
   return M < 0 || n_pairs < 1 ? 0 : preference_loss_scratch(M, n_pairs);
 }
 
-int gpt_op_preference_loss(const void* logits, int dtype, long long ld, const int32_t* targets,
-                           const int32_t* cu_seqlens, int n_pairs, const float* ref_logp, int M, int V, float beta,
-                           float label_smoothing, float* loss, float* margin, float* seq_logp, float* logp,
-                           void* dlogits, long long ld_d, void* scratch, void* stream) {
+int gpt_op_preference_loss_ex(const void* logits, int dtype, long long ld, const int32_t* targets,
+                              const int32_t* cu_seqlens, int n_pairs, const float* ref_logp, int M, int V, float beta,
+                              float label_smoothing, float* loss, float* margin, float* seq_logp, float* logp,
+                              void* dlogits, long long ld_d, int clear_past, void* scratch, void* stream) {
   LossRows r;
   int rc = loss_rows(logits, dtype, ld, targets, M, V, dlogits, ld_d, scratch, &r);
   if (rc) return rc;
@@ -1897,11 +1897,20 @@ int gpt_op_preference_loss(const void* logits, int dtype, long long ld, const in
   if (!cu_seqlens || !loss || !margin || !seq_logp || (M > 0 && !logp)) return fail(GPT_EINVAL, "null pointer");
   if (!std::isfinite(beta) || !(label_smoothing >= 0.f && label_smoothing <= 1.f))
     return fail(GPT_EINVAL, "beta must be finite and label_smoothing in [0, 1]");
-  PreferenceArgs a{cu_seqlens, n_pairs, ref_logp, beta, label_smoothing, loss, margin, seq_logp, logp};
+  PreferenceArgs a{cu_seqlens, n_pairs, ref_logp, beta, label_smoothing, loss, margin, seq_logp, logp,
+                   clear_past != 0};
   int* err = nullptr;
   if ((rc = op_err(&err))) return rc;
   GPT_CK(launch_preference_loss(r, a, scratch, err, static_cast<cudaStream_t>(stream)));
   return GPT_OK;
+}
+
+int gpt_op_preference_loss(const void* logits, int dtype, long long ld, const int32_t* targets,
+                           const int32_t* cu_seqlens, int n_pairs, const float* ref_logp, int M, int V, float beta,
+                           float label_smoothing, float* loss, float* margin, float* seq_logp, float* logp,
+                           void* dlogits, long long ld_d, void* scratch, void* stream) {
+  return gpt_op_preference_loss_ex(logits, dtype, ld, targets, cu_seqlens, n_pairs, ref_logp, M, V, beta,
+                                   label_smoothing, loss, margin, seq_logp, logp, dlogits, ld_d, 0, scratch, stream);
 }
 
 int gpt_op_rmsnorm_fwd(const float* x, void* y, float* rstd, int M, int d, void* stream) {

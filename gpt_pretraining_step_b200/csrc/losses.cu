@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(1024) policy_sum_kernel(const float4* __restri
 __device__ __forceinline__ int last_row(const PreferenceArgs& a, int M) { return min(a.cu[2 * a.n_pairs], M); }
 
 // Words that the kernels of a call share: blocks of the sums' kernel that are
-// done, and the rows that the sequences cover (0 if their offsets are bad).
+// done, and the rows that the sequences cover (-1 if their offsets are bad).
 struct PairWords {
   int done, rows;
 };
@@ -516,10 +516,12 @@ __global__ void __launch_bounds__(kSumThreads)
   for (int i = tid; i < n; i += kSumThreads) bad |= a.cu[i + 1] < a.cu[i];
   bad = __syncthreads_or(bad);
   if (blockIdx.x == 0 && tid == 0) {
-    words->rows = bad ? 0 : a.cu[n];
+    words->rows = bad ? -1 : a.cu[n];
     if (bad && err) atomicOr(err, ERRF_SEQUENCE);
   }
   if (bad) return;
+  // positions past the last sequence are not counted
+  for (int r = a.cu[n] + blockIdx.x * kSumThreads + tid; r < R.M; r += gridDim.x * kSumThreads) a.logp[r] = 0.f;
   for (int q = blockIdx.x; q < n; q += gridDim.x) {
     const int r1 = a.cu[q + 1];
     double s = 0.0;
@@ -575,10 +577,10 @@ __global__ void __launch_bounds__(G)
                            const float* __restrict__ g, const PairWords* __restrict__ words) {
   extern __shared__ uint4 ring[];
   chain_wait();
-  const int r = blockIdx.x;
-  if (r >= words->rows) return;
+  const int r = blockIdx.x, rows = words->rows;
+  if (rows < 0 || (r >= rows && !a.clear_past)) return;
   T* d = static_cast<T*>(R.dlogits) + r * R.ld_d;
-  const int y = row_target(R, r, nullptr);
+  const int y = r < rows ? row_target(R, r, nullptr) : -1;
   if (y < 0) {
     row_zero<T, G>(d, R.V);
     return;

@@ -36,6 +36,7 @@ struct PreferenceArgs {
   float* margin;     // [n_pairs]
   float* seq_logp;   // [2 n_pairs]
   float* logp;       // [M]
+  bool clear_past;   // zeros in the gradient's rows past the last sequence
 };
 
 size_t policy_loss_scratch(int M);

@@ -536,21 +536,29 @@ int gpt_op_policy_loss(const void* logits, int dtype, long long ld, const int32_
  * counted positions of s and z_i = beta ((L_2i - ref_2i) - (L_2i+1 -
  * ref_2i+1)), the loss is the mean over the pairs of
  *   -(1 - label_smoothing) log sigmoid(z) - label_smoothing log sigmoid(-z).
- *   logits, dtype, ld, targets, dlogits, ld_d   as for gpt_op_policy_loss
+ *   logits, dtype, ld, targets   as for gpt_op_policy_loss
+ *   dlogits, ld_d   as for gpt_op_policy_loss in the rows of the sequences.  The
+ *              rows past the last sequence keep what they held, in place the
+ *              logits: a product over all M rows has to leave them out.  With
+ *              clear_past the _ex call writes zeros there
  *   ref_logp   fp32 [2 n_pairs]: the reference model's sums (seq_logp of a
  *              call on its logits with dlogits NULL), or NULL: zero
  *   loss       fp32 [1];  margin  fp32 [n_pairs]: z
  *   seq_logp   fp32 [2 n_pairs]: L;  logp  fp32 [M]: per position, 0 where
- *              not counted
+ *              not counted, past the last sequence too
  *   scratch    device buffer of gpt_op_preference_loss_scratch(M, n_pairs)
  *              bytes, 256-byte aligned, of this call alone while it runs
- * Rows past the last sequence are neither read nor written.  Bad offsets:
+ * Logits and targets past the last sequence are not read.  Bad offsets:
  * nothing is written and gpt_op_check reports GPT_ERANGE. */
 size_t gpt_op_preference_loss_scratch(int M, int n_pairs);
 int gpt_op_preference_loss(const void* logits, int dtype, long long ld, const int32_t* targets,
                            const int32_t* cu_seqlens, int n_pairs, const float* ref_logp, int M, int V, float beta,
                            float label_smoothing, float* loss, float* margin, float* seq_logp, float* logp,
                            void* dlogits, long long ld_d, void* scratch, void* stream);
+int gpt_op_preference_loss_ex(const void* logits, int dtype, long long ld, const int32_t* targets,
+                              const int32_t* cu_seqlens, int n_pairs, const float* ref_logp, int M, int V, float beta,
+                              float label_smoothing, float* loss, float* margin, float* seq_logp, float* logp,
+                              void* dlogits, long long ld_d, int clear_past, void* scratch, void* stream);
 
 /* Embedding gradient ("¿Cómo Entrenar Tu Propio ChatGPT por $50?", section
  * "1. Modelo GPT": the token embedding x0 = wte[tok]; its gradient scatters
