@@ -633,7 +633,7 @@ def _loss_rows(torch, logits, grad, dlogits):
     ld = _rows("logits", logits, dev)
     M, V = logits.shape
     if M > _INT_MAX or V > _INT_MAX:
-        _refuse("logits", logits, "[M, V] with M below 2^31 and V up to 2^24")
+        _refuse("logits", logits, "[M, V] with M up to 2^30 and V up to 2^24")
     dtype = logits.dtype
     code = DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_FP32
     if code == DTYPE_FP32 and dtype != torch.float32:

@@ -1847,7 +1847,9 @@ int gpt_op_attention_packed_bwd(const gpt_heads* q, const gpt_heads* k, const gp
 // Rows of logits and gradient common to both losses.
 static int loss_rows(const void* logits, int dtype, long long ld, const int32_t* targets, int M, int V, void* dlogits,
                      long long ld_d, const void* scratch, LossRows* r) {
-  if (M < 0 || V < 1 || V > (1 << 24)) return fail(GPT_EINVAL, "bad logits shape (M >= 0, V in [1, 2^24])");
+  // rows are numbered in 32 bits, by loops that step past the last one
+  if (M < 0 || M > (1 << 30) || V < 1 || V > (1 << 24))
+    return fail(GPT_EINVAL, "bad logits shape (M in [0, 2^30], V in [1, 2^24])");
   if (dtype != GPT_DTYPE_BF16 && dtype != GPT_DTYPE_FP32)
     return fail(GPT_EINVAL, "logits must be GPT_DTYPE_BF16 or GPT_DTYPE_FP32");
   if (!scratch || (M > 0 && (!logits || !targets))) return fail(GPT_EINVAL, "null pointer");

@@ -505,7 +505,8 @@ enum { GPT_DTYPE_BF16 = 0, GPT_DTYPE_FP32 = 1 };
  * old_logp), A = advantage and d = ref_logp - lp, a position's loss is
  *   -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_coef (exp(d) - d - 1)
  * and the loss is its sum over the counted positions times weight[m].
- *   logits     [M, V] in dtype, row stride ld >= V elements; -inf allowed
+ *   logits     [M, V] in dtype, M up to 2^30, V up to 2^24, row stride ld >= V
+ *              elements; -inf allowed
  *   targets    device int32 [M]; -1: the position is not counted.  Other ids
  *              outside [0, V) are not counted either and latched as GPT_ERANGE
  *   old_logp   fp32 [M], or NULL: the present ones (r = 1, with -A as the
