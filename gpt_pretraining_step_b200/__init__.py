@@ -508,12 +508,16 @@ def _heads(name, t, shape, dev, bf16):
     return Heads(t.data_ptr(), token, head)
 
 
-def _raw_stream(torch, stream, dev, *made):
+def _raw_stream(torch, stream, dev, *made, plan=None):
     """Handle of `stream` or of the current one.  Memory of the tensors made
     for the call must not be given out again on the current stream before
-    another stream's work on it has run."""
+    another stream's work on it has run, nor the plan's on the stream that it
+    was allocated on: its buffer is not the caller's to look after."""
     current = torch._C._cuda_getCurrentRawStream(dev)
-    if stream is None or stream.cuda_stream == current:
+    raw = current if stream is None else stream.cuda_stream
+    if plan is not None and raw != plan.home:
+        plan.buf.record_stream(stream or torch.cuda.current_stream(dev))
+    if raw == current:
         return current
     for t in made:
         if t is not None:
@@ -541,6 +545,7 @@ class AttentionPlan:
             raise GptError(GPT_EINVAL, f"n_tokens must be in [0, 2^30]; got {n_tokens}")
         self.device = _current(torch, "cu_seqlens", cu_seqlens)
         self.buf = cu_seqlens.new_empty(_words("gpt_op_attention_plan_bytes", self.n_tokens), dtype=torch.int32)
+        self.home = torch._C._cuda_getCurrentRawStream(self.device)   # its memory goes back to this stream
         self.update(cu_seqlens, stream)
 
     def update(self, cu_seqlens, stream=None):
@@ -552,7 +557,7 @@ class AttentionPlan:
             _refuse("cu_seqlens", cu_seqlens, "[sequences + 1], up to 2^30 sequences")
         cu = _flat("cu_seqlens", cu_seqlens, torch.int32, (n,), self.device)
         _check(lib().gpt_op_attention_plan(cu, n - 1, self.n_tokens, self.window, self.buf.data_ptr(),
-                                           _raw_stream(torch, stream, self.device, self.buf)))
+                                           _raw_stream(torch, stream, self.device, plan=self)))
 
 
 def _planned(torch, q, plan):
@@ -587,7 +592,7 @@ def attention_packed_fwd(q, k, v, plan, scale=0.0, o=None, lse=None, stream=None
         lse = q.new_empty((H, n), dtype=f32)
     _check(lib().gpt_op_attention_packed_fwd(
         hq, hk, hv, _heads("o", o, rows, dev, bf16), _flat("lse", lse, f32, (H, n), dev), n, H, Hkv, scale,
-        plan.buf.data_ptr(), _raw_stream(torch, stream, dev, o, lse)))
+        plan.buf.data_ptr(), _raw_stream(torch, stream, dev, o, lse, plan=plan)))
     return o, lse
 
 
@@ -612,7 +617,8 @@ def attention_packed_bwd(q, k, v, o, lse, dout, plan, scale=0.0, dq=None, dk=Non
         hq, hk, hv, _heads("o", o, rows, dev, bf16), _flat("lse", lse, f32, (H, n), dev),
         _heads("dout", dout, rows, dev, bf16), _heads("dq", dq, rows, dev, bf16),
         _heads("dk", dk, kv_rows, dev, bf16), _heads("dv", dv, kv_rows, dev, bf16), n, H, Hkv, scale,
-        plan.buf.data_ptr(), scratch.data_ptr(), _raw_stream(torch, stream, dev, dq, dk, dv, scratch)))
+        plan.buf.data_ptr(), scratch.data_ptr(), _raw_stream(torch, stream, dev, dq, dk, dv, scratch,
+                                                                plan=plan)))
     return dq, dk, dv
 
 
