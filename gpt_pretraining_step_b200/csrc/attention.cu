@@ -71,6 +71,37 @@ enum { kCtlSched = 0, kCtlEntries = 1, kCtlValid = 2 };
 enum { kMetaTotal = 0, kMetaFwd = 1, kMetaBwd = 2, kMetaT = 3, kMetaMagic = 4, kPlanMeta = 64 };
 constexpr int kPlanMagic = 0x5e91a7e;
 
+// What the kernels take from a plan is bounded, and entries out of bounds are
+// left out and latched as ERRF_SHAPE: a buffer that something else has
+// overwritten must not send them out of the tensors or through 2^31 key blocks.
+struct PlanSizes {
+  bool fits;            // a plan of T positions
+  int valid, fwd, bwd;  // positions that hold sequences, entries
+};
+__device__ __forceinline__ PlanSizes plan_sizes(const int* meta, int T) {
+  PlanSizes s = {meta[kMetaMagic] == kPlanMagic && meta[kMetaT] == T, 0, 0, 0};
+  if (s.fits) {
+    s.valid = max(0, min(meta[kMetaTotal], T));
+    const int tiles = (s.valid + 127) / 128;
+    s.fwd = max(0, min(meta[kMetaFwd], tiles));
+    s.bwd = max(0, min(meta[kMetaBwd], tiles));
+  }
+  return s;
+}
+// query tile and first key block
+__device__ __forceinline__ bool fwd_entry_ok(int2 e, int valid, int* err) {
+  if (e.x >= 0 && e.x < (valid + 127) / 128 && e.y >= 0 && e.y <= e.x) return true;
+  if (err) atomicOr(err, ERRF_SHAPE);
+  return false;
+}
+// key block and number of query blocks
+__device__ __forceinline__ bool bwd_entry_ok(int2 e, int valid, int* err) {
+  const int tiles = (valid + 127) / 128;
+  if (e.x >= 0 && e.x < tiles && e.y >= 1 && e.y <= tiles - e.x) return true;
+  if (err) atomicOr(err, ERRF_SHAPE);
+  return false;
+}
+
 // The packed forward takes its items from the grid: it is launched with a
 // block for each, and a running block asks for the index of one that has not
 // started, which is then never started (cluster launch control).  So items go
@@ -741,24 +772,26 @@ __global__ void __launch_bounds__(192, 2)
   const uint32_t tmem = *tmem_holder;
   chain_wait();
   // positions that hold sequences; a plan of another T is refused
-  const bool fits = pk.meta[kMetaMagic] == kPlanMagic && pk.meta[kMetaT] == T;
-  const int Tv = fits ? pk.meta[kMetaTotal] : 0;
-  if (!fits && blockIdx.x == 0 && threadIdx.x == 0 && err) atomicOr(err, ERRF_SHAPE);
+  const PlanSizes plan = plan_sizes(pk.meta, T);
+  const int Tv = plan.valid;
+  if (!plan.fits && blockIdx.x == 0 && threadIdx.x == 0 && err) atomicOr(err, ERRF_SHAPE);
 
   if (warp == 4) {
     if (lane == 0) {
       // -------------------------------------------------------------- TMA
       // item number and fields are fetched one item ahead, so that the answer's
       // and the plan's latency hides behind the current item's loads
-      const int entries = fits ? pk.meta[kMetaFwd] : 0, n_items = entries * H;
+      const int entries = plan.fwd, n_items = entries * H;
       int nx_h = -1;
       int2 nx = make_int2(0, 0);
       bool asked = false;
       uint32_t answers = 0;
       auto fetch = [&](int idx) {   // false: a block without work (tiles past the sequences)
         if (idx >= n_items) return false;
-        nx_h = idx / entries;
-        nx = __ldg(pk.fwd + (idx - nx_h * entries));
+        const int h = idx / entries;
+        nx = __ldg(pk.fwd + (idx - h * entries));
+        if (!fwd_entry_ok(nx, Tv, err)) return false;
+        nx_h = h;
         return true;
       };
       auto take = [&] {   // false: the wait expired
@@ -1287,10 +1320,12 @@ __global__ void __launch_bounds__(512, 1)
       int nx_idx = -1, nx_hk = 0;
       int2 nx = make_int2(0, 0);
       auto take = [&] {
-        nx_idx = atomicAdd(sched, 1);
-        if (nx_idx >= n_units) { nx_idx = -1; return; }
-        nx_hk = nx_idx / entries;
-        nx = __ldg(pa.bwd + (nx_idx - nx_hk * entries));
+        do {
+          nx_idx = atomicAdd(sched, 1);
+          if (nx_idx >= n_units) { nx_idx = -1; return; }
+          nx_hk = nx_idx / entries;
+          nx = __ldg(pa.bwd + (nx_idx - nx_hk * entries));
+        } while (!bwd_entry_ok(nx, Tv, err));
       };
       if constexpr (kPacked) take();
       bool ok = true;
@@ -2133,12 +2168,12 @@ struct SetupMaps {
 __device__ __forceinline__ void packed_setup(const SetupMaps& in, CUtensorMap* out, int* ctl, const int* meta, int T,
                                              int* err, CUtensorMap* stage) {
   const int lane = lane_id();
-  const bool fits = meta[kMetaMagic] == kPlanMagic && meta[kMetaT] == T;
-  const int valid = fits ? meta[kMetaTotal] : 0;
+  const PlanSizes plan = plan_sizes(meta, T);
+  const int valid = plan.valid;
   if (lane == 0) {
-    if (!fits && err) atomicOr(err, ERRF_SHAPE);
+    if (!plan.fits && err) atomicOr(err, ERRF_SHAPE);
     ctl[kCtlSched] = 0;
-    ctl[kCtlEntries] = fits ? meta[kMetaBwd] : 0;
+    ctl[kCtlEntries] = plan.bwd;
     ctl[kCtlValid] = valid;
   }
   for (int i = 0; i < 4; ++i)
@@ -2259,8 +2294,8 @@ __global__ void __launch_bounds__(608, 1)
   const uint32_t tmem = *tmem_holder;
   chain_wait();
   // positions that hold sequences; a plan of another T is refused (by the setup)
-  const bool fits = pk.meta[kMetaMagic] == kPlanMagic && pk.meta[kMetaT] == T;
-  const int Tv = fits ? pk.meta[kMetaTotal] : 0;
+  const PlanSizes plan = plan_sizes(pk.meta, T);
+  const int Tv = plan.valid;
 
   if (warp == 18) {
     packed_setup(in, maps, ctl, pk.meta, T, err, stage);
@@ -2268,15 +2303,17 @@ __global__ void __launch_bounds__(608, 1)
     if (lane == 0) {
       // -------------------------------------------------------------- TMA
       // item number and fields are fetched one item ahead, as in the forward
-      const int entries = fits ? pk.meta[kMetaFwd] : 0, n_items = entries * H;
+      const int entries = plan.fwd, n_items = entries * H;
       int nx_h = -1;
       int2 nx = make_int2(0, 0);
       bool asked = false;
       uint32_t answers = 0;
       auto fetch = [&](int idx) {   // false: a block without work (tiles past the sequences)
         if (idx >= n_items) return false;
-        nx_h = idx / entries;
-        nx = __ldg(pk.fwd + (idx - nx_h * entries));
+        const int h = idx / entries;
+        nx = __ldg(pk.fwd + (idx - h * entries));
+        if (!fwd_entry_ok(nx, Tv, err)) return false;
+        nx_h = h;
         return true;
       };
       auto take = [&] {   // false: the wait expired
