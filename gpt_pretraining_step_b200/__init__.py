@@ -508,21 +508,51 @@ def _heads(name, t, shape, dev, bf16):
     return Heads(t.data_ptr(), token, head)
 
 
-def _raw_stream(torch, stream, dev, *made, plan=None):
-    """Handle of `stream` or of the current one.  Memory of the tensors made
-    for the call must not be given out again on the current stream before
-    another stream's work on it has run, nor the plan's on the stream that it
-    was allocated on: its buffer is not the caller's to look after."""
-    current = torch._C._cuda_getCurrentRawStream(dev)
-    raw = current if stream is None else stream.cuda_stream
-    if plan is not None and raw != plan.home:
-        plan.buf.record_stream(stream or torch.cuda.current_stream(dev))
-    if raw == current:
-        return current
-    for t in made:
-        if t is not None:
-            t.record_stream(stream)
-    return stream.cuda_stream
+class _Run:
+    """Where a call runs: on `stream`, or on the current one if that is None.
+
+    What the call allocates comes from the pool of the stream that it runs on: of
+    another pool it could be a block whose freed tensor that stream still uses.
+    Run on a stream other than the current one, every tensor of the call is then
+    recorded on both, so that memory dropped on either side is not given out
+    again before the other's queued work on it has run.  The order of the two
+    streams' work is the caller's: `stream` has to wait for the inputs, the
+    current stream for the results."""
+
+    __slots__ = ("raw", "stream", "caller", "context")
+
+    def __init__(self, torch, stream, dev):
+        current = torch._C._cuda_getCurrentRawStream(dev)
+        self.caller = None
+        if stream is None or stream.cuda_stream == current:
+            self.raw = current
+            return
+        if stream.device.index != dev:
+            raise GptError(GPT_EINVAL, f"stream is on {stream.device}, the tensors on cuda:{dev}")
+        self.raw, self.stream, self.caller = stream.cuda_stream, stream, torch.cuda.current_stream(dev)
+        self.context = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.caller is not None:
+            self.context.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.caller is not None:
+            self.context.__exit__(*exc)
+
+    def share(self, *tensors):
+        if self.caller is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+                    t.record_stream(self.caller)
+
+    def plan(self, torch, plan):
+        """Raw handle; the buffer of a plan is not the caller's to look after."""
+        if self.raw != plan.home:
+            plan.buf.record_stream(torch.cuda.current_stream(plan.device) if self.caller is None else self.stream)
+        return self.raw
 
 
 _INT_MAX = 2 ** 31 - 1
@@ -544,8 +574,9 @@ class AttentionPlan:
         if not 0 <= self.n_tokens <= _INT_MAX:
             raise GptError(GPT_EINVAL, f"n_tokens must be in [0, 2^30]; got {n_tokens}")
         self.device = _current(torch, "cu_seqlens", cu_seqlens)
-        self.buf = cu_seqlens.new_empty(_words("gpt_op_attention_plan_bytes", self.n_tokens), dtype=torch.int32)
-        self.home = torch._C._cuda_getCurrentRawStream(self.device)   # its memory goes back to this stream
+        with _Run(torch, stream, self.device) as run:
+            self.buf = cu_seqlens.new_empty(_words("gpt_op_attention_plan_bytes", self.n_tokens), dtype=torch.int32)
+            self.home = run.raw   # its memory goes back to this stream
         self.update(cu_seqlens, stream)
 
     def update(self, cu_seqlens, stream=None):
@@ -556,8 +587,10 @@ class AttentionPlan:
         if not 1 <= n <= _INT_MAX:
             _refuse("cu_seqlens", cu_seqlens, "[sequences + 1], up to 2^30 sequences")
         cu = _flat("cu_seqlens", cu_seqlens, torch.int32, (n,), self.device)
+        run = _Run(torch, stream, self.device)
         _check(lib().gpt_op_attention_plan(cu, n - 1, self.n_tokens, self.window, self.buf.data_ptr(),
-                                           _raw_stream(torch, stream, self.device, plan=self)))
+                                           run.plan(torch, self)))
+        run.share(cu_seqlens)
 
 
 def _planned(torch, q, plan):
@@ -586,13 +619,15 @@ def attention_packed_fwd(q, k, v, plan, scale=0.0, o=None, lse=None, stream=None
     rows, kv_rows = (n, H, 128), (n, Hkv, 128)
     hq, hk, hv = (_heads("q", q, rows, dev, bf16), _heads("k", k, kv_rows, dev, bf16),
                   _heads("v", v, kv_rows, dev, bf16))
-    if o is None:
-        o = q.new_empty(rows)
-    if lse is None:
-        lse = q.new_empty((H, n), dtype=f32)
-    _check(lib().gpt_op_attention_packed_fwd(
-        hq, hk, hv, _heads("o", o, rows, dev, bf16), _flat("lse", lse, f32, (H, n), dev), n, H, Hkv, scale,
-        plan.buf.data_ptr(), _raw_stream(torch, stream, dev, o, lse, plan=plan)))
+    with _Run(torch, stream, dev) as run:
+        if o is None:
+            o = q.new_empty(rows)
+        if lse is None:
+            lse = q.new_empty((H, n), dtype=f32)
+        _check(lib().gpt_op_attention_packed_fwd(
+            hq, hk, hv, _heads("o", o, rows, dev, bf16), _flat("lse", lse, f32, (H, n), dev), n, H, Hkv, scale,
+            plan.buf.data_ptr(), run.plan(torch, plan)))
+        run.share(q, k, v, o, lse)
     return o, lse
 
 
@@ -606,19 +641,20 @@ def attention_packed_bwd(q, k, v, o, lse, dout, plan, scale=0.0, dq=None, dk=Non
     rows, kv_rows = (n, H, 128), (n, Hkv, 128)
     hq, hk, hv = (_heads("q", q, rows, dev, bf16), _heads("k", k, kv_rows, dev, bf16),
                   _heads("v", v, kv_rows, dev, bf16))
-    if dq is None:
-        dq = q.new_empty(rows)
-    if dk is None:
-        dk = q.new_empty(kv_rows)
-    if dv is None:
-        dv = q.new_empty(kv_rows)
-    scratch = q.new_empty(_words("gpt_op_attention_packed_bwd_scratch", n, H), dtype=f32)
-    _check(lib().gpt_op_attention_packed_bwd(
-        hq, hk, hv, _heads("o", o, rows, dev, bf16), _flat("lse", lse, f32, (H, n), dev),
-        _heads("dout", dout, rows, dev, bf16), _heads("dq", dq, rows, dev, bf16),
-        _heads("dk", dk, kv_rows, dev, bf16), _heads("dv", dv, kv_rows, dev, bf16), n, H, Hkv, scale,
-        plan.buf.data_ptr(), scratch.data_ptr(), _raw_stream(torch, stream, dev, dq, dk, dv, scratch,
-                                                                plan=plan)))
+    with _Run(torch, stream, dev) as run:
+        if dq is None:
+            dq = q.new_empty(rows)
+        if dk is None:
+            dk = q.new_empty(kv_rows)
+        if dv is None:
+            dv = q.new_empty(kv_rows)
+        scratch = q.new_empty(_words("gpt_op_attention_packed_bwd_scratch", n, H), dtype=f32)
+        _check(lib().gpt_op_attention_packed_bwd(
+            hq, hk, hv, _heads("o", o, rows, dev, bf16), _flat("lse", lse, f32, (H, n), dev),
+            _heads("dout", dout, rows, dev, bf16), _heads("dq", dq, rows, dev, bf16),
+            _heads("dk", dk, kv_rows, dev, bf16), _heads("dv", dv, kv_rows, dev, bf16), n, H, Hkv, scale,
+            plan.buf.data_ptr(), scratch.data_ptr(), run.plan(torch, plan)))
+        run.share(q, k, v, lse, dout, dq, dk, dv)
     return dq, dk, dv
 
 
@@ -632,10 +668,9 @@ def _rows(name, t, dev):
     return row if M > 1 else max(row, V)
 
 
-def _loss_rows(torch, logits, grad, dlogits):
+def _loss_rows(torch, logits, grad, dlogits, dev):
     """(M, V, dtype code, row stride, gradient or None, its address and row
-    stride, device) of both losses."""
-    dev = _current(torch, "logits", logits)
+    stride) of both losses."""
     ld = _rows("logits", logits, dev)
     M, V = logits.shape
     if M > _INT_MAX or V > _INT_MAX:
@@ -645,7 +680,7 @@ def _loss_rows(torch, logits, grad, dlogits):
     if code == DTYPE_FP32 and dtype != torch.float32:
         _refuse("logits", logits, "bf16 or fp32")
     if not grad:
-        return M, V, code, ld, None, None, ld, dev
+        return M, V, code, ld, None, None, ld
     ld_d = ld
     if dlogits is None:
         # rows aligned to 16 bytes as the logits' are, without their gaps
@@ -655,7 +690,7 @@ def _loss_rows(torch, logits, grad, dlogits):
         ld_d = _rows("dlogits", dlogits, dev)
         if dlogits.shape != logits.shape or dlogits.dtype != dtype:
             _refuse("dlogits", dlogits, f"{dtype} {(M, V)}")
-    return M, V, code, ld, dlogits, dlogits.data_ptr(), ld_d, dev
+    return M, V, code, ld, dlogits, dlogits.data_ptr(), ld_d
 
 
 def policy_loss(logits, targets, old_logp, advantage, weight, ref_logp=None, kl_coef=0.0, clip_low=0.2,
@@ -669,17 +704,20 @@ def policy_loss(logits, targets, old_logp, advantage, weight, ref_logp=None, kl_
     and of the clipped positions; dlogits (None with grad=False) is new unless
     given, and may be logits itself."""
     import torch
-    M, V, code, ld, dlogits, d, ld_d, dev = _loss_rows(torch, logits, grad, dlogits)
-    f32, shape = torch.float32, (M,)
-    args = (_flat("targets", targets, torch.int32, shape, dev),
-            None if old_logp is None else _flat("old_logp", old_logp, f32, shape, dev),
-            None if ref_logp is None else _flat("ref_logp", ref_logp, f32, shape, dev),
-            _flat("advantage", advantage, f32, shape, dev), _flat("weight", weight, f32, shape, dev))
-    stats, logp = weight.new_empty(4), weight.new_empty(M)
-    scratch = weight.new_empty(_words("gpt_op_policy_loss_scratch", M))
-    _check(lib().gpt_op_policy_loss(
-        logits.data_ptr(), code, ld, *args, M, V, clip_low, clip_high, kl_coef, stats.data_ptr(), logp.data_ptr(), d,
-        ld_d, scratch.data_ptr(), _raw_stream(torch, stream, dev, stats, logp, scratch, dlogits)))
+    dev = _current(torch, "logits", logits)
+    with _Run(torch, stream, dev) as run:
+        M, V, code, ld, dlogits, d, ld_d = _loss_rows(torch, logits, grad, dlogits, dev)
+        f32, shape = torch.float32, (M,)
+        args = (_flat("targets", targets, torch.int32, shape, dev),
+                None if old_logp is None else _flat("old_logp", old_logp, f32, shape, dev),
+                None if ref_logp is None else _flat("ref_logp", ref_logp, f32, shape, dev),
+                _flat("advantage", advantage, f32, shape, dev), _flat("weight", weight, f32, shape, dev))
+        stats, logp = weight.new_empty(4), weight.new_empty(M)
+        scratch = weight.new_empty(_words("gpt_op_policy_loss_scratch", M))
+        _check(lib().gpt_op_policy_loss(
+            logits.data_ptr(), code, ld, *args, M, V, clip_low, clip_high, kl_coef, stats.data_ptr(), logp.data_ptr(),
+            d, ld_d, scratch.data_ptr(), run.raw))
+        run.share(logits, targets, old_logp, ref_logp, advantage, weight, stats, logp, dlogits)
     return stats, logp, dlogits
 
 
@@ -696,19 +734,22 @@ def preference_loss(logits, targets, cu_seqlens, ref_logp=None, beta=0.1, label_
     import torch
     if clear_past is None:
         clear_past = dlogits is None
-    M, V, code, ld, dlogits, d, ld_d, dev = _loss_rows(torch, logits, grad, dlogits)
-    n, f32, i32 = cu_seqlens.numel() - 1, torch.float32, torch.int32
-    if n < 2 or n % 2 or n > _INT_MAX:
-        _refuse("cu_seqlens", cu_seqlens, "[2 * pairs + 1]")
-    y, cu = _flat("targets", targets, i32, (M,), dev), _flat("cu_seqlens", cu_seqlens, i32, (n + 1,), dev)
-    ref = None if ref_logp is None else _flat("ref_logp", ref_logp, f32, (n,), dev)
-    loss, margin = logits.new_empty((), dtype=f32), logits.new_empty(n // 2, dtype=f32)
-    seq_logp, logp = logits.new_empty(n, dtype=f32), logits.new_empty(M, dtype=f32)
-    scratch = targets.new_empty(_words("gpt_op_preference_loss_scratch", M, n // 2))
-    _check(lib().gpt_op_preference_loss_ex(
-        logits.data_ptr(), code, ld, y, cu, n // 2, ref, M, V, beta, label_smoothing, loss.data_ptr(),
-        margin.data_ptr(), seq_logp.data_ptr(), logp.data_ptr(), d, ld_d, bool(clear_past), scratch.data_ptr(),
-        _raw_stream(torch, stream, dev, loss, margin, seq_logp, logp, scratch, dlogits)))
+    dev = _current(torch, "logits", logits)
+    with _Run(torch, stream, dev) as run:
+        M, V, code, ld, dlogits, d, ld_d = _loss_rows(torch, logits, grad, dlogits, dev)
+        n, f32, i32 = cu_seqlens.numel() - 1, torch.float32, torch.int32
+        if n < 2 or n % 2 or n > _INT_MAX:
+            _refuse("cu_seqlens", cu_seqlens, "[2 * pairs + 1]")
+        y, cu = _flat("targets", targets, i32, (M,), dev), _flat("cu_seqlens", cu_seqlens, i32, (n + 1,), dev)
+        ref = None if ref_logp is None else _flat("ref_logp", ref_logp, f32, (n,), dev)
+        loss, margin = logits.new_empty((), dtype=f32), logits.new_empty(n // 2, dtype=f32)
+        seq_logp, logp = logits.new_empty(n, dtype=f32), logits.new_empty(M, dtype=f32)
+        scratch = targets.new_empty(_words("gpt_op_preference_loss_scratch", M, n // 2))
+        _check(lib().gpt_op_preference_loss_ex(
+            logits.data_ptr(), code, ld, y, cu, n // 2, ref, M, V, beta, label_smoothing, loss.data_ptr(),
+            margin.data_ptr(), seq_logp.data_ptr(), logp.data_ptr(), d, ld_d, bool(clear_past), scratch.data_ptr(),
+            run.raw))
+        run.share(logits, targets, cu_seqlens, ref_logp, loss, margin, seq_logp, logp, dlogits)
     return loss, margin, seq_logp, logp, dlogits
 
 

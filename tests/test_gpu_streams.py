@@ -87,3 +87,75 @@ def test_entries_out_of_bounds_are_left_out(torch):
     o2, lse2 = g.attention_packed_fwd(q, k, v, plan)
     g.op_check()
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def loss_inputs(torch):
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn((40, 3000), generator=g, device="cuda").bfloat16()
+    y = torch.randint(0, 3000, (40,), generator=g, device="cuda").to(torch.int32)
+    return x, y, torch.randn(40, device="cuda"), torch.tensor([0, 10, 40], dtype=torch.int32, device="cuda")
+
+
+def home(torch, t):
+    """The stream whose pool a tensor's memory is from."""
+    at = t.untyped_storage().data_ptr()
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= at < s["address"] + s["total_size"]:
+            return s["stream"]
+    raise AssertionError("not the allocator's")
+
+
+def test_new_memory_is_of_the_stream_that_the_call_runs_on(torch):
+    """A block of another stream's pool may still be in use there."""
+    import gpt_pretraining_step_b200 as g
+    q, k, v, do, cu = packed(torch)
+    x, y, a, pairs = loss_inputs(torch)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def calls(stream):
+        plan = g.attention_plan(cu, 300, stream=stream)
+        o, lse = g.attention_packed_fwd(q, k, v, plan, stream=stream)
+        grads = g.attention_packed_bwd(q, k, v, o, lse, do, plan, stream=stream)
+        return [plan.buf, o, lse, *grads, *g.policy_loss(x, y, None, a, a, stream=stream),
+                *g.preference_loss(x, y, pairs, stream=stream)]
+
+    here, there = calls(None), calls(side)
+    assert all(home(torch, t) == torch.cuda.current_stream().cuda_stream for t in here)
+    assert all(home(torch, t) == side.cuda_stream for t in there)
+    assert torch.cuda.current_stream().cuda_stream != side.cuda_stream
+    torch.cuda.current_stream().wait_stream(side)
+    for i, (s, t) in enumerate(zip(here, there)):
+        assert i in (0, 3) or torch.equal(s, t), i      # a plan's order of equal entries and dq's sums vary
+    g.op_check()
+
+
+def test_every_tensor_of_a_call_is_recorded_on_both_streams(torch, monkeypatch):
+    import gpt_pretraining_step_b200 as g
+    q, k, v, do, cu = packed(torch)
+    x, y, a, pairs = loss_inputs(torch)
+    side, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    side.wait_stream(here)
+    noted = {}
+
+    def note(t, s):
+        noted.setdefault(t.data_ptr(), set()).add(s.cuda_stream)
+        plain(t, s)
+
+    plain = torch.Tensor.record_stream
+    monkeypatch.setattr(torch.Tensor, "record_stream", note)
+    plan = g.attention_plan(cu, 300, stream=side)
+    o, lse = g.attention_packed_fwd(q, k, v, plan, stream=side)
+    grads = g.attention_packed_bwd(q, k, v, o, lse, do, plan, stream=side)
+    out = [*g.policy_loss(x, y, a, a, a, ref_logp=a, stream=side), *g.preference_loss(x, y, pairs, stream=side)]
+    both = {side.cuda_stream, here.cuda_stream}
+    for t in [q, k, v, do, cu, o, lse, *grads, x, y, a, pairs, *out]:
+        assert noted[t.data_ptr()] == both
+    torch.cuda.synchronize()
+    # nothing is recorded where there is one stream alone
+    noted.clear()
+    plan = g.attention_plan(cu, 300)
+    g.attention_packed_fwd(q, k, v, plan)
+    g.policy_loss(x, y, a, a, a)
+    assert not noted
+    g.op_check()
