@@ -601,6 +601,14 @@ def _planned(torch, q, plan):
     return dev
 
 
+def _head_counts(q, k):
+    if q.dim() != 3:
+        _refuse("q", q, "[n_tokens, heads, 128]")
+    if k.dim() != 3:
+        _refuse("k", k, "[n_tokens, kv heads, 128]")
+    return q.shape[1], k.shape[1]
+
+
 def attention_plan(cu_seqlens, n_tokens, window=-1, stream=None):
     """Plan of the sequences cu_seqlens (int32 [n + 1], on the device) packed
     into n_tokens positions, for attention_packed_fwd and _bwd."""
@@ -615,7 +623,7 @@ def attention_packed_fwd(q, k, v, plan, scale=0.0, o=None, lse=None, stream=None
     they held (new tensors: anything)."""
     import torch
     n, dev, bf16, f32 = plan.n_tokens, _planned(torch, q, plan), torch.bfloat16, torch.float32
-    H, Hkv = q.shape[1], k.shape[1]
+    H, Hkv = _head_counts(q, k)
     rows, kv_rows = (n, H, 128), (n, Hkv, 128)
     hq, hk, hv = (_heads("q", q, rows, dev, bf16), _heads("k", k, kv_rows, dev, bf16),
                   _heads("v", v, kv_rows, dev, bf16))
@@ -637,7 +645,7 @@ def attention_packed_bwd(q, k, v, o, lse, dout, plan, scale=0.0, dq=None, dk=Non
     checked but not read: gpt_op_attention_packed_bwd)."""
     import torch
     n, dev, bf16, f32 = plan.n_tokens, _planned(torch, q, plan), torch.bfloat16, torch.float32
-    H, Hkv = q.shape[1], k.shape[1]
+    H, Hkv = _head_counts(q, k)
     rows, kv_rows = (n, H, 128), (n, Hkv, 128)
     hq, hk, hv = (_heads("q", q, rows, dev, bf16), _heads("k", k, kv_rows, dev, bf16),
                   _heads("v", v, kv_rows, dev, bf16))
