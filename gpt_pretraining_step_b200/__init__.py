@@ -36,7 +36,7 @@ ABI_FUNCTIONS = [
     "gpt_op_attention_plan_bytes", "gpt_op_attention_plan", "gpt_op_attention_packed_fwd",
     "gpt_op_attention_packed_bwd_scratch", "gpt_op_attention_packed_bwd", "gpt_op_policy_loss_scratch",
     "gpt_op_policy_loss", "gpt_op_preference_loss_scratch", "gpt_op_preference_loss",
-    "gpt_op_preference_loss_ex",
+    "gpt_op_preference_loss_ex", "gpt_op_attention_packed_fwd_ex", "gpt_op_attention_packed_bwd_ex",
 ]
 DTYPE_BF16, DTYPE_FP32 = 0, 1
 GRAD_BUCKETS = 6
@@ -133,6 +133,9 @@ def lib():
             "gpt_op_attention_packed_fwd": (i32, [hp, hp, hp, hp, vp, i32, i32, i32, f32, vp, vp]),
             "gpt_op_attention_packed_bwd": (i32, [hp, hp, hp, hp, vp, hp, hp, hp, hp, i32, i32, i32, f32, vp, vp,
                                                   vp]),
+            "gpt_op_attention_packed_fwd_ex": (i32, [hp, hp, hp, hp, vp, i32, i32, i32, f32, vp, i32, vp]),
+            "gpt_op_attention_packed_bwd_ex": (i32, [hp, hp, hp, hp, vp, hp, hp, hp, hp, i32, i32, i32, f32, vp, i32,
+                                                     vp, vp]),
             "gpt_op_policy_loss_scratch": (sz, [i32]),
             "gpt_op_policy_loss": (i32, [vp, i32, i64, vp, vp, vp, vp, vp, i32, i32, f32, f32, f32, vp, vp, vp, i64,
                                          vp, vp]),
@@ -508,51 +511,34 @@ def _heads(name, t, shape, dev, bf16):
     return Heads(t.data_ptr(), token, head)
 
 
-class _Run:
-    """Where a call runs: on `stream`, or on the current one if that is None.
+def _on(stream, call, *args, **kw):
+    """call(*args, **kw) with `stream` as the current one.
 
-    What the call allocates comes from the pool of the stream that it runs on: of
-    another pool it could be a block whose freed tensor that stream still uses.
-    Run on a stream other than the current one, every tensor of the call is then
-    recorded on both, so that memory dropped on either side is not given out
-    again before the other's queued work on it has run.  The order of the two
-    streams' work is the caller's: `stream` has to wait for the inputs, the
-    current stream for the results."""
+    What the call allocates then comes from the pool of the stream that it runs
+    on: of another pool it could be a block whose freed tensor that stream still
+    uses.  Every tensor of the call is recorded on both streams, so that memory
+    dropped on either side is not given out again before the other's queued
+    work on it has run.  The order of the two streams' work is the caller's:
+    `stream` has to wait for the inputs, the current stream for the results."""
+    import torch
+    caller = torch.cuda.current_stream()
+    if stream.device != caller.device:
+        raise GptError(GPT_EINVAL, f"stream is on {stream.device}, the current one on {caller.device}")
+    with torch.cuda.stream(stream):
+        out = call(*args, **kw)
+    for t in (*args, *kw.values(), *(out or ())):
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
+            t.record_stream(caller)
+    return out
 
-    __slots__ = ("raw", "stream", "caller", "context")
 
-    def __init__(self, torch, stream, dev):
-        current = torch._C._cuda_getCurrentRawStream(dev)
-        self.caller = None
-        if stream is None or stream.cuda_stream == current:
-            self.raw = current
-            return
-        if stream.device.index != dev:
-            raise GptError(GPT_EINVAL, f"stream is on {stream.device}, the tensors on cuda:{dev}")
-        self.raw, self.stream, self.caller = stream.cuda_stream, stream, torch.cuda.current_stream(dev)
-        self.context = torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.caller is not None:
-            self.context.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.caller is not None:
-            self.context.__exit__(*exc)
-
-    def share(self, *tensors):
-        if self.caller is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
-                    t.record_stream(self.caller)
-
-    def plan(self, torch, plan):
-        """Raw handle; the buffer of a plan is not the caller's to look after."""
-        if self.raw != plan.home:
-            plan.buf.record_stream(torch.cuda.current_stream(plan.device) if self.caller is None else self.stream)
-        return self.raw
+def _plan_stream(torch, plan):
+    """Handle of the current stream.  The buffer of a plan is not the caller's to look after."""
+    raw = torch._C._cuda_getCurrentRawStream(plan.device)
+    if raw != plan.home:
+        plan.buf.record_stream(torch.cuda.current_stream(plan.device))
+    return raw
 
 
 _INT_MAX = 2 ** 31 - 1
@@ -574,23 +560,29 @@ class AttentionPlan:
         if not 0 <= self.n_tokens <= _INT_MAX:
             raise GptError(GPT_EINVAL, f"n_tokens must be in [0, 2^30]; got {n_tokens}")
         self.device = _current(torch, "cu_seqlens", cu_seqlens)
-        with _Run(torch, stream, self.device) as run:
-            self.buf = cu_seqlens.new_empty(_words("gpt_op_attention_plan_bytes", self.n_tokens), dtype=torch.int32)
-            self.home = run.raw   # its memory goes back to this stream
+        if stream is None:
+            self._allocate(torch, cu_seqlens)
+        else:
+            with torch.cuda.stream(stream):
+                self._allocate(torch, cu_seqlens)
         self.update(cu_seqlens, stream)
+
+    def _allocate(self, torch, like):
+        self.buf = like.new_empty(_words("gpt_op_attention_plan_bytes", self.n_tokens), dtype=torch.int32)
+        self.home = torch._C._cuda_getCurrentRawStream(self.device)   # its memory goes back to this stream
 
     def update(self, cu_seqlens, stream=None):
         """Plan another batch of the same n_tokens and window into the same buffer."""
+        if stream is not None:
+            return _on(stream, self.update, cu_seqlens)
         import torch
         _current(torch, "cu_seqlens", cu_seqlens)
         n = cu_seqlens.numel()
         if not 1 <= n <= _INT_MAX:
             _refuse("cu_seqlens", cu_seqlens, "[sequences + 1], up to 2^30 sequences")
         cu = _flat("cu_seqlens", cu_seqlens, torch.int32, (n,), self.device)
-        run = _Run(torch, stream, self.device)
         _check(lib().gpt_op_attention_plan(cu, n - 1, self.n_tokens, self.window, self.buf.data_ptr(),
-                                           run.plan(torch, self)))
-        run.share(cu_seqlens)
+                                           _plan_stream(torch, self)))
 
 
 def _planned(torch, q, plan):
@@ -615,54 +607,60 @@ def attention_plan(cu_seqlens, n_tokens, window=-1, stream=None):
     return AttentionPlan(cu_seqlens, n_tokens, window, stream)
 
 
-def attention_packed_fwd(q, k, v, plan, scale=0.0, o=None, lse=None, stream=None):
+def attention_packed_fwd(q, k, v, plan, scale=0.0, o=None, lse=None, stream=None, clear_past=None):
     """Causal attention of each sequence of the plan.  q [n_tokens, H, 128], k
     and v [n_tokens, Hkv, 128] bf16 with any token and head strides (multiples
     of 8); scale 0 is 1 / sqrt(128).  Returns o [n_tokens, H, 128] and lse
-    [H, n_tokens], new unless given; rows past the last sequence keep what
-    they held (new tensors: anything)."""
+    [H, n_tokens], new unless given.  Rows past the last sequence hold zeros in
+    new outputs and keep what they held in given ones; clear_past True or False
+    says either of both."""
+    if stream is not None:
+        return _on(stream, attention_packed_fwd, q, k, v, plan, scale, o, lse, clear_past=clear_past)
     import torch
+    clear = (o is None) + 2 * (lse is None) if clear_past is None else 3 * bool(clear_past)   # GPT_CLEAR_*
     n, dev, bf16, f32 = plan.n_tokens, _planned(torch, q, plan), torch.bfloat16, torch.float32
     H, Hkv = _head_counts(q, k)
     rows, kv_rows = (n, H, 128), (n, Hkv, 128)
     hq, hk, hv = (_heads("q", q, rows, dev, bf16), _heads("k", k, kv_rows, dev, bf16),
                   _heads("v", v, kv_rows, dev, bf16))
-    with _Run(torch, stream, dev) as run:
-        if o is None:
-            o = q.new_empty(rows)
-        if lse is None:
-            lse = q.new_empty((H, n), dtype=f32)
-        _check(lib().gpt_op_attention_packed_fwd(
-            hq, hk, hv, _heads("o", o, rows, dev, bf16), _flat("lse", lse, f32, (H, n), dev), n, H, Hkv, scale,
-            plan.buf.data_ptr(), run.plan(torch, plan)))
-        run.share(q, k, v, o, lse)
+    if o is None:
+        o = q.new_empty(rows)
+    if lse is None:
+        lse = q.new_empty((H, n), dtype=f32)
+    _check(lib().gpt_op_attention_packed_fwd_ex(
+        hq, hk, hv, _heads("o", o, rows, dev, bf16), _flat("lse", lse, f32, (H, n), dev), n, H, Hkv, scale,
+        plan.buf.data_ptr(), clear, _plan_stream(torch, plan)))
     return o, lse
 
 
-def attention_packed_bwd(q, k, v, o, lse, dout, plan, scale=0.0, dq=None, dk=None, dv=None, stream=None):
+def attention_packed_bwd(q, k, v, o, lse, dout, plan, scale=0.0, dq=None, dk=None, dv=None, stream=None,
+                         clear_past=None):
     """Gradients (bf16, shaped as q, k and v; new unless given) of
     attention_packed_fwd, from its lse and the gradient dout of o (o itself is
-    checked but not read: gpt_op_attention_packed_bwd)."""
+    checked but not read: gpt_op_attention_packed_bwd).  Rows past the last
+    sequence and clear_past as in the forward."""
+    if stream is not None:
+        return _on(stream, attention_packed_bwd, q, k, v, o, lse, dout, plan, scale, dq, dk, dv, clear_past=clear_past)
     import torch
+    clear = ((dq is None) + 2 * (dk is None) + 4 * (dv is None) if clear_past is None
+             else 7 * bool(clear_past))   # GPT_CLEAR_*
     n, dev, bf16, f32 = plan.n_tokens, _planned(torch, q, plan), torch.bfloat16, torch.float32
     H, Hkv = _head_counts(q, k)
     rows, kv_rows = (n, H, 128), (n, Hkv, 128)
     hq, hk, hv = (_heads("q", q, rows, dev, bf16), _heads("k", k, kv_rows, dev, bf16),
                   _heads("v", v, kv_rows, dev, bf16))
-    with _Run(torch, stream, dev) as run:
-        if dq is None:
-            dq = q.new_empty(rows)
-        if dk is None:
-            dk = q.new_empty(kv_rows)
-        if dv is None:
-            dv = q.new_empty(kv_rows)
-        scratch = q.new_empty(_words("gpt_op_attention_packed_bwd_scratch", n, H), dtype=f32)
-        _check(lib().gpt_op_attention_packed_bwd(
-            hq, hk, hv, _heads("o", o, rows, dev, bf16), _flat("lse", lse, f32, (H, n), dev),
-            _heads("dout", dout, rows, dev, bf16), _heads("dq", dq, rows, dev, bf16),
-            _heads("dk", dk, kv_rows, dev, bf16), _heads("dv", dv, kv_rows, dev, bf16), n, H, Hkv, scale,
-            plan.buf.data_ptr(), scratch.data_ptr(), run.plan(torch, plan)))
-        run.share(q, k, v, lse, dout, dq, dk, dv)
+    if dq is None:
+        dq = q.new_empty(rows)
+    if dk is None:
+        dk = q.new_empty(kv_rows)
+    if dv is None:
+        dv = q.new_empty(kv_rows)
+    scratch = q.new_empty(_words("gpt_op_attention_packed_bwd_scratch", n, H), dtype=f32)
+    _check(lib().gpt_op_attention_packed_bwd_ex(
+        hq, hk, hv, _heads("o", o, rows, dev, bf16), _flat("lse", lse, f32, (H, n), dev),
+        _heads("dout", dout, rows, dev, bf16), _heads("dq", dq, rows, dev, bf16),
+        _heads("dk", dk, kv_rows, dev, bf16), _heads("dv", dv, kv_rows, dev, bf16), n, H, Hkv, scale,
+        plan.buf.data_ptr(), clear, scratch.data_ptr(), _plan_stream(torch, plan)))
     return dq, dk, dv
 
 
@@ -676,9 +674,10 @@ def _rows(name, t, dev):
     return row if M > 1 else max(row, V)
 
 
-def _loss_rows(torch, logits, grad, dlogits, dev):
+def _loss_rows(torch, logits, grad, dlogits):
     """(M, V, dtype code, row stride, gradient or None, its address and row
-    stride) of both losses."""
+    stride, device) of both losses."""
+    dev = _current(torch, "logits", logits)
     ld = _rows("logits", logits, dev)
     M, V = logits.shape
     if M > _INT_MAX or V > _INT_MAX:
@@ -688,7 +687,7 @@ def _loss_rows(torch, logits, grad, dlogits, dev):
     if code == DTYPE_FP32 and dtype != torch.float32:
         _refuse("logits", logits, "bf16 or fp32")
     if not grad:
-        return M, V, code, ld, None, None, ld
+        return M, V, code, ld, None, None, ld, dev
     ld_d = ld
     if dlogits is None:
         # rows aligned to 16 bytes as the logits' are, without their gaps
@@ -698,7 +697,7 @@ def _loss_rows(torch, logits, grad, dlogits, dev):
         ld_d = _rows("dlogits", dlogits, dev)
         if dlogits.shape != logits.shape or dlogits.dtype != dtype:
             _refuse("dlogits", dlogits, f"{dtype} {(M, V)}")
-    return M, V, code, ld, dlogits, dlogits.data_ptr(), ld_d
+    return M, V, code, ld, dlogits, dlogits.data_ptr(), ld_d, dev
 
 
 def policy_loss(logits, targets, old_logp, advantage, weight, ref_logp=None, kl_coef=0.0, clip_low=0.2,
@@ -711,21 +710,21 @@ def policy_loss(logits, targets, old_logp, advantage, weight, ref_logp=None, kl_
     loss and the weighted sums of the clipped surrogate, of the KL estimate
     and of the clipped positions; dlogits (None with grad=False) is new unless
     given, and may be logits itself."""
+    if stream is not None:
+        return _on(stream, policy_loss, logits, targets, old_logp, advantage, weight, ref_logp, kl_coef, clip_low,
+                   clip_high, grad, dlogits)
     import torch
-    dev = _current(torch, "logits", logits)
-    with _Run(torch, stream, dev) as run:
-        M, V, code, ld, dlogits, d, ld_d = _loss_rows(torch, logits, grad, dlogits, dev)
-        f32, shape = torch.float32, (M,)
-        args = (_flat("targets", targets, torch.int32, shape, dev),
-                None if old_logp is None else _flat("old_logp", old_logp, f32, shape, dev),
-                None if ref_logp is None else _flat("ref_logp", ref_logp, f32, shape, dev),
-                _flat("advantage", advantage, f32, shape, dev), _flat("weight", weight, f32, shape, dev))
-        stats, logp = weight.new_empty(4), weight.new_empty(M)
-        scratch = weight.new_empty(_words("gpt_op_policy_loss_scratch", M))
-        _check(lib().gpt_op_policy_loss(
-            logits.data_ptr(), code, ld, *args, M, V, clip_low, clip_high, kl_coef, stats.data_ptr(), logp.data_ptr(),
-            d, ld_d, scratch.data_ptr(), run.raw))
-        run.share(logits, targets, old_logp, ref_logp, advantage, weight, stats, logp, dlogits)
+    M, V, code, ld, dlogits, d, ld_d, dev = _loss_rows(torch, logits, grad, dlogits)
+    f32, shape = torch.float32, (M,)
+    args = (_flat("targets", targets, torch.int32, shape, dev),
+            None if old_logp is None else _flat("old_logp", old_logp, f32, shape, dev),
+            None if ref_logp is None else _flat("ref_logp", ref_logp, f32, shape, dev),
+            _flat("advantage", advantage, f32, shape, dev), _flat("weight", weight, f32, shape, dev))
+    stats, logp = weight.new_empty(4), weight.new_empty(M)
+    scratch = weight.new_empty(_words("gpt_op_policy_loss_scratch", M))
+    _check(lib().gpt_op_policy_loss(
+        logits.data_ptr(), code, ld, *args, M, V, clip_low, clip_high, kl_coef, stats.data_ptr(), logp.data_ptr(), d,
+        ld_d, scratch.data_ptr(), torch._C._cuda_getCurrentRawStream(dev)))
     return stats, logp, dlogits
 
 
@@ -739,25 +738,25 @@ def preference_loss(logits, targets, cu_seqlens, ref_logp=None, beta=0.1, label_
     Rows past the last sequence: logp and a new dlogits hold zeros there; a
     given dlogits keeps what it held (in place: the logits), or zeros with
     clear_past=True."""
+    if stream is not None:
+        return _on(stream, preference_loss, logits, targets, cu_seqlens, ref_logp, beta, label_smoothing, grad,
+                   dlogits, clear_past=clear_past)
     import torch
     if clear_past is None:
         clear_past = dlogits is None
-    dev = _current(torch, "logits", logits)
-    with _Run(torch, stream, dev) as run:
-        M, V, code, ld, dlogits, d, ld_d = _loss_rows(torch, logits, grad, dlogits, dev)
-        n, f32, i32 = cu_seqlens.numel() - 1, torch.float32, torch.int32
-        if n < 2 or n % 2 or n > _INT_MAX:
-            _refuse("cu_seqlens", cu_seqlens, "[2 * pairs + 1]")
-        y, cu = _flat("targets", targets, i32, (M,), dev), _flat("cu_seqlens", cu_seqlens, i32, (n + 1,), dev)
-        ref = None if ref_logp is None else _flat("ref_logp", ref_logp, f32, (n,), dev)
-        loss, margin = logits.new_empty((), dtype=f32), logits.new_empty(n // 2, dtype=f32)
-        seq_logp, logp = logits.new_empty(n, dtype=f32), logits.new_empty(M, dtype=f32)
-        scratch = targets.new_empty(_words("gpt_op_preference_loss_scratch", M, n // 2))
-        _check(lib().gpt_op_preference_loss_ex(
-            logits.data_ptr(), code, ld, y, cu, n // 2, ref, M, V, beta, label_smoothing, loss.data_ptr(),
-            margin.data_ptr(), seq_logp.data_ptr(), logp.data_ptr(), d, ld_d, bool(clear_past), scratch.data_ptr(),
-            run.raw))
-        run.share(logits, targets, cu_seqlens, ref_logp, loss, margin, seq_logp, logp, dlogits)
+    M, V, code, ld, dlogits, d, ld_d, dev = _loss_rows(torch, logits, grad, dlogits)
+    n, f32, i32 = cu_seqlens.numel() - 1, torch.float32, torch.int32
+    if n < 2 or n % 2 or n > _INT_MAX:
+        _refuse("cu_seqlens", cu_seqlens, "[2 * pairs + 1]")
+    y, cu = _flat("targets", targets, i32, (M,), dev), _flat("cu_seqlens", cu_seqlens, i32, (n + 1,), dev)
+    ref = None if ref_logp is None else _flat("ref_logp", ref_logp, f32, (n,), dev)
+    loss, margin = logits.new_empty((), dtype=f32), logits.new_empty(n // 2, dtype=f32)
+    seq_logp, logp = logits.new_empty(n, dtype=f32), logits.new_empty(M, dtype=f32)
+    scratch = targets.new_empty(_words("gpt_op_preference_loss_scratch", M, n // 2))
+    _check(lib().gpt_op_preference_loss_ex(
+        logits.data_ptr(), code, ld, y, cu, n // 2, ref, M, V, beta, label_smoothing, loss.data_ptr(),
+        margin.data_ptr(), seq_logp.data_ptr(), logp.data_ptr(), d, ld_d, bool(clear_past), scratch.data_ptr(),
+        torch._C._cuda_getCurrentRawStream(dev)))
     return loss, margin, seq_logp, logp, dlogits
 
 

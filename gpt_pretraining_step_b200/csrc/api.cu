@@ -1800,9 +1800,9 @@ int gpt_op_attention_plan(const int32_t* cu_seqlens, int n_seq, int n_tokens, in
   return GPT_OK;
 }
 
-int gpt_op_attention_packed_fwd(const gpt_heads* q, const gpt_heads* k, const gpt_heads* v, const gpt_heads* o,
-                                float* lse, int n_tokens, int H, int Hkv, float scale, const void* plan,
-                                void* stream) {
+int gpt_op_attention_packed_fwd_ex(const gpt_heads* q, const gpt_heads* k, const gpt_heads* v, const gpt_heads* o,
+                                   float* lse, int n_tokens, int H, int Hkv, float scale, const void* plan,
+                                   int clear_past, void* stream) {
   int rc = packed_shape(n_tokens, H, Hkv, scale, plan);
   if (rc || n_tokens == 0) return rc;
   if (!lse) return fail(GPT_EINVAL, "null pointer: lse");
@@ -1813,18 +1813,24 @@ int gpt_op_attention_packed_fwd(const gpt_heads* q, const gpt_heads* k, const gp
   int* err = nullptr;
   if ((rc = op_err(&err))) return rc;
   GPT_CK(launch_attn_packed_fwd(tq, tk, tv, to, lse, H, Hkv, n_tokens, scale > 0.f ? scale : 1.f / sqrtf(128.f), plan,
-                                static_cast<cudaStream_t>(stream), err, g_op_wait_cycles.load()));
+                                clear_past, static_cast<cudaStream_t>(stream), err, g_op_wait_cycles.load()));
   return GPT_OK;
+}
+
+int gpt_op_attention_packed_fwd(const gpt_heads* q, const gpt_heads* k, const gpt_heads* v, const gpt_heads* o,
+                                float* lse, int n_tokens, int H, int Hkv, float scale, const void* plan,
+                                void* stream) {
+  return gpt_op_attention_packed_fwd_ex(q, k, v, o, lse, n_tokens, H, Hkv, scale, plan, 0, stream);
 }
 
 size_t gpt_op_attention_packed_bwd_scratch(int n_tokens, int H) {
   return n_tokens < 0 || H < 1 ? 0 : attention_packed_bwd_scratch(n_tokens, H);
 }
 
-int gpt_op_attention_packed_bwd(const gpt_heads* q, const gpt_heads* k, const gpt_heads* v, const gpt_heads* o,
-                                const float* lse, const gpt_heads* dout, const gpt_heads* dq, const gpt_heads* dk,
-                                const gpt_heads* dv, int n_tokens, int H, int Hkv, float scale, const void* plan,
-                                void* scratch, void* stream) {
+int gpt_op_attention_packed_bwd_ex(const gpt_heads* q, const gpt_heads* k, const gpt_heads* v, const gpt_heads* o,
+                                   const float* lse, const gpt_heads* dout, const gpt_heads* dq, const gpt_heads* dk,
+                                   const gpt_heads* dv, int n_tokens, int H, int Hkv, float scale, const void* plan,
+                                   int clear_past, void* scratch, void* stream) {
   int rc = packed_shape(n_tokens, H, Hkv, scale, plan);
   if (rc || n_tokens == 0) return rc;
   if (!scratch || !aligned_scratch(scratch)) return fail(GPT_EINVAL, "scratch must be 256-byte aligned");
@@ -1839,9 +1845,17 @@ int gpt_op_attention_packed_bwd(const gpt_heads* q, const gpt_heads* k, const gp
   int* err = nullptr;
   if ((rc = op_err(&err))) return rc;
   GPT_CK(launch_attn_packed_bwd(tq, tk, tv, tdo, lse, tdq, tdk, tdv, H, Hkv, n_tokens,
-                                scale > 0.f ? scale : 1.f / sqrtf(128.f), plan, scratch,
+                                scale > 0.f ? scale : 1.f / sqrtf(128.f), plan, scratch, clear_past,
                                 static_cast<cudaStream_t>(stream), err, g_op_wait_cycles.load()));
   return GPT_OK;
+}
+
+int gpt_op_attention_packed_bwd(const gpt_heads* q, const gpt_heads* k, const gpt_heads* v, const gpt_heads* o,
+                                const float* lse, const gpt_heads* dout, const gpt_heads* dq, const gpt_heads* dk,
+                                const gpt_heads* dv, int n_tokens, int H, int Hkv, float scale, const void* plan,
+                                void* scratch, void* stream) {
+  return gpt_op_attention_packed_bwd_ex(q, k, v, o, lse, dout, dq, dk, dv, n_tokens, H, Hkv, scale, plan, 0, scratch,
+                                        stream);
 }
 
 // Rows of logits and gradient common to both losses.

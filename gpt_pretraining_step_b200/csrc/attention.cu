@@ -41,8 +41,8 @@ constexpr int HD = 128;
 // items sorted by their number of blocks, longest first.  (Tiles that start
 // with their sequence would need 6% fewer blocks on documents of 128 to 2048
 // tokens, 14% on chats of 24 to 1024, but more tiles.)
-// Positions past the last sequence are neither read nor written.  Their
-// memory may hold NaN, which a zero probability would not remove: the forward
+// Positions past the last sequence are not read, and written only as zeros and on
+// request (kClear*).  Their memory may hold NaN, which a zero probability would not remove: the forward
 // clears those rows of a V tile in shared memory (K and Q there reach only
 // scores that are masked and rows that are not stored), the backward copies
 // the tensor maps to device memory with their token extent cut to the
@@ -64,7 +64,10 @@ struct PackedArgs {
   const CUtensorMap* maps;  // backward: q, k, v, dO with the extent patched in
   long long o_tok, o_head;    // forward: strides of o in elements; backward: of dk
   long long dv_tok, dv_head;  // backward: strides of dv
+  int clear;                  // forward: kClear* bits
 };
+// Outputs whose rows past the last sequence become zeros instead of staying as they are.
+enum { kClearO = 1, kClearLse = 2, kClearDq = 1, kClearDk = 2, kClearDv = 4 };
 enum { kCtlSched = 0, kCtlEntries = 1, kCtlValid = 2 };
 // Words of a plan: positions that the sequences hold, forward and backward
 // entries, T.
@@ -786,12 +789,21 @@ __global__ void __launch_bounds__(192, 2)
       int2 nx = make_int2(0, 0);
       bool asked = false;
       uint32_t answers = 0;
-      auto fetch = [&](int idx) {   // false: a block without work (tiles past the sequences)
-        if (idx >= n_items) return false;
-        const int h = idx / entries;
-        nx = __ldg(pk.fwd + (idx - h * entries));
-        if (!fwd_entry_ok(nx, Tv, err)) return false;
-        nx_h = h;
+      // a block for every tile: those past the sequences, after the others, to clear
+      const int tiles = (Tv + 127) / 128, past = plan.fits && pk.clear ? (T + 127) / 128 - tiles : 0;
+      auto fetch = [&](int idx) {   // false: a block without work
+        if (idx < n_items) {
+          const int h = idx / entries;
+          nx = __ldg(pk.fwd + (idx - h * entries));
+          if (!fwd_entry_ok(nx, Tv, err)) return false;
+          nx_h = h;
+          return true;
+        }
+        idx -= n_items;
+        if (idx >= past * H) return false;
+        nx_h = idx / past;
+        nx.x = tiles + idx - nx_h * past;
+        nx.y = nx.x + 1;   // no key block
         return true;
       };
       auto take = [&] {   // false: the wait expired
@@ -824,6 +836,11 @@ __global__ void __launch_bounds__(192, 2)
         next_block_ask(answer, answered);
         asked = true;
         const int hk = h / (H / Hkv);
+        if (j0 > qt) {   // rows to clear: no loads
+          mbar_arrive(q_full);
+          if (!take()) { ok = false; break; }
+          continue;
+        }
         mbar_arrive_expect_tx(q_full, TF_BUF);
         tma_load_3d(sQ, &tq, q_full, 0, qt * 128, h);
         tma_load_3d(sQ + TF_TILE, &tq, q_full, 64, qt * 128, h);
@@ -879,6 +896,7 @@ __global__ void __launch_bounds__(192, 2)
       const int h = __shfl_sync(0xffffffffu, f[0], 0), qt = __shfl_sync(0xffffffffu, f[1], 0);
       const int j0 = __shfl_sync(0xffffffffu, f[2], 0);
       if (h < 0) break;
+      if (j0 > qt) umma_commit_by(leader, q_empty);
       for (int j = j0; j <= qt; ++j, ++g) {
         // S over P of the block before, once its product has read it
         if (!wait1(k_full, g & 1) || (g > 0 && !wait1(pv_done, (g - 1) & 1))) { ok = false; break; }
@@ -931,6 +949,13 @@ __global__ void __launch_bounds__(192, 2)
       if (lane == 0) mbar_arrive(q_empty);   // this warp has the fields
       if (h < 0) break;
       const int w0 = qt * 128 + warp * 32, q = w0 + lane;   // the warp's first row, this thread's
+      if (pk.clear && w0 + 32 > Tv) {   // rows past the sequences, those of a tile before it is computed
+        if (pk.clear & kClearO)
+          for (int row = max(w0, Tv) + (lane >> 4); row < min(w0 + 32, T); row += 2)
+            *reinterpret_cast<uint4*>(o + row * pk.o_tok + h * pk.o_head + (lane & 15) * 8) = make_uint4(0, 0, 0, 0);
+        if ((pk.clear & kClearLse) && q >= Tv && q < T) lse[static_cast<long long>(h) * T + q] = 0.f;
+      }
+      if (j0 > qt) continue;
       const int lo = q < Tv ? __ldg(pk.lo + q) : 0;         // first key of the row
       const int lo_max = __reduce_max_sync(0xffffffffu, lo);
       float m_ref = -INFINITY, l = 0.f;   // reference max (log2 units) and row sum relative to it
@@ -2174,7 +2199,7 @@ __device__ __forceinline__ void packed_setup(const SetupMaps& in, CUtensorMap* o
     if (!plan.fits && err) atomicOr(err, ERRF_SHAPE);
     ctl[kCtlSched] = 0;
     ctl[kCtlEntries] = plan.bwd;
-    ctl[kCtlValid] = valid;
+    ctl[kCtlValid] = plan.fits ? valid : -1;   // -1: no output is touched
   }
   for (int i = 0; i < 4; ++i)
     reinterpret_cast<uint32_t*>(&stage[i])[lane] = reinterpret_cast<const uint32_t*>(&in.m[i])[lane];
@@ -2242,7 +2267,8 @@ __global__ void __launch_bounds__(608, 1)
     chain_wait();
     if (threadIdx.x == 0) {
       if (err) atomicOr(err, ERRF_SHAPE);
-      ctl[kCtlSched] = ctl[kCtlEntries] = ctl[kCtlValid] = 0;   // no backward either
+      ctl[kCtlSched] = ctl[kCtlEntries] = 0;   // no backward either
+      ctl[kCtlValid] = -1;
     }
     return;
   }
@@ -2512,14 +2538,28 @@ __global__ void __launch_bounds__(608, 1)
   }
 }
 
-// dq in bf16 from the fp32 sums, rows that hold sequences.  A warp takes
-// kRowsPerWarp of them, whose loads are issued together.
+// dq in bf16 from the fp32 sums, rows that hold sequences; zeros in the rows past
+// them of the gradients that `clear` names (kClear*).  A warp takes
+// kRowsPerWarp rows, whose loads are issued together.
 constexpr int kRowsPerWarp = 4;
 __global__ void __launch_bounds__(256)
     attention_packed_dq_kernel(const float* __restrict__ acc, bf16* __restrict__ dq, long long dq_tok,
-                               long long dq_head, const int* ctl, int H, int T) {
+                               long long dq_head, bf16* __restrict__ dk, long long dk_tok, long long dk_head,
+                               bf16* __restrict__ dv, long long dv_tok, long long dv_head, const int* ctl, int H,
+                               int Hkv, int T, int clear) {
   chain_wait();
   const int rows = ctl[kCtlValid] * H, w = (blockIdx.x * 8 + warp_id()) * kRowsPerWarp;
+  if (rows < 0) return;
+  if (clear && w + kRowsPerWarp > rows) {
+    for (int x = max(w, rows); x < min(w + kRowsPerWarp, T * H); ++x) {
+      const int t = x / H, h = x - t * H;
+      const uint2 zero = make_uint2(0u, 0u);
+      if (clear & kClearDq) *reinterpret_cast<uint2*>(dq + t * dq_tok + h * dq_head + lane_id() * 4) = zero;
+      if (h >= Hkv) continue;
+      if (clear & kClearDk) *reinterpret_cast<uint2*>(dk + t * dk_tok + h * dk_head + lane_id() * 4) = zero;
+      if (clear & kClearDv) *reinterpret_cast<uint2*>(dv + t * dv_tok + h * dv_head + lane_id() * 4) = zero;
+    }
+  }
   float4 v[kRowsPerWarp];
 #pragma unroll
   for (int i = 0; i < kRowsPerWarp; ++i) {
@@ -2665,7 +2705,7 @@ void launch_attention_plan(const int* cu, int n_seq, int T, int window, void* pl
 
 cudaError_t launch_attn_packed_fwd(const PackedTensor& q, const PackedTensor& k, const PackedTensor& v,
                                    const PackedTensor& o, float* lse, int H, int Hkv, int T, float scale,
-                                   const void* plan, cudaStream_t s, int* err, long long wait_cycles) {
+                                   const void* plan, int clear, cudaStream_t s, int* err, long long wait_cycles) {
   const bool fine = wait_limit_or_default(wait_cycles) < kShortWaitCycles;
   auto kern = fine ? attn_packed_fwd_kernel<true> : attn_packed_fwd_kernel<false>;
   static std::atomic<unsigned long long> configured[2] = {};
@@ -2681,6 +2721,7 @@ cudaError_t launch_attn_packed_fwd(const PackedTensor& q, const PackedTensor& k,
   pa.fwd = P.fwd;
   pa.o_tok = o.tok;
   pa.o_head = o.head;
+  pa.clear = clear;
   const int items = (T + 127) / 128 * H;   // a block each; most are taken over before they start
   return launch_chained(kern, items, 192, PF_SMEM, s, mq, mk, mv, static_cast<bf16*>(const_cast<void*>(o.ptr)), lse, H,
                         Hkv, T, scale * 1.4426950408889634f, err, wait_cycles, pa);
@@ -2689,7 +2730,8 @@ cudaError_t launch_attn_packed_fwd(const PackedTensor& q, const PackedTensor& k,
 cudaError_t launch_attn_packed_bwd(const PackedTensor& q, const PackedTensor& k, const PackedTensor& v,
                                    const PackedTensor& dout, const float* lse, const PackedTensor& dq,
                                    const PackedTensor& dk, const PackedTensor& dv, int H, int Hkv, int T, float scale,
-                                   const void* plan, void* scratch, cudaStream_t s, int* err, long long wait_cycles) {
+                                   const void* plan, void* scratch, int clear, cudaStream_t s, int* err,
+                                   long long wait_cycles) {
   const bool fine = wait_limit_or_default(wait_cycles) < kShortWaitCycles;
   auto kern = fine ? attn_bwd_tc_kernel<true, true> : attn_bwd_tc_kernel<false, true>;
   auto dot = fine ? attention_packed_dot_kernel<true> : attention_packed_dot_kernel<false>;
@@ -2739,7 +2781,9 @@ cudaError_t launch_attn_packed_bwd(const PackedTensor& q, const PackedTensor& k,
                      Hkv, Hkv, T, 1 << 30, scale, 0, ctl + kCtlSched, err, wait_cycles, nullptr, nullptr, nullptr, pa);
   if (e != cudaSuccess) return e;
   return launch_chained(attention_packed_dq_kernel, row_blocks, 256, 0, s, acc,
-                        static_cast<bf16*>(const_cast<void*>(dq.ptr)), dq.tok, dq.head, ctl, H, T);
+                        static_cast<bf16*>(const_cast<void*>(dq.ptr)), dq.tok, dq.head,
+                        static_cast<bf16*>(const_cast<void*>(dk.ptr)), dk.tok, dk.head,
+                        static_cast<bf16*>(const_cast<void*>(dv.ptr)), dv.tok, dv.head, ctl, H, Hkv, T, clear);
 }
 
 }  // namespace gpt

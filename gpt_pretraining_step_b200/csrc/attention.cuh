@@ -55,14 +55,16 @@ size_t attention_plan_bytes(int T);
 void launch_attention_plan(const int* cu, int n_seq, int T, int window, void* plan, int* err, cudaStream_t s);
 
 // Packed attention over the T positions of a plan.  T * H fits in an int.
+// clear: outputs whose rows past the last sequence become zeros, bits as in the C ABI.
 // cudaErrorInvalidValue: a tensor whose base or strides TMA cannot take.
 cudaError_t launch_attn_packed_fwd(const PackedTensor& q, const PackedTensor& k, const PackedTensor& v,
                                    const PackedTensor& o, float* lse, int H, int Hkv, int T, float scale,
-                                   const void* plan, cudaStream_t s, int* err, long long wait_cycles);
+                                   const void* plan, int clear, cudaStream_t s, int* err, long long wait_cycles);
 size_t attention_packed_bwd_scratch(int T, int H);
 cudaError_t launch_attn_packed_bwd(const PackedTensor& q, const PackedTensor& k, const PackedTensor& v,
                                    const PackedTensor& dout, const float* lse, const PackedTensor& dq,
                                    const PackedTensor& dk, const PackedTensor& dv, int H, int Hkv, int T, float scale,
-                                   const void* plan, void* scratch, cudaStream_t s, int* err, long long wait_cycles);
+                                   const void* plan, void* scratch, int clear, cudaStream_t s, int* err,
+                                   long long wait_cycles);
 
 }  // namespace gpt

@@ -460,8 +460,8 @@ typedef struct gpt_heads {
  * planned into the same buffer, also by replaying a captured graph.
  *   cu_seqlens  device int32 [n_seq + 1], n_seq up to 2^30; it has to start at 0, not decrease
  *               and end within n_tokens: otherwise the plan holds no
- *               sequence, so the calls that use it write nothing, and
- *               gpt_op_check reports GPT_ERANGE
+ *               sequence, so the calls that use it write nothing (but zeros
+ *               that they are asked for), and gpt_op_check reports GPT_ERANGE
  *   plan        device buffer of gpt_op_attention_plan_bytes(n_tokens) bytes,
  *               256-byte aligned */
 size_t gpt_op_attention_plan_bytes(int n_tokens);
@@ -470,8 +470,10 @@ int gpt_op_attention_plan(const int32_t* cu_seqlens, int n_seq, int n_tokens, in
 /* Attention over the packed sequences of plan, forward: per query head h
  * (kv head h / (H / Hkv)) o_t = sum_j softmax_j(scale q_t . k_j) v_j over the
  * keys that t sees, and lse fp32 [H, n_tokens], the natural log of the
- * softmax denominator.  Rows past the last sequence are neither read nor
- * written.  o must not overlap k or v.  Within a 128-position tile a NaN or
+ * softmax denominator.  Rows past the last sequence are not read, and keep what
+ * they held in the outputs, here and in the backward: a product over all
+ * n_tokens rows has to leave them out.  The _ex calls take in clear_past a sum of
+ * GPT_CLEAR_* bits, the outputs that get zeros there.  o must not overlap k or v.  Within a 128-position tile a NaN or
  * infinity in an input of one sequence may reach the others of the tile, here
  * and in the backward.
  *   scale    > 0, or 0 for 1 / sqrt(128)
@@ -480,6 +482,10 @@ int gpt_op_attention_plan(const int32_t* cu_seqlens, int n_seq, int n_tokens, in
 int gpt_op_attention_packed_fwd(const gpt_heads* q, const gpt_heads* k, const gpt_heads* v, const gpt_heads* o,
                                 float* lse, int n_tokens, int H, int Hkv, float scale, const void* plan,
                                 void* stream);
+enum { GPT_CLEAR_O = 1, GPT_CLEAR_LSE = 2, GPT_CLEAR_DQ = 1, GPT_CLEAR_DK = 2, GPT_CLEAR_DV = 4 };
+int gpt_op_attention_packed_fwd_ex(const gpt_heads* q, const gpt_heads* k, const gpt_heads* v, const gpt_heads* o,
+                                   float* lse, int n_tokens, int H, int Hkv, float scale, const void* plan,
+                                   int clear_past, void* stream);
 
 /* Its backward: gradients of q, k and v (bf16; dk and dv summed over the
  * query heads of a kv head) from dout, with lse of the forward.  Sums
@@ -496,6 +502,10 @@ int gpt_op_attention_packed_bwd(const gpt_heads* q, const gpt_heads* k, const gp
                                 const float* lse, const gpt_heads* dout, const gpt_heads* dq, const gpt_heads* dk,
                                 const gpt_heads* dv, int n_tokens, int H, int Hkv, float scale, const void* plan,
                                 void* scratch, void* stream);
+int gpt_op_attention_packed_bwd_ex(const gpt_heads* q, const gpt_heads* k, const gpt_heads* v, const gpt_heads* o,
+                                   const float* lse, const gpt_heads* dout, const gpt_heads* dq, const gpt_heads* dk,
+                                   const gpt_heads* dv, int n_tokens, int H, int Hkv, float scale, const void* plan,
+                                   int clear_past, void* scratch, void* stream);
 
 /* Element types of logits. */
 enum { GPT_DTYPE_BF16 = 0, GPT_DTYPE_FP32 = 1 };

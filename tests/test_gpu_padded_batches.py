@@ -109,3 +109,123 @@ def test_preference_bad_offsets_clear_nothing(torch):
     with pytest.raises(gpt.GptError) as e:
         gpt.op_check()
     assert e.value.code == gpt.GPT_ERANGE and (d == 7.0).all()
+
+
+def attention_batch(torch, lens, pad, H, Hkv, fill, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    total = sum(lens)
+    x = torch.randn((total + pad, 2 * H + 2 * Hkv, 128), generator=g, device="cuda").bfloat16()
+    x[total:] = fill
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    return (*x.split([H, Hkv, Hkv, H], 1), torch.tensor(cu, dtype=torch.int32, device="cuda"), total)
+
+
+@pytest.mark.parametrize("lens,pad", [([100, 60], 1), ([100, 28], 128), ([100, 27], 700), ([1], 3000), ([], 150),
+                                      ([0, 0], 10), ([300, 84], 0), ([256], 40), ([40] * 60, 2700)])
+@pytest.mark.parametrize("H,Hkv", [(3, 1), (4, 4)])
+def test_attention(torch, lens, pad, H, Hkv):
+    import gpt_pretraining_step_b200 as g
+    q, k, v, do, cu, total = attention_batch(torch, lens, pad, H, Hkv, float("nan"))
+    n = total + pad
+    plan = g.attention_plan(cu, n)
+
+    def marked(*shape, dtype=torch.bfloat16):
+        return torch.full(shape, 7.0, dtype=dtype, device="cuda")
+
+    def forward(**kw):
+        return g.attention_packed_fwd(q, k, v, plan, **kw)
+
+    # given: rows past the sequences stay
+    o, lse = forward(o=marked(n, H, 128), lse=marked(H, n, dtype=torch.float32))
+    assert (o[total:] == 7.0).all() and (lse[:, total:] == 7.0).all()
+    grads = g.attention_packed_bwd(q, k, v, o, lse, do, plan, dq=marked(n, H, 128), dk=marked(n, Hkv, 128),
+                                   dv=marked(n, Hkv, 128))
+    assert all((t[total:] == 7.0).all() for t in grads)
+    # new: zeros there, the others' rows the same
+    for shape, dt in (((n, H, 128), torch.bfloat16), ((H, n), torch.float32), ((n, Hkv, 128), torch.bfloat16)):
+        dirty(torch, *shape, dtype=dt)
+        dirty(torch, *shape, dtype=dt)
+    o2, lse2 = forward()
+    new = g.attention_packed_bwd(q, k, v, o2, lse2, do, plan)
+    assert (o2[total:] == 0).all() and (lse2[:, total:] == 0).all()
+    assert torch.equal(o2[:total], o[:total]) and torch.equal(lse2[:, :total], lse[:, :total])
+    assert all((t[total:] == 0).all() for t in new)
+    assert torch.equal(new[1][:total], grads[1][:total]) and torch.equal(new[2][:total], grads[2][:total])
+    # one given, the others new
+    o3, lse3 = forward(o=marked(n, H, 128))
+    assert (o3[total:] == 7.0).all() and (lse3[:, total:] == 0).all()
+    o4, lse4 = forward(lse=marked(H, n, dtype=torch.float32))
+    assert (o4[total:] == 0).all() and (lse4[:, total:] == 7.0).all()
+    for i, name in enumerate(("dq", "dk", "dv")):
+        mixed = g.attention_packed_bwd(q, k, v, o, lse, do, plan, **{name: marked(n, Hkv if i else H, 128)})
+        for j, t in enumerate(mixed):
+            assert (t[total:] == (7.0 if i == j else 0.0)).all(), (name, j)
+    # given ones, cleared on request; in slices of a wider buffer, whose other columns stay
+    wide = marked(n, 2 * H + 2 * Hkv + 1, 128)
+    parts = wide.split([H, H, Hkv, Hkv, 1], 1)
+    o5, lse5 = forward(o=parts[0], lse=marked(H, n, dtype=torch.float32), clear_past=True)
+    g.attention_packed_bwd(q, k, v, o, lse, do, plan, dq=parts[1], dk=parts[2], dv=parts[3], clear_past=True)
+    assert (wide[total:, :-1] == 0).all() and (wide[:, -1] == 7.0).all() and (lse5[:, total:] == 0).all()
+    assert torch.equal(o5[:total], o[:total]) and torch.equal(parts[3][:total], grads[2][:total])
+    g.op_check()
+
+
+def test_attention_replayed_with_other_lengths(torch):
+    import gpt_pretraining_step_b200 as g
+    q, k, v, do, cu, _ = attention_batch(torch, [100, 200], 400, 2, 1, 1.0)
+    n = 700
+    plan = g.attention_plan(cu, n)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan.update(cu)
+        o, lse = g.attention_packed_fwd(q, k, v, plan)
+        grads = g.attention_packed_bwd(q, k, v, o, lse, do, plan)
+    for edges in ([0, 100, 300], [0, 1, 700], [0, 0, 0], [0, 5, 129], [0, 300, 640]):
+        cu.copy_(torch.tensor(edges, dtype=torch.int32))
+        for t in (o, lse, *grads):
+            t.fill_(float("nan"))
+        graph.replay()
+        g.op_check()
+        at = edges[-1]
+        for t in (o[at:], lse[:, at:], *(t[at:] for t in grads)):
+            assert (t == 0).all(), edges
+        assert o[:at].isfinite().all() and lse[:, :at].isfinite().all() and all(t[:at].isfinite().all() for t in grads)
+
+
+def test_a_whole_step_of_a_padded_batch(torch):
+    """Packed attention, projections and the preference loss in new buffers:
+    weight gradients of a padded batch, whose pad rows hold anything, are those of
+    the batch without padding."""
+    import gpt_pretraining_step_b200 as gpt
+    g = torch.Generator(device="cuda").manual_seed(1)
+    d, V, lens, pad = 256, 500, [30, 50, 7, 60], 200
+    total = sum(lens)
+    w = [(torch.randn(s, generator=g, device="cuda") * s[0] ** -0.5).bfloat16() for s in ((d, 512), (256, d), (d, V))]
+    cu = torch.tensor([0, 30, 80, 87, 147], dtype=torch.int32, device="cuda")
+    x = torch.randn((total + pad, d), generator=g, device="cuda").bfloat16()
+    y = torch.randint(0, V, (total + pad,), generator=g, device="cuda").to(torch.int32)
+
+    def step(x, y):
+        n = x.shape[0]
+        plan = gpt.attention_plan(cu, n)
+        q, k, v = (x @ w[0]).view(n, 4, 128).split([2, 1, 1], 1)
+        o, lse = gpt.attention_packed_fwd(q, k, v, plan)
+        h = o.view(n, 256) @ w[1]
+        dl = gpt.preference_loss(h @ w[2], y, cu)[4]
+        dh = dl @ w[2].t()
+        dqkv = torch.empty((n, 4, 128), dtype=torch.bfloat16, device="cuda")
+        new = gpt.attention_packed_bwd(q, k, v, o, lse, (dh @ w[1].t()).view(n, 2, 128), plan)
+        torch.cat(new, 1, out=dqkv)
+        return [x.t().float() @ dqkv.view(n, 512).float(), o.view(n, 256).t().float() @ dh.float(),
+                h.t().float() @ dl.float()]
+
+    for t in (x[:total], x):       # leave NaN where the new tensors will be
+        for width in (256, 512, d, V):
+            dirty(torch, t.shape[0], width, dtype=torch.bfloat16)
+    padded, whole = step(x, y), step(x[:total], y[:total])
+    gpt.op_check()
+    for a, b in zip(padded, whole):
+        # products in bf16 of other sizes may add up in another order: three roundings of 2^-8 in a row, of the largest
+        assert (a - b).abs().max() <= 3 * 2.0 ** -8 * b.abs().max()
