@@ -168,8 +168,7 @@ __device__ __forceinline__ void tensormap_acquire(const CUtensorMap* m) {
 //               work on one tile while the other tile's softmax runs.
 //   warps 4..7  softmax of tile A, warps 8..11 of tile B, one query row (TMEM
 //               lane) per thread: the block max from a first pass over the S
-//               row, exp2 into bf16 P (three of every eight exponentials by a
-//               polynomial on the FMA pipe), the row sum; after the last
+//               row, exp2 into bf16 P, the row sum; after the last
 //               block, O / l and the log-sum-exp.
 // The reference max of a row only moves when the block max exceeds it by
 // more than 8 (log2 units), so P stays below 2^8; when it moves, the warp
@@ -177,8 +176,9 @@ __device__ __forceinline__ void tensormap_acquire(const CUtensorMap* m) {
 // S of this block was issued after it).
 
 // Exponentials per group of 8 scores evaluated on the MUFU unit (the rest by
-// the polynomial on the FMA pipe): forward, alternating between two values
-// over consecutive groups; backward, one value.  Even numbers (pairs).
+// the polynomial on the FMA pipe; all on MUFU is fastest) in the kernels over
+// whole rows: forward, alternating between two values over consecutive groups;
+// backward, one value.  Even numbers (pairs).
 #ifndef GPT_FWD_MUFU_EVEN
 #define GPT_FWD_MUFU_EVEN 8
 #endif
@@ -1026,24 +1026,12 @@ __global__ void __launch_bounds__(192, 2)
         auto probabilities = [&](const uint32_t (&x)[32], int c) {
           uint32_t pk[16];
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            float p[8];
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              float x0, x1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(x[k + e]), __uint_as_float(x[k + e + 1])), sl2, nb2), x0, x1);
-              if (e < ((k & 8) ? GPT_FWD_MUFU_ODD : GPT_FWD_MUFU_EVEN)) {
-                p[e] = ex2_approx(x0);
-                p[e + 1] = ex2_approx(x1);
-              } else {
-                f2_unpack(f2_exp2_poly(f2_pack(fmaxf(x0, -126.f), fmaxf(x1, -126.f))), p[e], p[e + 1]);
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              rs2 = f2_add(rs2, f2_pack(p[e], p[e + 1]));
-              pk[(k + e) >> 1] = pack_bf16x2(p[e], p[e + 1]);
-            }
+          for (int k = 0; k < 32; k += 2) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), sl2, nb2), x0, x1);
+            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            rs2 = f2_add(rs2, f2_pack(p0, p1));
+            pk[k >> 1] = pack_bf16x2(p0, p1);
           }
           tmem_store16(t_s + 16 * c, pk);
         };
@@ -1737,7 +1725,7 @@ __global__ void __launch_bounds__(512, 1)
                 const float4 lb = *reinterpret_cast<const float4*>(nls + c * 32 + kq + 4);
                 const float nl[8] = {la.x, la.y, la.z, la.w, lb.x, lb.y, lb.z, lb.w};   // -lse * log2(e)
                 // P = 2^(S * scale * log2(e) - lse * log2(e)): GPT_BWD_MUFU of every
-                // eight on the MUFU unit, the rest by the polynomial on the FMA pipe
+                // eight (packed: all) on the MUFU unit, the rest by the polynomial on the FMA pipe
                 float p[8];
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
@@ -1745,7 +1733,7 @@ __global__ void __launch_bounds__(512, 1)
                   f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[kq + e]), __uint_as_float(sr[kq + e + 1])), sl2,
                                    f2_pack(nl[e], nl[e + 1])),
                             x0, x1);
-                  if (e < GPT_BWD_MUFU) {
+                  if (kPacked || e < GPT_BWD_MUFU) {
                     p[e] = ex2_approx(x0);
                     p[e + 1] = ex2_approx(x1);
                   } else {

@@ -323,18 +323,6 @@ __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t adesc, uint64
       : "memory");
 }
 
-// Same with the A operand in TMEM (M rows in lanes, K along the columns, two
-// bf16 values per 32-bit column, the lower half first).
-__device__ __forceinline__ void umma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                                uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // Same with fp32 operands read as tf32.
 __device__ __forceinline__ void umma_tf32(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                           uint32_t idesc, uint32_t accumulate) {
@@ -383,6 +371,8 @@ __device__ __forceinline__ void umma_f16_by(bool leader, uint32_t d_tmem, uint64
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader ? 1u : 0u)
       : "memory");
 }
+// the A operand in TMEM (M rows in lanes, K along the columns, two bf16 values
+// per 32-bit column, the lower half first)
 __device__ __forceinline__ void umma_f16_tmem_a_by(bool leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
                                                    uint32_t idesc, uint32_t accumulate) {
   asm volatile(
