@@ -54,6 +54,11 @@ constexpr int HD = 128;
 // against 64 bits on sequences of 2 to 300 tokens, scores of the usual size and
 // eight times as large: dq and dk 0.0023 to 0.0025, dv 0.0015 to 0.0023, o 0.0018
 // to 0.0021, of which 0.0017 is the rounding of the result.
+// A [tokens, heads, 128] bf16 tensor, strides in elements.
+struct HeadRows {
+  const bf16* ptr;
+  long long tok, head;
+};
 struct PackedArgs {
   const int* meta;          // forward: the plan's kMeta* words
   const int* lo;            // [T]
@@ -65,10 +70,20 @@ struct PackedArgs {
   long long o_tok, o_head;    // forward: strides of o in elements; backward: of dk
   long long dv_tok, dv_head;  // backward: strides of dv
   int clear;                  // forward: kClear* bits
+  HeadRows q, k, v;           // forward: for rows to repair
+  int* bad;                   // backward: ctl[kCtlBad]
 };
+// A tile's products run over keys (or queries) that a row does not see, too, with
+// probability 0, which does not remove a NaN or an infinity there.  Such a value
+// makes every output that it reaches non-finite, so the kernels look at their
+// outputs, and rows that are not finite although all that they see is, are
+// computed again from that alone, by a warp each (repair_*).  Looking costs the
+// forward nothing measurable, the backward 3 to 5 us.
+
 // Outputs whose rows past the last sequence become zeros instead of staying as they are.
 enum { kClearO = 1, kClearLse = 2, kClearDq = 1, kClearDk = 2, kClearDv = 4 };
-enum { kCtlSched = 0, kCtlEntries = 1, kCtlValid = 2 };
+// kCtlBad: some row of a gradient is not finite
+enum { kCtlSched = 0, kCtlEntries = 1, kCtlValid = 2, kCtlBad = 3 };
 // Words of a plan: positions that the sequences hold, forward and backward
 // entries, T.
 enum { kMetaTotal = 0, kMetaFwd = 1, kMetaBwd = 2, kMetaT = 3, kMetaMagic = 4, kPlanMeta = 64 };
@@ -270,19 +285,26 @@ __device__ __forceinline__ void causal_mask_row(uint32_t (&sr)[128], int lane) {
 // dst + row * pitch (elements), row = 0 .. n_rows - 1 of the warp's 32, through
 // 64 kCols bytes of shared memory: kCols / 8 lanes write one row's values
 // together.  (With a lane for each row a store touched 32 cache lines.)
-template <int kCols>
-__device__ __forceinline__ void store_rows(uint32_t taddr, float f, uint8_t* stage, bf16* dst, long long pitch,
-                                           int n_rows) {
+// kCheck: returns 0 if this lane's values are finite, else NaN.
+template <int kCols, bool kCheck = false>
+__device__ __forceinline__ float store_rows(uint32_t taddr, float f, uint8_t* stage, bf16* dst, long long pitch,
+                                            int n_rows) {
   constexpr int kUnits = kCols / 8, kBytes = kCols * 2;   // of 16 bytes in a row; of a row
   const int lane = lane_id();
   // unit u of row r lies at u ^ swap(r): eight lanes, or rows, meet 32 different banks
   auto swap = [](int r) { return kUnits == 8 ? r & 7 : (r >> 1) & 3; };
   uint32_t w[kCols / 2];
+  uint64_t z = f2_pack(0.f, 0.f);
 #pragma unroll
   for (int c = 0; c < kCols; c += 32) {
     uint32_t x[32];
     tmem_load32_async(taddr + c, x);
     tmem_wait_ld();
+    if constexpr (kCheck) {
+#pragma unroll
+      for (int k = 0; k < 32; k += 2)
+        z = f2_fma(f2_pack(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f2_pack(0.f, 0.f), z);
+    }
 #pragma unroll
     for (int k = 0; k < 16; ++k)
       w[c / 2 + k] = pack_bf16x2(__uint_as_float(x[2 * k]) * f, __uint_as_float(x[2 * k + 1]) * f);
@@ -300,6 +322,51 @@ __device__ __forceinline__ void store_rows(uint32_t taddr, float f, uint8_t* sta
     const uint4 v = *reinterpret_cast<const uint4*>(stage + row * kBytes + ((u ^ swap(row)) << 4));
     if (row < n_rows) *reinterpret_cast<uint4*>(dst + row * pitch + u * 8) = v;
   }
+  float z0, z1;
+  f2_unpack(z, z0, z1);
+  return z0 + z1;
+}
+
+// ---- rows computed again (a warp for a row, 4 of the 128 dims a lane)
+
+__device__ __forceinline__ float4 row4(const HeadRows& r, int t, int h) {
+  const uint2 u = *reinterpret_cast<const uint2*>(r.ptr + t * r.tok + h * r.head + lane_id() * 4);
+  return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+}
+__device__ __forceinline__ bool finite4(float4 x) { return x.x * 0.f + x.y * 0.f + x.z * 0.f + x.w * 0.f == 0.f; }
+__device__ __forceinline__ bool finite_row(float4 x) { return __all_sync(0xffffffffu, finite4(x)); }
+__device__ __forceinline__ float dot_row(float4 a, float4 b) {
+  return warp_sum(a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w);
+}
+__device__ __forceinline__ void add_row(float4& a, float f, float4 x) {
+  a.x = fmaf(f, x.x, a.x);
+  a.y = fmaf(f, x.y, a.y);
+  a.z = fmaf(f, x.z, a.z);
+  a.w = fmaf(f, x.w, a.w);
+}
+__device__ __forceinline__ void put_row(bf16* row, float f, float4 x) {
+  *reinterpret_cast<uint2*>(row + lane_id() * 4) = make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
+}
+
+// o of query t of head h, which sees the keys lo .. t of those that its tile
+// visits, first .. last: left as it is if they explain it.  The nearest keys
+// first, so that a sequence that has diverged is left after a few.
+__device__ __noinline__ void repair_o_row(const PackedArgs& a, bf16* o, int h, int hk, int t, int lo, int first,
+                                          int last, float lse2, float scale_log2) {
+  const float4 q = row4(a.q, t, h);
+  if (!finite_row(q)) return;
+  lo = min(max(lo, first), t);   // whatever the plan holds
+  bool clean = true;
+  for (int j = first; j <= last && clean; ++j)
+    if (j < lo || j > t) clean = finite_row(row4(a.v, j, hk));
+  if (clean) return;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j = t; j >= lo; --j) {
+    const float4 k = row4(a.k, j, hk), v = row4(a.v, j, hk);
+    if (!finite_row(k) || !finite_row(v)) return;
+    add_row(acc, ex2_approx(fmaf(dot_row(q, k), scale_log2, -lse2)), v);
+  }
+  put_row(o + t * a.o_tok + h * a.o_head, 1.f, acc);
 }
 
 template <bool kFine>
@@ -718,7 +785,7 @@ __global__ void __launch_bounds__(192, 2)
     attn_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                            const __grid_constant__ CUtensorMap tv, bf16* __restrict__ o, float* __restrict__ lse,
                            int H, int Hkv, int T, float scale_log2, int* err, long long wait_cycles,
-                           const PackedArgs pk) {
+                           const __grid_constant__ PackedArgs pk) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // the 128-byte-swizzled tiles need a 1024-byte-aligned base, which the
   // dynamic shared memory window provides; refuse to run otherwise
@@ -1080,9 +1147,20 @@ __global__ void __launch_bounds__(192, 2)
         tc_fence_after();
         const float inv = 1.f / l;
         bf16* orow = o + w0 * pk.o_tok + h * pk.o_head;
+        float z = 0.f;
 #pragma unroll 1
         for (int c = 0; c < 128; c += 32)
-          store_rows<32>(t_o + c, inv, sOut + warp * 2048, orow + c, pk.o_tok, Tv - w0);
+          z += store_rows<32, true>(t_o + c, inv, sOut + warp * 2048, orow + c, pk.o_tok, Tv - w0);
+        uint32_t bad = __ballot_sync(0xffffffffu, q < Tv && !(z == 0.f));
+        if (bad) {
+          const float lse2 = m_ref + log2f(l);
+          __syncwarp();   // the rows are stored
+          for (; bad; bad &= bad - 1) {
+            const int r = __ffs(bad) - 1;
+            repair_o_row(pk, o, h, h / (H / Hkv), w0 + r, __shfl_sync(0xffffffffu, lo, r), j0 * 128,
+                         min(qt * 128 + 127, Tv - 1), __shfl_sync(0xffffffffu, lse2, r), scale_log2);
+          }
+        }
         if (q < Tv) lse[static_cast<long long>(h) * T + q] = (m_ref + log2f(l)) * 0.69314718055994531f;
         // O has been read: the next item's first P V may overwrite it
         tc_fence_before();
@@ -2000,8 +2078,11 @@ __global__ void __launch_bounds__(512, 1)
             const long long pitch = kPacked ? (c ? pa.o_tok : pa.dv_tok) : 128;
             bf16* row = (c ? dk : dv) + (kPacked ? w0 * pitch + kb.hk * (c ? pa.o_head : pa.dv_head)
                                                  : (static_cast<long long>(bkv) * T + w0) * 128);
-            store_rows<64>(tmem + lane_base + 256 + 128 * c + 64 * half, c ? scale : 1.f,
-                           sdSt + half * TF_TILE + quarter * 4096, row + 64 * half, pitch, rows);
+            const float z = store_rows<64, kPacked>(tmem + lane_base + 256 + 128 * c + 64 * half, c ? scale : 1.f,
+                                                    sdSt + half * TF_TILE + quarter * 4096, row + 64 * half, pitch,
+                                                    rows);
+            if constexpr (kPacked)
+              if (lane < rows && !(z == 0.f)) *pa.bad = 1;
           }
           __syncwarp();   // read before the next item's dS goes there
           // dK and dV have been read: the next key block's first products may
@@ -2186,6 +2267,7 @@ __device__ __forceinline__ void packed_setup(const SetupMaps& in, CUtensorMap* o
   if (lane == 0) {
     if (!plan.fits && err) atomicOr(err, ERRF_SHAPE);
     ctl[kCtlSched] = 0;
+    ctl[kCtlBad] = 0;
     ctl[kCtlEntries] = plan.bwd;
     ctl[kCtlValid] = plan.fits ? valid : -1;   // -1: no output is touched
   }
@@ -2255,7 +2337,7 @@ __global__ void __launch_bounds__(608, 1)
     chain_wait();
     if (threadIdx.x == 0) {
       if (err) atomicOr(err, ERRF_SHAPE);
-      ctl[kCtlSched] = ctl[kCtlEntries] = 0;   // no backward either
+      ctl[kCtlSched] = ctl[kCtlEntries] = ctl[kCtlBad] = 0;   // no backward either
       ctl[kCtlValid] = -1;
     }
     return;
@@ -2451,7 +2533,7 @@ __global__ void __launch_bounds__(608, 1)
       const int lo_max = __reduce_max_sync(0xffffffffu, lo);
       const float m = row ? lse[static_cast<long long>(h) * T + q] * -1.4426950408889634f : -INFINITY;
       const uint64_t m2 = f2_pack(m, m);
-      // zeros for the sums of dq, each warp every eighth row
+      // zeros for the sums of dq, each warp every sixteenth row
       for (int x = qt * 128 + warp; x < min(qt * 128 + 128, Tv); x += 16)
         reinterpret_cast<float4*>(dq + (static_cast<long long>(h) * T + x) * HD)[lane] =
             make_float4(0.f, 0.f, 0.f, 0.f);
@@ -2526,26 +2608,93 @@ __global__ void __launch_bounds__(608, 1)
   }
 }
 
+// What the last kernels of a backward need beside dq's sums.
+struct FinishArgs {
+  HeadRows q, k, v, dout, dq, dk, dv;   // the last three are written
+  const int* ctl;
+  const int* lo;
+  const int* hi;
+  const float* nl;   // [H][T rounded up to 128]
+  const float* nd;
+  int H, Hkv, T, clear;
+  float scale;
+};
+__device__ __forceinline__ bf16* row_of(const HeadRows& r, int t, int h) {
+  return const_cast<bf16*>(r.ptr) + t * r.tok + h * r.head;
+}
+
+// dq of query t of head h, which sees the keys lo[t] .. t of those that its tile
+// visits.
+__device__ __noinline__ void repair_dq_row(const FinishArgs& a, int valid, int t, int h) {
+  if (finite_row(row4(a.dq, t, h))) return;
+  const float4 q = row4(a.q, t, h), d = row4(a.dout, t, h);
+  const long long at = static_cast<long long>(h) * ((a.T + 127) / 128 * 128) + t;
+  const float nl = a.nl[at], nd = a.nd[at];
+  if (!finite_row(q) || !finite_row(d) || !isfinite(nl) || !isfinite(nd)) return;
+  const int hk = h / (a.H / a.Hkv), last = min(t | 127, valid - 1);
+  const int first = min(max(a.lo[t & ~127], 0), t) & ~127, lo = min(max(a.lo[t], first), t);
+  bool clean = true;
+  for (int j = first; j <= last && clean; ++j)
+    if (j < lo || j > t) clean = finite_row(row4(a.k, j, hk)) && finite_row(row4(a.v, j, hk));
+  if (clean) return;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j = t; j >= lo; --j) {
+    const float4 k = row4(a.k, j, hk), v = row4(a.v, j, hk);
+    if (!finite_row(k) || !finite_row(v)) return;
+    const float p = ex2_approx(fmaf(dot_row(q, k), a.scale * 1.4426950408889634f, nl));
+    add_row(acc, p * (dot_row(d, v) + nd), k);
+  }
+  put_row(row_of(a.dq, t, h), a.scale, acc);
+}
+
+// dk and dv of key j of kv head hk, which the queries j .. hi[j] see of those
+// that its block visits.
+__device__ __noinline__ void repair_dkv_row(const FinishArgs& a, int valid, int j, int hk) {
+  if (finite_row(row4(a.dk, j, hk)) && finite_row(row4(a.dv, j, hk))) return;
+  const float4 k = row4(a.k, j, hk), v = row4(a.v, j, hk);
+  if (!finite_row(k) || !finite_row(v)) return;
+  const int G = a.H / a.Hkv, hi = min(max(a.hi[j], j), valid - 1);
+  const int last = min(a.hi[min(j | 127, valid - 1)] | 127, valid - 1);
+  const long long pitch = (a.T + 127) / 128 * 128;
+  bool clean = true;
+  for (int t = j & ~127; t <= last && clean; ++t)
+    for (int h = hk * G; h < (hk + 1) * G && clean && (t < j || t > hi); ++h)
+      clean = finite_row(row4(a.q, t, h)) && finite_row(row4(a.dout, t, h)) && isfinite(a.nl[h * pitch + t]) &&
+              isfinite(a.nd[h * pitch + t]);
+  if (clean) return;
+  float4 sk = make_float4(0.f, 0.f, 0.f, 0.f), sv = sk;
+  for (int t = j; t <= hi; ++t)
+    for (int h = hk * G; h < (hk + 1) * G; ++h) {
+      const float4 q = row4(a.q, t, h), d = row4(a.dout, t, h);
+      const float nl = a.nl[h * pitch + t], nd = a.nd[h * pitch + t];
+      if (!finite_row(q) || !finite_row(d) || !isfinite(nl) || !isfinite(nd)) return;
+      const float p = ex2_approx(fmaf(dot_row(q, k), a.scale * 1.4426950408889634f, nl));
+      add_row(sk, p * (dot_row(d, v) + nd), q);
+      add_row(sv, p, d);
+    }
+  put_row(row_of(a.dk, j, hk), a.scale, sk);
+  put_row(row_of(a.dv, j, hk), 1.f, sv);
+}
+
 // dq in bf16 from the fp32 sums, rows that hold sequences; zeros in the rows past
 // them of the gradients that `clear` names (kClear*).  A warp takes
 // kRowsPerWarp rows, whose loads are issued together.
 constexpr int kRowsPerWarp = 4;
 __global__ void __launch_bounds__(256)
     attention_packed_dq_kernel(const float* __restrict__ acc, bf16* __restrict__ dq, long long dq_tok,
-                               long long dq_head, bf16* __restrict__ dk, long long dk_tok, long long dk_head,
-                               bf16* __restrict__ dv, long long dv_tok, long long dv_head, const int* ctl, int H,
-                               int Hkv, int T, int clear) {
+                               long long dq_head, int* ctl, const __grid_constant__ FinishArgs a) {
+  chain_go();
   chain_wait();
-  const int rows = ctl[kCtlValid] * H, w = (blockIdx.x * 8 + warp_id()) * kRowsPerWarp;
+  const int H = a.H, T = a.T, rows = ctl[kCtlValid] * H, w = (blockIdx.x * 8 + warp_id()) * kRowsPerWarp;
   if (rows < 0) return;
-  if (clear && w + kRowsPerWarp > rows) {
+  if (a.clear && w + kRowsPerWarp > rows) {
     for (int x = max(w, rows); x < min(w + kRowsPerWarp, T * H); ++x) {
       const int t = x / H, h = x - t * H;
-      const uint2 zero = make_uint2(0u, 0u);
-      if (clear & kClearDq) *reinterpret_cast<uint2*>(dq + t * dq_tok + h * dq_head + lane_id() * 4) = zero;
-      if (h >= Hkv) continue;
-      if (clear & kClearDk) *reinterpret_cast<uint2*>(dk + t * dk_tok + h * dk_head + lane_id() * 4) = zero;
-      if (clear & kClearDv) *reinterpret_cast<uint2*>(dv + t * dv_tok + h * dv_head + lane_id() * 4) = zero;
+      const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (a.clear & kClearDq) put_row(dq + t * dq_tok + h * dq_head, 1.f, zero);
+      if (h >= a.Hkv) continue;
+      if (a.clear & kClearDk) put_row(row_of(a.dk, t, h), 1.f, zero);
+      if (a.clear & kClearDv) put_row(row_of(a.dv, t, h), 1.f, zero);
     }
   }
   float4 v[kRowsPerWarp];
@@ -2559,10 +2708,22 @@ __global__ void __launch_bounds__(256)
   for (int i = 0; i < kRowsPerWarp; ++i) {
     if (w >= rows - i) break;
     const int t = (w + i) / H, h = w + i - t * H;
-    uint2 u;
-    u.x = pack_bf16x2(v[i].x, v[i].y);
-    u.y = pack_bf16x2(v[i].z, v[i].w);
-    *reinterpret_cast<uint2*>(dq + t * dq_tok + h * dq_head + lane_id() * 4) = u;
+    put_row(dq + t * dq_tok + h * dq_head, 1.f, v[i]);
+    if (!finite4(v[i])) ctl[kCtlBad] = 1;
+  }
+}
+
+// The end of a backward whose gradients are not all finite: the rows that need
+// not be so.  Returns at once otherwise (in the kernel before, the same work
+// doubled its time by its registers).
+__global__ void __launch_bounds__(256) attention_packed_repair_kernel(const __grid_constant__ FinishArgs a) {
+  chain_wait();
+  if (!a.ctl[kCtlBad]) return;
+  const int valid = a.ctl[kCtlValid], rows = valid * a.H, step = gridDim.x * 8;
+  for (long long x = blockIdx.x * 8 + warp_id(); x < rows; x += step) {
+    const int t = static_cast<int>(x) / a.H, h = static_cast<int>(x) - t * a.H;
+    repair_dq_row(a, valid, t, h);
+    if (h < a.Hkv) repair_dkv_row(a, valid, t, h);
   }
 }
 
@@ -2673,6 +2834,8 @@ constexpr size_t kPackedHead = 256 + 4 * sizeof(CUtensorMap);
 // Strides of an extent-1 dimension are never used: any legal value stands in.
 long long stride_or(long long extent, long long stride) { return extent > 1 ? stride : HD; }
 
+HeadRows head_rows(const PackedTensor& t) { return HeadRows{static_cast<const bf16*>(t.ptr), t.tok, t.head}; }
+
 bool map_heads(CUtensorMap* m, const PackedTensor& t, long long tokens, long long heads) {
   return make_map(m, t.ptr, 2, HD, tokens, heads, stride_or(tokens, t.tok), stride_or(heads, t.head), 64, 128);
 }
@@ -2710,6 +2873,9 @@ cudaError_t launch_attn_packed_fwd(const PackedTensor& q, const PackedTensor& k,
   pa.o_tok = o.tok;
   pa.o_head = o.head;
   pa.clear = clear;
+  pa.q = head_rows(q);
+  pa.k = head_rows(k);
+  pa.v = head_rows(v);
   const int items = (T + 127) / 128 * H;   // a block each; most are taken over before they start
   return launch_chained(kern, items, 192, PF_SMEM, s, mq, mk, mv, static_cast<bf16*>(const_cast<void*>(o.ptr)), lse, H,
                         Hkv, T, scale * 1.4426950408889634f, err, wait_cycles, pa);
@@ -2757,6 +2923,7 @@ cudaError_t launch_attn_packed_bwd(const PackedTensor& q, const PackedTensor& k,
   pa.hi = P.hi;
   pa.bwd = P.bwd;
   pa.ctl = ctl;
+  pa.bad = ctl + kCtlBad;
   pa.maps = dmaps;
   pa.o_tok = dk.tok;
   pa.o_head = dk.head;
@@ -2768,10 +2935,28 @@ cudaError_t launch_attn_packed_bwd(const PackedTensor& q, const PackedTensor& k,
                      static_cast<bf16*>(const_cast<void*>(dk.ptr)), static_cast<bf16*>(const_cast<void*>(dv.ptr)), H,
                      Hkv, Hkv, T, 1 << 30, scale, 0, ctl + kCtlSched, err, wait_cycles, nullptr, nullptr, nullptr, pa);
   if (e != cudaSuccess) return e;
-  return launch_chained(attention_packed_dq_kernel, row_blocks, 256, 0, s, acc,
-                        static_cast<bf16*>(const_cast<void*>(dq.ptr)), dq.tok, dq.head,
-                        static_cast<bf16*>(const_cast<void*>(dk.ptr)), dk.tok, dk.head,
-                        static_cast<bf16*>(const_cast<void*>(dv.ptr)), dv.tok, dv.head, ctl, H, Hkv, T, clear);
+  FinishArgs fin = {};
+  fin.q = head_rows(q);
+  fin.k = head_rows(k);
+  fin.v = head_rows(v);
+  fin.dout = head_rows(dout);
+  fin.dq = head_rows(dq);
+  fin.dk = head_rows(dk);
+  fin.dv = head_rows(dv);
+  fin.ctl = ctl;
+  fin.lo = P.lo;
+  fin.hi = P.hi;
+  fin.nl = nl;
+  fin.nd = nd;
+  fin.H = H;
+  fin.Hkv = Hkv;
+  fin.T = T;
+  fin.clear = clear;
+  fin.scale = scale;
+  e = launch_chained(attention_packed_dq_kernel, row_blocks, 256, 0, s, acc,
+                     static_cast<bf16*>(const_cast<void*>(dq.ptr)), dq.tok, dq.head, ctl, fin);
+  if (e != cudaSuccess) return e;
+  return launch_chained(attention_packed_repair_kernel, std::min(row_blocks, 2 * device_sm_count()), 256, 0, s, fin);
 }
 
 }  // namespace gpt

@@ -473,9 +473,10 @@ int gpt_op_attention_plan(const int32_t* cu_seqlens, int n_seq, int n_tokens, in
  * softmax denominator.  Rows past the last sequence are not read, and keep what
  * they held in the outputs, here and in the backward: a product over all
  * n_tokens rows has to leave them out.  The _ex calls take in clear_past a sum of
- * GPT_CLEAR_* bits, the outputs that get zeros there.  o must not overlap k or v.  Within a 128-position tile a NaN or
- * infinity in an input of one sequence may reach the others of the tile, here
- * and in the backward.
+ * GPT_CLEAR_* bits, the outputs that get zeros there.  o must not overlap k or v.
+ * A NaN or infinity in an input reaches no row that does not see it, here and
+ * in the backward (rows that share a 128-position tile with one are computed
+ * again, slowly; with o in the place of q they stay NaN).
  *   scale    > 0, or 0 for 1 / sqrt(128)
  *   plan     made for the same n_tokens (another plan: nothing is written and
  *            gpt_op_check reports it) */
