@@ -360,11 +360,27 @@ __device__ __noinline__ void repair_o_row(const PackedArgs& a, bf16* o, int h, i
   for (int j = first; j <= last && clean; ++j)
     if (j < lo || j > t) clean = finite_row(row4(a.v, j, hk));
   if (clean) return;
+  // eight keys at a time, for their latencies
+  constexpr int kKeys = 8;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j = t; j >= lo; --j) {
-    const float4 k = row4(a.k, j, hk), v = row4(a.v, j, hk);
-    if (!finite_row(k) || !finite_row(v)) return;
-    add_row(acc, ex2_approx(fmaf(dot_row(q, k), scale_log2, -lse2)), v);
+  for (int j = t; j >= lo; j -= kKeys) {
+    float4 k[kKeys], v[kKeys];
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) {
+      k[i] = row4(a.k, max(j - i, lo), hk);
+      v[i] = row4(a.v, max(j - i, lo), hk);
+    }
+    bool finite = true;
+    float s[kKeys];
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) {
+      finite &= finite4(k[i]) && finite4(v[i]);
+      s[i] = dot_row(q, k[i]);
+    }
+    if (!__all_sync(0xffffffffu, finite)) return;
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i)
+      if (j - i >= lo) add_row(acc, ex2_approx(fmaf(s[i], scale_log2, -lse2)), v[i]);
   }
   put_row(o + t * a.o_tok + h * a.o_head, 1.f, acc);
 }
@@ -2082,7 +2098,7 @@ __global__ void __launch_bounds__(512, 1)
                                                     sdSt + half * TF_TILE + quarter * 4096, row + 64 * half, pitch,
                                                     rows);
             if constexpr (kPacked)
-              if (lane < rows && !(z == 0.f)) *pa.bad = 1;
+              if (lane < rows && !(z == 0.f) && *static_cast<volatile int*>(pa.bad) == 0) *pa.bad = 1;
           }
           __syncwarp();   // read before the next item's dS goes there
           // dK and dV have been read: the next key block's first products may
@@ -2704,13 +2720,16 @@ __global__ void __launch_bounds__(256)
     const int t = (w + i) / H, h = w + i - t * H;
     v[i] = reinterpret_cast<const float4*>(acc + static_cast<long long>(h * T + t) * HD)[lane_id()];
   }
+  bool finite = true;
 #pragma unroll
   for (int i = 0; i < kRowsPerWarp; ++i) {
     if (w >= rows - i) break;
     const int t = (w + i) / H, h = w + i - t * H;
     put_row(dq + t * dq_tok + h * dq_head, 1.f, v[i]);
-    if (!finite4(v[i])) ctl[kCtlBad] = 1;
+    finite &= finite4(v[i]);
   }
+  // the word is set once or a few times: in a batch of NaN a store from every warp took 450 us
+  if (!finite && *static_cast<volatile int*>(ctl + kCtlBad) == 0) ctl[kCtlBad] = 1;
 }
 
 // The end of a backward whose gradients are not all finite: the rows that need
