@@ -778,12 +778,12 @@ __device__ __forceinline__ float max32(const uint32_t (&x)[32], float m) {
 // taken in turn; the two hide each other's softmax and products, start and
 // end of a tile.  (Pairs of tiles that share their key blocks in one block, as
 // above, leave a fifth of the softmax time idle here: neighbours seldom see
-// equally many blocks.  16,384 tokens of chats of 24 to 1024, 10 heads over 2:
-// 79 us against 90; 32,768 of documents of 128 to 2048, 10 heads: 186 against
-// 205, 500 TFLOP/s of visible pairs, 670 of the blocks it runs.)  A tile takes
+// equally many blocks.  Kernel times, 16,384 tokens of chats of 24 to 1024, 10
+// heads over 2: 79 us against 90; 32,768 of documents of 128 to 2048, 10 heads:
+// 186 against 205, 500 TFLOP/s of visible pairs, 670 of the blocks it runs.)  A tile takes
 // about 4.4 us and 2.35 us a key block, of which S = Q K^T alone fills half
 // the shared-memory bandwidth (both operands of a 128 x 128 product): bound by
-// the chain S, softmax, P V of the two tiles, with the tensor pipe 37% busy
+// the chain S, softmax, P V of the two tiles, with the tensor pipe 36% busy
 // and 31% of the issue slots used.  Two threads a row measured the same.
 // 192 threads:
 //   warps 0..3  softmax, one query row (TMEM lane) per thread, as above; then
@@ -1247,10 +1247,12 @@ __global__ void __launch_bounds__(192, 2)
 // and -D come with Q and dO by bulk copies (from attention_packed_dot_kernel's
 // arrays of whole tiles), so that its softmax warps meet at no barrier; the
 // masks of a 32-query chunk are bits; dK and dV rows go out through the dS
-// tile.  32,768 tokens of documents, 10 heads: 350 us, 606 TFLOP/s of visible
-// pairs, 830 of the blocks it runs (466 us with staged lse and D, a form for
-// each kind of mask and a lane for each stored row); bound by the softmax
+// tile; P stays in fp32 until dS is formed.  32,768 tokens of documents, 10 heads:
+// kernel 360 us (650 TFLOP/s of visible pairs) where the power cap leaves the
+// clock alone, 390 to 410 in passes back to back; bound by the softmax
 // warps, about 1,800 cycles for P and as many for dS of the 4,400 a block takes.
+// (In one build of it all: 466 us with staged lse and D, a form for each kind of
+// mask and a lane for each stored row, against 350; P in fp32 cost 1 to 2%.)
 
 // Row r, query columns 64*half .. 64*half+63 of a [128][128] bf16 tile kept as
 // two 64-column halves of [128 rows][128 B] with the 128-byte swizzle (16-byte
@@ -2315,28 +2317,32 @@ __device__ __forceinline__ void packed_setup(const SetupMaps& in, CUtensorMap* o
 // row's tile (nl -inf: P = 0); zeros in the fp32 dq accumulator; and the
 // backward's setup.
 //
-// D could be had as dO_t . o_t from the forward's o, in 50 us instead of 155 (32,768
-// tokens of documents, 10 heads), but o is rounded to bf16, and dS = P (dP - D)
-// would carry the whole error of D in rows whose probability sits on one key,
-// where dP - D of that key is small: dq and dk were then off by 0.004 to 0.008 of
-// their norm on sequences of 2 to 40 tokens, against 0.0024 now.  So the kernel takes P and dP as the backward will, S =
-// Q K^T and dP = dO V^T into TMEM and P = exp(S - lse), and divides by sum_j P_tj,
-// which makes the row sums of dS vanish to fp32.
+// D could be had as dO_t . o_t from the forward's o, in 50 us instead of 150 to 165
+// (32,768 tokens of documents, 10 heads), but o is rounded to bf16, and dS = P (dP
+// - D) would carry the whole error of D in rows whose probability sits on one
+// key, where dP - D of that key is small: dq and dk were then off by 0.004 to
+// 0.008 of their norm on sequences of 2 to 40 tokens, against 0.0024 now.  So the
+// kernel takes P and dP as the backward will, S = Q K^T and dP = dO V^T into TMEM
+// and P = exp(S - lse), and divides by sum_j P_tj, which makes the row sums of dS
+// vanish to fp32.
 //
 // Persistent, a block an SM, items by cluster launch control as in the
 // forward.  608 threads:
 //   warps 0..15 two groups of eight, group b for every other key block, in TMEM
 //               columns 256 b (S) and 256 b + 128 (dP); two threads for a query
 //               row (TMEM lane), each 64 of the block's keys; the four sums of a
-//               row meet in shared memory.  (One thread a row and group: 184 us.)
+//               row meet in shared memory.  (One thread a row and group took
+//               a fifth longer.)
 //   warp 16     TMA: takes the items and publishes them in a shared ring; loads
 //               Q and dO, and K_j and V_j through two-slot rings
 //   warp 17     TMEM owner and MMA issuer
 //   warp 18     the backward's setup (every block writes the same words)
-// DRAM alone takes 75 us (q, k, v, dO read, the zeros written); the rest is the
-// latency of TMEM loads and barriers (tensor pipe 41% busy, issue slots 33%).  Two
-// tiles that share their key blocks load half as much, but leave no second
-// buffer of S and dP: 193 us.
+// DRAM alone takes 75 us (q, k, v, dO read, the zeros written), the products by
+// themselves 55, waiting for each tile's Q and dO 51 (3 us a tile); what overlaps
+// of these leaves the tensor pipe 41% busy and the issue slots 33%.  Second buffers
+// for Q and dO gained 3% alone and nothing in whole passes, where the clock falls
+// with the power drawn; two tiles that share their key blocks load half as
+// much, but leave no second buffer of S and dP: 193 us against 161.
 constexpr int PD_SUMS = 2 * 3 * 128 * 8;
 constexpr int PD_SMEM = 6 * TF_BUF + PD_SUMS + 4 * static_cast<int>(sizeof(CUtensorMap)) + 256;
 

@@ -31,7 +31,7 @@ using bf16 = __nv_bfloat16;
 // computes and the third writes), of 6 for longer policy rows (fewer rows then
 // compete for L2: 111 us instead of 122 for 1500 rows of 50,257 fp32 values),
 // of 2 for the sums (69 us instead of 72 for 5,100 rows of 64 KB).
-// Measured: 8192 x 32768 bf16 policy loss, 6,550 rows counted, 179 us, 5.4 TB/s;
+// Measured: 8192 x 32768 bf16 policy loss, 6,550 rows counted, kernel 179 us, 5.4 TB/s;
 // it issues 17 instructions for an element (both passes, two exponentials) and
 // the exponentials' unit is half busy, which the copies do not quite hide.
 constexpr int kVecs = 2;   // vectors of a thread in a piece

@@ -517,7 +517,8 @@ enum { GPT_DTYPE_BF16 = 0, GPT_DTYPE_FP32 = 1 };
  *   -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_coef (exp(d) - d - 1)
  * and the loss is its sum over the counted positions times weight[m].
  *   logits     [M, V] in dtype, M up to 2^30, V up to 2^24, row stride ld >= V
- *              elements; -inf allowed
+ *              elements; -inf allowed (a counted row of nothing else has no
+ *              log-probability: NaN)
  *   targets    device int32 [M]; -1: the position is not counted.  Other ids
  *              outside [0, V) are not counted either and latched as GPT_ERANGE
  *   old_logp   fp32 [M], or NULL: the present ones (r = 1, with -A as the
@@ -530,7 +531,8 @@ enum { GPT_DTYPE_BF16 = 0, GPT_DTYPE_FP32 = 1 };
  *   logp       fp32 [M]: lp, 0 where not counted
  *   dlogits    [M, V] in dtype with row stride ld_d: the gradient of the loss
  *              (rows not counted are zero, whatever their logits hold); may
- *              be logits itself (ld_d = ld); NULL: no gradient
+ *              be logits itself (ld_d = ld) and must not overlap them otherwise;
+ *              NULL: no gradient
  *   scratch    device buffer of gpt_op_policy_loss_scratch(M) bytes, 256-byte
  *              aligned, of this call alone while it runs
  * Log-probabilities, sums and scalars are held in 32 bits or more; results
