@@ -99,16 +99,20 @@ def test_rows_that_do_not_see_it(torch, lens, which, at, window, H, Hkv, value, 
 
 
 def test_a_batch_of_nan_alone(torch):
-    """Nothing to repair, and quickly seen: every row sees a NaN."""
-    import time
+    """Nothing to repair, and quickly seen: every row sees a NaN.  The rows' own
+    keys for each would be 17 million steps of a warp."""
     lens = [5000, 3000]
     *t, cu = make(torch, lens, 4, 2, 1)
     for x in t:
         x.fill_(NAN)
-    run(torch, *t, cu, -1)
-    torch.cuda.synchronize()
-    start = time.perf_counter()
     got = run(torch, *t, cu, -1)
-    torch.cuda.synchronize()
-    assert time.perf_counter() - start < 0.1
     assert all(x.isnan().all() for x in got)
+    times = []
+    for _ in range(5):
+        begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        begin.record()
+        run(torch, *t, cu, -1)
+        end.record()
+        end.synchronize()
+        times.append(begin.elapsed_time(end))
+    assert min(times) < 20, times    # ms; a batch of numbers takes 1

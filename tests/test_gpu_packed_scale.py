@@ -92,6 +92,36 @@ def test_many_tiles_of_one_sequence(torch):
         check(torch, [t[a:a + step] for t in got], [w[keep] for w in want], [e[keep] for e in errs], a)
 
 
+def test_offsets_past_32_bits(torch):
+    """More than 2^31 elements in q, o, dq and the fp32 sums: the first and the last sequences."""
+    import gpt_pretraining_step_b200 as g
+    H, length, count = 16, 500, 2121
+    n = length * count
+    assert n * H * 128 > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    q, do = (torch.empty((n, H, 128), dtype=torch.bfloat16, device="cuda").normal_(generator=gen) for _ in range(2))
+    k, v = (torch.empty((n, 1, 128), dtype=torch.bfloat16, device="cuda").normal_(generator=gen) for _ in range(2))
+    # head-major q and o, token-major do: both kinds of large strides
+    q = q.view(H, n, 128).transpose(0, 1)
+    plan = g.attention_plan(torch.arange(0, n + 1, length, dtype=torch.int32, device="cuda"), n)
+    o = torch.full((H, n, 128), math.nan, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    o, lse = g.attention_packed_fwd(q, k, v, plan, o=o)
+    got = g.attention_packed_bwd(q, k, v, o, lse, do, plan)
+    g.op_check()
+    for at in (0, 1060, 2119, 2120):
+        rows = slice(at * length, (at + 1) * length)
+        part = [t[rows] for t in (q, k, v, do)]
+        want, errs, _ = sequence(torch, *part, -1, SCALE)
+        check(torch, [t[rows] for t in got], want, errs, at)
+        again = g.attention_packed_fwd(*(t.contiguous() for t in part[:3]),
+                                       g.attention_plan(torch.tensor([0, length], dtype=torch.int32, device="cuda"),
+                                                        length))
+        # tiles cut the sequence elsewhere there: products add up in another order and P is rounded by another maximum
+        assert (again[0].float() - o[rows].float()).abs().max() <= 2.0 ** -6 * 4
+        assert (again[1] - lse[:, rows]).abs().max() <= 1e-4
+    assert all(bool(t.isfinite().all()) for t in (o, lse, *got))
+
+
 def test_two_streams(torch):
     """Forward and backward of two batches over one plan at the same time."""
     import gpt_pretraining_step_b200 as g
