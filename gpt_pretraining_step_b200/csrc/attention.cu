@@ -41,12 +41,19 @@ constexpr int HD = 128;
 // items sorted by their number of blocks, longest first.  (Tiles that start
 // with their sequence would need 6% fewer blocks on documents of 128 to 2048
 // tokens, 14% on chats of 24 to 1024, but more tiles.)
-// Positions past the last sequence are not read, and written only as zeros and on
-// request (kClear*).  Their memory may hold NaN, which a zero probability would not remove: the forward
-// clears those rows of a V tile in shared memory (K and Q there reach only
-// scores that are masked and rows that are not stored), the backward copies
-// the tensor maps to device memory with their token extent cut to the
-// sequences' end, so that TMA fills the rows of all four operands with zeros.
+// Positions past the last sequence are not read, and written only as zeros and
+// on request (kClear*).  Their memory may hold NaN, which a zero probability
+// would not remove: the forward clears those rows of a V tile in shared memory
+// (K and Q there reach only scores that are masked and rows that are not
+// stored), the backward copies the tensor maps to device memory with their
+// token extent cut to the sequences' end, so that TMA fills the rows of all four
+// operands with zeros.
+// Inside the sequences, too, a tile's products run over keys (or queries) that a
+// row does not see, with probability 0.  A NaN or an infinity there makes every
+// output that it reaches non-finite, so the kernels look at their outputs, and
+// rows that are not finite although all that they see is, are computed again
+// from that alone, by a warp each (repair_*).  Looking costs the forward nothing
+// measurable, the backward 3 to 5 us.
 // Scores, maxima, row sums, lse, D and every sum over keys or queries are fp32.
 // Rounded to bf16 are only P, as the operand of P V and P^T dO, and dS, formed
 // from P in fp32, as that of dS K and dS^T Q: the tensor cores take both operands
@@ -54,6 +61,7 @@ constexpr int HD = 128;
 // against 64 bits on sequences of 2 to 300 tokens, scores of the usual size and
 // eight times as large: dq and dk 0.0023 to 0.0025, dv 0.0015 to 0.0023, o 0.0018
 // to 0.0021, of which 0.0017 is the rounding of the result.
+
 // A [tokens, heads, 128] bf16 tensor, strides in elements.
 struct HeadRows {
   const bf16* ptr;
@@ -73,13 +81,6 @@ struct PackedArgs {
   HeadRows q, k, v;           // forward: for rows to repair
   int* bad;                   // backward: ctl[kCtlBad]
 };
-// A tile's products run over keys (or queries) that a row does not see, too, with
-// probability 0, which does not remove a NaN or an infinity there.  Such a value
-// makes every output that it reaches non-finite, so the kernels look at their
-// outputs, and rows that are not finite although all that they see is, are
-// computed again from that alone, by a warp each (repair_*).  Looking costs the
-// forward nothing measurable, the backward 3 to 5 us.
-
 // Outputs whose rows past the last sequence become zeros instead of staying as they are.
 enum { kClearO = 1, kClearLse = 2, kClearDq = 1, kClearDk = 2, kClearDv = 4 };
 // kCtlBad: some row of a gradient is not finite
@@ -299,7 +300,7 @@ __device__ __forceinline__ float store_rows(uint32_t taddr, float f, uint8_t* st
   for (int c = 0; c < kCols; c += 32) {
     uint32_t x[32];
     tmem_load32_async(taddr + c, x);
-    tmem_wait_ld();
+    tmem_landed(x);
     if constexpr (kCheck) {
 #pragma unroll
       for (int k = 0; k < 32; k += 2)
@@ -780,8 +781,8 @@ __device__ __forceinline__ float max32(const uint32_t (&x)[32], float m) {
 // above, leave a fifth of the softmax time idle here: neighbours seldom see
 // equally many blocks.  Kernel times, 16,384 tokens of chats of 24 to 1024, 10
 // heads over 2: 79 us against 90; 32,768 of documents of 128 to 2048, 10 heads:
-// 186 against 205, 500 TFLOP/s of visible pairs, 670 of the blocks it runs.)  A tile takes
-// about 4.4 us and 2.35 us a key block, of which S = Q K^T alone fills half
+// 186 against 205, 500 TFLOP/s of visible pairs, 670 of the blocks it runs.)  A
+// tile takes about 4.4 us and 2.35 us a key block, of which S = Q K^T alone fills half
 // the shared-memory bandwidth (both operands of a 128 x 128 product): bound by
 // the chain S, softmax, P V of the two tiles, with the tensor pipe 36% busy
 // and 31% of the issue slots used.  Two threads a row measured the same.

@@ -51,8 +51,8 @@ def expected(torch, q, k, v, do, lens, window):
 
 
 CASES = [([40, 50, 30], 1, 10, -1, 2, 1), ([40, 50, 30], 1, 49, -1, 2, 2), ([1, 1, 1, 1], 2, 0, -1, 1, 1),
-         ([300, 20, 200, 100], 1, 5, -1, 4, 2), ([300, 20, 200, 100], 0, 290, -1, 2, 2), ([500, 130, 7], 1, 100, 60, 3, 1),
-         ([100] * 10, 4, 50, -1, 2, 1)]
+         ([300, 20, 200, 100], 1, 5, -1, 4, 2), ([300, 20, 200, 100], 0, 290, -1, 2, 2),
+         ([500, 130, 7], 1, 100, 60, 3, 1), ([100] * 10, 4, 50, -1, 2, 1)]
 
 
 @pytest.mark.parametrize("lens,which,at,window,H,Hkv", CASES)
